@@ -25,7 +25,7 @@ HIP_FLAGS = [
     "-I", INCLUDE, "-I", CSRC,
 ]
 HIP_SOURCES = ["gemv.hip", "gemv_mfma.hip", "gemm.hip", "gemm_i8.hip", "misc.hip", "writer.hip",
-               "qmv_api.cpp"]
+               "norm.hip", "kv_cache.hip", "kv_attend.hip", "logprobs.hip", "qmv_api.cpp", "serve_api.cpp"]
 HOST_SOURCES = ["qmv_host.cpp"]  # no HIP: plain g++
 # Per-file flags.  The int8 product reads every matrix-core result with
 # vector instructions; in the accumulation-register form each result would

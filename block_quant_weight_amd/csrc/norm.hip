@@ -1,0 +1,171 @@
+// Root-mean-square norm with the residual's addition, in the forms that the
+// products take (float32, bfloat16, Q8_0 blocks of 32).
+//
+// For a row of n values: h = x + res, r = 1 / sqrt(sum h^2 / n + eps),
+// y = (h r) w; with Q8_0 output, per block of 32: d = amax / 127, q =
+// trunc(y (127 / amax) + copysign(0.5, y)), the activation quantizer's rule.
+//
+// One pass over the row: a workgroup keeps it in registers (float4 i * NT +
+// tid of the row in thread tid), so x and res are read once and every output
+// is written from the same values.  The squares are summed in 64 bits (h^2
+// is exact there), because a code lies next to a border where a last-bit
+// difference of r moves it by a whole step; r and everything after it is
+// float32, each operation rounded on its own, so codes do not depend on how
+// a row is split over threads.  A block of 32 is eight neighbouring lanes'
+// float4s: its amax is three lane exchanges.
+#include "device_common.h"
+#include "serve_kernels.h"
+
+namespace qmv {
+namespace {
+
+#pragma clang fp contract(off)
+
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp_u32(uint32_t v) {
+    return static_cast<uint32_t>(
+        __builtin_amdgcn_mov_dpp(static_cast<int>(v), CTRL, 0xF, 0xF, true));
+}
+
+__device__ __forceinline__ double wave_sum(double v) {
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1) v += __shfl_xor(v, m);
+    return v;
+}
+
+__device__ __forceinline__ uint32_t abs_bits(float v) {
+    return __builtin_bit_cast(uint32_t, v) & 0x7FFFFFFFu;
+}
+
+// Writes float4 `i` of row `row` of every output after the sum.
+__device__ __forceinline__ void put(const NormArgs& a, uint64_t row, uint32_t i, float4 h, float r) {
+    const float4 w = reinterpret_cast<const float4*>(a.w)[i];
+    const float hx = h.x * r, hy = h.y * r, hz = h.z * r, hw = h.w * r;
+    const float4 y = make_float4(hx * w.x, hy * w.y, hz * w.z, hw * w.w);
+    const uint64_t at = row * a.cols + 4ull * i;
+    if (a.y != nullptr) *reinterpret_cast<float4*>(a.y + at) = y;
+    if (a.y_bf16 != nullptr) {
+        typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+        const bf16x4 b = {static_cast<__bf16>(y.x), static_cast<__bf16>(y.y),
+                          static_cast<__bf16>(y.z), static_cast<__bf16>(y.w)};
+        *reinterpret_cast<bf16x4*>(a.y_bf16 + at) = b;
+    }
+    if (a.q != nullptr) {
+        // largest magnitude of the block, as bits: infinities and NaNs are
+        // the largest of all
+        uint32_t m = max(max(abs_bits(y.x), abs_bits(y.y)), max(abs_bits(y.z), abs_bits(y.w)));
+        m = max(m, dpp_u32<0xB1>(m));   // lanes 1 apart
+        m = max(m, dpp_u32<0x4E>(m));   // 2 apart
+        m = max(m, dpp_u32<0x141>(m));  // half row mirrored: the other four
+        const float amax = __builtin_bit_cast(float, m);
+        float d = 0.f;
+        uint32_t word = 0;
+        if (m >= 0x7F800000u) {
+            d = __builtin_nanf("");
+        } else if (!(amax < 1e-30f)) {
+            d = amax / 127.0f;
+            const float id = 127.0f / amax;
+            const float v[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const float t = v[c] * id;
+                const float u = truncf(t + copysignf(0.5f, v[c]));
+                const int q = static_cast<int>(fminf(fmaxf(u, -127.f), 127.f));
+                word |= (static_cast<uint32_t>(q) & 0xFFu) << (8 * c);
+            }
+        }
+        *reinterpret_cast<uint32_t*>(a.q + at) = word;
+        if ((i & 7) == 0) a.d[at >> 5] = d;
+    }
+}
+
+__device__ __forceinline__ float inv_rms(double sum, uint32_t cols, float eps) {
+    return static_cast<float>(1.0 / sqrt(sum / static_cast<double>(cols) + static_cast<double>(eps)));
+}
+
+// NT threads a row, at most V float4s in each; LOOP: any length, the row's h
+// read again for the outputs.
+template <int NT, int V, bool LOOP>
+__global__ __launch_bounds__(NT) void rms_norm_kernel(NormArgs a) {
+    __shared__ double part[2][NT / 64];
+    const uint32_t n4 = a.cols >> 2;
+    const int tid = threadIdx.x;
+    int flip = 0;
+    for (uint64_t row = blockIdx.x; row < a.rows; row += gridDim.x, flip ^= 1) {
+        const float4* xp = reinterpret_cast<const float4*>(a.x + row * a.cols);
+        const float4* rp = a.res != nullptr ? reinterpret_cast<const float4*>(a.res + row * a.cols) : nullptr;
+        float4* sp = a.sum != nullptr ? reinterpret_cast<float4*>(a.sum + row * a.cols) : nullptr;
+        float4 h[V];
+        double s = 0.0;
+        auto load = [&](uint32_t i) {
+            float4 v = xp[i];
+            if (rp != nullptr) {
+                const float4 t = rp[i];
+                v = make_float4(v.x + t.x, v.y + t.y, v.z + t.z, v.w + t.w);
+            }
+            return v;
+        };
+        auto square = [&](const float4& v) {
+            const double p = v.x, q = v.y, u = v.z, w = v.w;
+            s += (p * p + q * q) + (u * u + w * w);
+        };
+        if constexpr (LOOP) {
+            for (uint32_t i = tid; i < n4; i += NT) {
+                const float4 v = load(i);
+                square(v);
+                if (sp != nullptr) sp[i] = v;
+            }
+        } else {
+#pragma unroll
+            for (int u = 0; u < V; ++u) {
+                const uint32_t i = u * NT + tid;
+                h[u] = i < n4 ? load(i) : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+#pragma unroll
+            for (int u = 0; u < V; ++u) {
+                square(h[u]);
+                const uint32_t i = u * NT + tid;
+                if (sp != nullptr && i < n4) sp[i] = h[u];
+            }
+        }
+        s = wave_sum(s);
+        if constexpr (NT > 64) {
+            if ((tid & 63) == 0) part[flip][tid >> 6] = s;
+            __syncthreads();  // the other buffer is written before the next one
+            s = 0.0;
+#pragma unroll
+            for (int w = 0; w < NT / 64; ++w) s += part[flip][w];
+        }
+        const float r = inv_rms(s, a.cols, a.eps);
+        if constexpr (LOOP) {
+            // the sum may have replaced res or x: each thread reads back the
+            // elements it wrote itself
+            for (uint32_t i = tid; i < n4; i += NT) put(a, row, i, sp != nullptr ? sp[i] : load(i), r);
+        } else {
+#pragma unroll
+            for (int u = 0; u < V; ++u) {
+                const uint32_t i = u * NT + tid;
+                if (i < n4) put(a, row, i, h[u], r);
+            }
+        }
+    }
+}
+
+template <int NT, int V, bool LOOP>
+hipError_t go(const NormArgs& a, hipStream_t s) {
+    const uint32_t grid = a.rows < (1u << 20) ? a.rows : (1u << 20);
+    hipLaunchKernelGGL((rms_norm_kernel<NT, V, LOOP>), dim3(grid), dim3(NT), 0, s, a);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_rms_norm(const NormArgs& a, hipStream_t s) {
+    if (a.cols <= 1024) return go<64, 4, false>(a, s);
+    if (a.cols <= 4096) return go<256, 4, false>(a, s);
+    if (a.cols <= 8192) return go<512, 4, false>(a, s);
+    if (a.cols <= 16384) return go<1024, 4, false>(a, s);
+    return go<1024, 1, true>(a, s);
+}
+
+}  // namespace qmv

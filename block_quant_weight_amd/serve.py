@@ -1,0 +1,274 @@
+"""Thin Python binding of the calls of include/qmv_serve.h, the operators
+between a quantized model's products: the norm, the 8-bit key/value cache,
+attention over it, and log probabilities.  As in qmv.py, arguments are
+marshalled from PyTorch tensors and streams and all computation happens in
+the HIP library.  Tensors live on the current device."""
+from __future__ import annotations
+
+import ctypes
+
+from . import qmv as _qmv
+from .qmv import QMV_E_ARG, QmvError, _check, _stream
+
+QMV_F32 = 0
+QMV_BF16 = 1
+QMV_KV_PAGE = 64
+
+# every symbol include/qmv_serve.h declares
+EXPORTS = ("qmv_rms_norm", "qmv_kv_write", "qmv_kv_read", "qmv_kv_attend_workspace",
+           "qmv_kv_attend", "qmv_logprobs_workspace", "qmv_logprobs")
+
+
+class _Cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("pages", ctypes.c_uint32),
+                ("kv_heads", ctypes.c_uint32), ("head_dim", ctypes.c_uint32)]
+
+
+class _Seqs(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("len", ctypes.c_void_p), ("start", ctypes.c_void_p),
+                ("seqs", ctypes.c_uint32), ("table_stride", ctypes.c_uint32),
+                ("rows", ctypes.c_uint32), ("max_new", ctypes.c_uint32),
+                ("max_len", ctypes.c_uint32)]
+
+
+_lib = None
+
+
+def lib():
+    global _lib
+    if _lib is None:
+        L = _qmv.lib()
+        u32, u64, i32, f32, vp = (ctypes.c_uint32, ctypes.c_uint64, ctypes.c_int, ctypes.c_float,
+                                  ctypes.c_void_p)
+        pc, ps, pu64 = ctypes.POINTER(_Cache), ctypes.POINTER(_Seqs), ctypes.POINTER(u64)
+        sig = {
+            "qmv_rms_norm": [vp, vp, vp, f32, u32, u32, vp, vp, vp, vp, vp, vp],
+            "qmv_kv_write": [pc, ps, u32, vp, vp, vp],
+            "qmv_kv_read": [pc, ps, u32, vp, vp, vp],
+            "qmv_kv_attend_workspace": [pc, ps, u32, u32, u32, pu64],
+            "qmv_kv_attend": [pc, ps, u32, u32, f32, u32, vp, vp, vp, u64, vp],
+            "qmv_logprobs_workspace": [u32, u32, u32, pu64],
+            "qmv_logprobs": [vp, u32, u32, vp, u32, u32, vp, vp, vp, vp, vp, u64, vp],
+        }
+        for name, args in sig.items():
+            fn = getattr(L, name)
+            fn.argtypes = args
+            fn.restype = i32
+        _lib = L
+    return _lib
+
+
+def _dev(t, dtype, numel, what):
+    """Address of a contiguous tensor of the current GPU with at least numel elements."""
+    import torch
+    if not t.is_cuda:
+        raise ValueError(f"{what} must be a GPU tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{what} must be {dtype}, not {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+    if t.numel() < numel:
+        raise ValueError(f"{what} holds {t.numel()} elements, needs {numel}")
+    if t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{what} is not on the current device")
+    return t.data_ptr()
+
+
+def _dtype(t, what):
+    """QMV_F32 or QMV_BF16 of a tensor."""
+    import torch
+    if t.dtype == torch.float32:
+        return QMV_F32
+    if t.dtype == torch.bfloat16:
+        return QMV_BF16
+    raise TypeError(f"{what} must be float32 or bfloat16, not {t.dtype}")
+
+
+def workspace(nbytes, device="cuda"):
+    """A scratch tensor of nbytes for the calls that take one (never empty)."""
+    import torch
+    return torch.empty(max(int(nbytes), 16), dtype=torch.uint8, device=device)
+
+
+class KvCache:
+    """The arrays of a cache (qmv_kv_cache): k int8 [pages, kv_heads, 64,
+    head_dim], v int8 [pages, kv_heads, head_dim, 64], k_scale and v_scale
+    float32 [pages, kv_heads].  KvCache.empty allocates them."""
+
+    def __init__(self, k, v, k_scale, v_scale):
+        import torch
+        if k.dim() != 4 or k.shape[2] != QMV_KV_PAGE:
+            raise ValueError("k must be [pages, kv_heads, 64, head_dim]")
+        self.pages, self.kv_heads, _, self.head_dim = k.shape
+        if tuple(v.shape) != (self.pages, self.kv_heads, self.head_dim, QMV_KV_PAGE):
+            raise ValueError("v must be [pages, kv_heads, head_dim, 64]")
+        if tuple(k_scale.shape) != tuple(k.shape[:2]) or tuple(v_scale.shape) != tuple(k.shape[:2]):
+            raise ValueError("the scales must be [pages, kv_heads]")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        n = k.numel()
+        self.c = _Cache(_dev(k, torch.int8, n, "k"), _dev(v, torch.int8, n, "v"),
+                        _dev(k_scale, torch.float32, 0, "k_scale"),
+                        _dev(v_scale, torch.float32, 0, "v_scale"),
+                        self.pages, self.kv_heads, self.head_dim)
+        self.ref = ctypes.pointer(self.c)
+
+    @classmethod
+    def empty(cls, pages, kv_heads, head_dim, device="cuda"):
+        import torch
+        return cls(torch.empty(pages, kv_heads, QMV_KV_PAGE, head_dim, dtype=torch.int8, device=device),
+                   torch.empty(pages, kv_heads, head_dim, QMV_KV_PAGE, dtype=torch.int8, device=device),
+                   torch.empty(pages, kv_heads, dtype=torch.float32, device=device),
+                   torch.empty(pages, kv_heads, dtype=torch.float32, device=device))
+
+
+class KvSeqs:
+    """The tokens a call is about (qmv_kv_seqs): table int32 [seqs,
+    table_stride], len int32 [seqs], start int32 [seqs + 1], on the GPU; rows
+    of the call's arrays are given by each call's tensors.  max_new and
+    max_len, the largest number of rows and of tokens of one sequence, shape
+    the launch only.  One object serves all layers of a step."""
+
+    def __init__(self, table, len, start, max_new, max_len):
+        import torch
+        if table.dim() != 2:
+            raise ValueError("table must be [seqs, table_stride]")
+        self.seqs = table.shape[0]
+        self.table, self.len, self.start = table, len, start
+        self.c = _Seqs(_dev(table, torch.int32, table.numel(), "table"),
+                       _dev(len, torch.int32, self.seqs, "len"),
+                       _dev(start, torch.int32, self.seqs + 1, "start"),
+                       self.seqs, table.shape[1], 0, int(max_new), int(max_len))
+
+
+def _rows(seqs, t, heads, dim, what):
+    """A call's own copy of seqs with the rows of t [rows, heads, dim], and t's elements."""
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
+        raise ValueError(f"{what} must be [rows, {heads}, {dim}]")
+    c = _Seqs.from_buffer_copy(seqs.c)
+    c.rows = t.shape[0]
+    return ctypes.byref(c), t.numel()
+
+
+def qmv_rms_norm(x, w, eps, res=None, sum=None, y=None, q=None, d=None, stream=None):
+    """x, res, sum: float32 [rows, cols]; w: float32 [cols]; y: float32 or
+    bfloat16 [rows, cols]; q int8 [rows, cols] with d float32 [rows, cols/32].
+    Outputs that are None are not computed; sum may be res or x."""
+    import torch
+    if x.dim() != 2:
+        raise ValueError("x must be [rows, cols]")
+    rows, cols = x.shape
+    n = rows * cols
+    f32 = torch.float32
+    y32 = yb = None
+    if y is not None:
+        if _dtype(y, "y") == QMV_F32:
+            y32 = _dev(y, f32, n, "y")
+        else:
+            yb = _dev(y, torch.bfloat16, n, "y")
+    _check(lib().qmv_rms_norm(
+        _dev(x, f32, n, "x"), None if res is None else _dev(res, f32, n, "res"),
+        _dev(w, f32, cols, "w"), eps, rows, cols, None if sum is None else _dev(sum, f32, n, "sum"),
+        y32, yb, None if q is None else _dev(q, torch.int8, n, "q"),
+        None if d is None else _dev(d, f32, n // 32, "d"), _stream(stream)), "qmv_rms_norm")
+
+
+def qmv_kv_write(cache: KvCache, seqs: KvSeqs, k, v, stream=None):
+    """k, v: float32 or bfloat16 [rows, kv_heads, head_dim]: the rows of seqs into the cache."""
+    dt = _dtype(k, "k")
+    ref, n = _rows(seqs, k, cache.kv_heads, cache.head_dim, "k")
+    _check(lib().qmv_kv_write(cache.ref, ref, dt, _dev(k, k.dtype, n, "k"),
+                              _dev(v, k.dtype, n, "v"), _stream(stream)), "qmv_kv_write")
+
+
+def qmv_kv_read(cache: KvCache, seqs: KvSeqs, k=None, v=None, stream=None):
+    """k, v (either may be None): float32 or bfloat16 [rows, kv_heads,
+    head_dim], receiving the tokens of seqs."""
+    t = k if k is not None else v
+    if t is None:
+        raise QmvError(QMV_E_ARG, "qmv_kv_read")
+    dt = _dtype(t, "k or v")
+    ref, n = _rows(seqs, t, cache.kv_heads, cache.head_dim, "k or v")
+    _check(lib().qmv_kv_read(cache.ref, ref, dt, None if k is None else _dev(k, t.dtype, n, "k"),
+                             None if v is None else _dev(v, t.dtype, n, "v"), _stream(stream)),
+           "qmv_kv_read")
+
+
+def qmv_kv_attend_workspace(cache: KvCache, seqs: KvSeqs, q, window=0) -> int:
+    """Bytes of workspace that qmv_kv_attend needs for q [rows, heads, head_dim]."""
+    out = ctypes.c_uint64(0)
+    dt = _dtype(q, "q")
+    if q.dim() != 3:
+        raise ValueError("q must be [rows, heads, head_dim]")
+    ref, _ = _rows(seqs, q, q.shape[1], cache.head_dim, "q")
+    _check(lib().qmv_kv_attend_workspace(cache.ref, ref, dt, q.shape[1], window,
+                                         ctypes.byref(out)), "qmv_kv_attend_workspace")
+    return out.value
+
+
+def qmv_kv_attend(cache: KvCache, seqs: KvSeqs, q, out, scale=None, window=0, workspace=None,
+                  stream=None):
+    """q, out: float32 or bfloat16 [rows, heads, head_dim]; scale defaults to
+    head_dim ** -0.5.  workspace: a uint8 GPU tensor of at least
+    qmv_kv_attend_workspace bytes; None allocates one, for use on the current
+    stream."""
+    import torch
+    dt = _dtype(q, "q")
+    if q.dim() != 3:
+        raise ValueError("q must be [rows, heads, head_dim]")
+    heads = q.shape[1]
+    ref, n = _rows(seqs, q, heads, cache.head_dim, "q")
+    if workspace is None:
+        nbytes = qmv_kv_attend_workspace(cache, seqs, q, window)
+        if nbytes:
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+            if stream is not None and hasattr(stream, "cuda_stream"):
+                workspace.record_stream(stream)
+    pw, nw = (None, 0) if workspace is None else (_dev(workspace, torch.uint8, 0, "workspace"),
+                                                  workspace.numel())
+    _check(lib().qmv_kv_attend(cache.ref, ref, dt, heads,
+                               cache.head_dim ** -0.5 if scale is None else scale, window,
+                               _dev(q, q.dtype, n, "q"), _dev(out, q.dtype, n, "out"), pw, nw,
+                               _stream(stream)), "qmv_kv_attend")
+
+
+def qmv_logprobs_workspace(rows, vocab, top=0) -> int:
+    out = ctypes.c_uint64(0)
+    _check(lib().qmv_logprobs_workspace(rows, vocab, top, ctypes.byref(out)), "qmv_logprobs_workspace")
+    return out.value
+
+
+def qmv_logprobs(logits, ids=None, lp=None, entropy=None, top_ids=None, top_lp=None, workspace=None,
+                 stream=None):
+    """logits: float32 [rows, vocab]; ids int32 and lp float32 [rows, n];
+    entropy float32 [rows]; top_ids int32 and top_lp float32 [rows, top].
+    workspace as for qmv_kv_attend."""
+    import torch
+    if logits.dim() != 2:
+        raise ValueError("logits must be [rows, vocab]")
+    rows, vocab = logits.shape
+    n = 0
+    if ids is not None:
+        if ids.dim() != 2 or ids.shape[0] != rows:
+            raise ValueError("ids must be [rows, n]")
+        n = ids.shape[1]
+    top = 0
+    if top_ids is not None:
+        if top_ids.dim() != 2 or top_ids.shape[0] != rows:
+            raise ValueError("top_ids must be [rows, top]")
+        top = top_ids.shape[1]
+    if workspace is None:
+        workspace = torch.empty(max(qmv_logprobs_workspace(rows, vocab, top), 16), dtype=torch.uint8,
+                                device=logits.device)
+        if stream is not None and hasattr(stream, "cuda_stream"):
+            workspace.record_stream(stream)
+    f32, i32 = torch.float32, torch.int32
+    _check(lib().qmv_logprobs(
+        _dev(logits, f32, rows * vocab, "logits"), rows, vocab,
+        None if ids is None else _dev(ids, i32, rows * n, "ids"), n, top,
+        None if lp is None else _dev(lp, f32, rows * n, "lp"),
+        None if entropy is None else _dev(entropy, f32, rows, "entropy"),
+        None if top_ids is None else _dev(top_ids, i32, rows * top, "top_ids"),
+        None if top_lp is None else _dev(top_lp, f32, rows * top, "top_lp"),
+        _dev(workspace, torch.uint8, 0, "workspace"), workspace.numel(), _stream(stream)),
+        "qmv_logprobs")

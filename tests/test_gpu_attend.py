@@ -1,0 +1,327 @@
+"""qmv_kv_attend against plain attention in 64 bits over the values that the
+cache stands for; the bound is derived in serve_ref.attend_bound."""
+import numpy as np
+import pytest
+
+import serve_ref as R
+from block_quant_weight_amd import qmv as Q
+from block_quant_weight_amd import serve as S
+
+pytestmark = pytest.mark.gpu
+PAGE = 64
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    import torch
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    yield
+
+
+def make(lens, kv_heads, dim, seed, extra=2, spread=True):
+    """A numpy cache of random codes and scales, and its table."""
+    g = np.random.default_rng(seed)
+    counts = [-(-n // PAGE) for n in lens]
+    pages = sum(counts) + extra
+    c = R.Cache(pages, kv_heads, dim)
+    c.k = np.clip(np.rint(40 * g.standard_normal(c.k.shape)), -127, 127)
+    c.v = np.clip(np.rint(40 * g.standard_normal(c.v.shape)), -127, 127)
+    c.k_scale = 2.0 ** g.integers(-6, -4, size=c.k_scale.shape)
+    c.v_scale = 2.0 ** (g.integers(-9, 3, size=c.v_scale.shape) if spread else np.full(c.v_scale.shape, -5))
+    table = np.full((len(lens), max(max(counts), 1)), -1)
+    ids = g.permutation(pages)
+    at = 0
+    for i, n in enumerate(counts):
+        table[i, :n] = ids[at:at + n]
+        at += n
+    return g, c, table
+
+
+def to_gpu(c):
+    import torch
+    return S.KvCache(torch.from_numpy(c.k.astype(np.int8)).cuda(),
+                     torch.from_numpy(np.ascontiguousarray(c.v.transpose(0, 1, 3, 2)).astype(np.int8)).cuda(),
+                     torch.from_numpy(c.k_scale.astype(np.float32)).cuda(),
+                     torch.from_numpy(c.v_scale.astype(np.float32)).cuda())
+
+
+def starts(news):
+    s = [0]
+    for m in news:
+        s.append(s[-1] + m)
+    return s
+
+
+def seqs(table, lens, start, max_new=None, max_len=None):
+    import torch
+    def i32(a):
+        return torch.tensor(np.asarray(a), dtype=torch.int32, device="cuda")
+    news = [b - a for a, b in zip(start, start[1:])]
+    return S.KvSeqs(i32(table), i32(lens), i32(start), max_new=max(news) if max_new is None else max_new,
+                    max_len=max(lens) if max_len is None else max_len)
+
+
+def attend(c, s, q, dtype, scale=None, window=0, rows=None):
+    """Outputs as float32, from a workspace full of NaN."""
+    import torch
+    dt = torch.float32 if dtype == "f32" else torch.bfloat16
+    qd = torch.from_numpy(q).cuda().to(dt)
+    out = torch.full(q.shape, 5.0, dtype=dt, device="cuda")
+    n = S.qmv_kv_attend_workspace(c, s, qd, window)
+    ws = torch.full((max(n, 16),), 0xFF, dtype=torch.uint8, device="cuda")
+    S.qmv_kv_attend(c, s, qd, out, scale=scale, window=window, workspace=ws)
+    torch.cuda.synchronize()
+    return out.float().cpu().numpy()
+
+
+def queries(g, rows, heads, dim):
+    return R.bf16(g.standard_normal((rows, heads, dim)).astype(np.float32))
+
+
+def check(lens, news, heads, kv_heads, dim, dtype, seed, window=0, scale=None, spare=3, hints=None):
+    g, c, table = make(lens, kv_heads, dim, seed)
+    start = starts(news)
+    q = queries(g, start[-1] + spare, heads, dim)
+    if dtype == "f32":
+        q = (q * np.float32(1.0003)).astype(np.float32)
+    sc = dim ** -0.5 if scale is None else scale
+    s = seqs(table, lens, start, *(hints or (None, None)))
+    got = attend(to_gpu(c), s, q, dtype, scale, window)
+    ref, b = R.attend(c, table, lens, start, q, np.float32(sc), window)
+    tol = R.attend_bound(b, q, sc, max(lens), dtype)
+    if dtype == "bf16":
+        tol = tol + 2.0 ** -8 * (np.abs(ref) + tol)
+    m = start[-1]
+    err = np.abs(got[:m] - ref[:m])
+    assert np.all(err <= tol[:m]), f"worst {np.nanmax(err / np.maximum(tol[:m], 1e-300)):.3g} of the bound"
+    assert np.all(got[m:] == 5.0), "rows of no sequence were written"
+    # a row that sees nothing is exactly 0
+    assert np.all(got[:m][b["smax"][:m, :, 0] + b["vmax"][:m, :, 0] == 0] == 0)
+
+
+SHAPES = [
+    # lens, new rows, heads, kv_heads, dim: one token; lengths around pages;
+    # groups of one, odd and more than a tile's columns
+    ([1], [1], 1, 1, 64),
+    ([1, 63, 64, 65, 129], [1, 1, 1, 1, 1], 8, 2, 64),
+    ([200, 1, 70], [1, 1, 1], 5, 1, 128),
+    ([100, 300], [1, 1], 32, 8, 128),
+    ([90, 257], [1, 1], 24, 1, 128),
+    ([130, 66], [1, 1], 6, 2, 256),
+    # several rows: every row its own causal end; all of a sequence's tokens
+    ([70, 64, 5], [7, 64, 5], 4, 4, 64),
+    ([200], [33], 6, 2, 128),
+    ([150, 80], [150, 2], 12, 4, 64),
+    ([129], [129], 4, 1, 256),
+    ([300, 40], [140, 40], 8, 2, 128),
+    # sequences without rows or tokens between others
+    ([0, 50, 64, 0], [0, 1, 0, 0], 4, 2, 64),
+]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("lens,news,heads,kv_heads,dim", SHAPES)
+def test_attend(lens, news, heads, kv_heads, dim, dtype):
+    check(lens, news, heads, kv_heads, dim, dtype, seed=sum(lens) + dim)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("window", [1, 2, 63, 64, 65, 100, 5000])
+def test_window(window, dtype):
+    check([300, 70, 1], [1, 70, 1], 4, 2, 64, dtype, seed=window, window=window)
+    check([260], [200], 8, 2, 128, dtype, seed=window + 1, window=window)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_long_sequences_in_pieces(dtype):
+    """Lengths at which the pages of a sequence are shared by many workgroups."""
+    check([5000, 1200, 3], [1, 1, 1], 4, 2, 64, dtype, seed=1)
+    check([4100], [3], 8, 1, 128, dtype, seed=2)
+    check([3001], [2], 4, 2, 256, dtype, seed=3, window=2500)
+    check([2500, 600], [40, 30], 4, 2, 128, dtype, seed=4)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_more_rows_than_tokens(dtype):
+    """Positions below 0 see nothing: zeros."""
+    check([3, 0, 70], [5, 4, 80], 4, 2, 64, dtype, seed=5)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_hints_do_not_change_results(dtype):
+    for hints in ((1, 1), (0, 0), (100000, 100000), (1, 100000)):
+        check([700, 90], [40, 90], 8, 2, 64, dtype, seed=6, hints=hints)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_pages_that_are_not_there(dtype):
+    """Unknown page ids and positions past the table are left out; a row whose
+    pages are all unknown gets zeros."""
+    import torch
+    g, c, table = make([300, 200, 70], 2, 64, 7)
+    table = table[:, :4].copy()
+    table[0, 1], table[0, 3] = -5, c.pages
+    table[1, :] = -1
+    table[2, 0] = 2147483647
+    lens, start = [300, 200, 70], [0, 2, 5, 75]
+    q = queries(g, 75, 4, 64)
+    got = attend(to_gpu(c), seqs(table, lens, start), q, dtype)
+    ref, b = R.attend(c, table, lens, start, q, 0.125, 0)
+    tol = R.attend_bound(b, q, 0.125, 300, dtype)
+    if dtype == "bf16":
+        tol = tol + 2.0 ** -8 * (np.abs(ref) + tol)
+    assert np.all(np.abs(got - ref) <= tol)
+    assert np.all(got[2:5] == 0) and np.all(got[5:69] == 0) and np.any(got[69:] != 0)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("news", [[1, 1, 1], [70, 80, 65]])
+def test_nan_touches_only_what_sees_it(dtype, news):
+    """NaN scales of pages that are masked (later pages, pages outside the
+    window) leave a row as it is; where they are seen, and for a NaN or
+    infinite query, the row and head is NaN."""
+    lens = [200, 200, 200]
+    g, c, table = make(lens, 2, 64, 8, spread=False)
+    start = starts(news)
+    rows = start[-1]
+    q = queries(g, rows, 4, 64)
+    window = 30
+    clean = attend(to_gpu(c), seqs(table, lens, start), q, dtype, window=window)
+    c.k_scale[table[0, 2], 0] = np.nan          # positions 128 .. 191, heads 0 and 1
+    c.v_scale[table[1, 2], 1] = np.nan          # heads 2 and 3
+    c.k_scale[table[1, 0], :] = np.nan          # outside every row's window
+    c.v_scale[table[2, 0], :] = np.nan
+    q[start[2] - 1, 0, 5] = np.nan              # the last row of sequence 1
+    q[rows - 1, 3, 0] = np.inf
+    got = attend(to_gpu(c), seqs(table, lens, start), q, dtype, window=window)
+    nan = np.zeros((rows, 4), dtype=bool)
+    for i, page, heads in ((0, 2, (0, 1)), (1, 2, (2, 3))):
+        for t in range(news[i]):
+            pos = 200 - news[i] + t
+            if pos >= page * 64 and pos - window + 1 < page * 64 + 64:
+                nan[start[i] + t, list(heads)] = True
+    nan[start[2] - 1, 0] = True
+    nan[rows - 1, 3] = True
+    assert np.array_equal(np.isnan(got).any(-1), nan) and np.array_equal(np.isnan(got).all(-1), nan)
+    assert np.array_equal(got[~nan], clean[~nan])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("news", [1, 80])
+def test_sharp_and_flat_rows(dtype, news):
+    """A zero query weighs all alike; a huge one picks one token; V scales far
+    apart; zero pages of K and V; many tokens far below the first one."""
+    lens = [1000]
+    g, c, table = make(lens, 1, 64, 9)
+    c.v_scale[table[0, 3]] = 2.0 ** -60
+    c.v_scale[table[0, 4]] = 0
+    c.k_scale[table[0, 5]] = 0
+    c.k[table[0, 0], 0, 0] = 127
+    q = queries(g, news, 4, 64)
+    q[-1, 0] = 0
+    q[-1, 1] *= 100
+    q[-1, 2] = 0
+    q[-1, 2, 0] = 1e-30
+    q[-1, 3] = 0.5       # the first token, then nothing near it
+    start = [0, news]
+    got = attend(to_gpu(c), seqs(table, lens, start), q, dtype)
+    ref, b = R.attend(c, table, lens, start, q, 0.125, 0)
+    tol = R.attend_bound(b, q, 0.125, 1000, dtype)
+    if dtype == "bf16":
+        tol = tol + 2.0 ** -8 * (np.abs(ref) + tol)
+    assert np.all(np.abs(got - ref) <= tol), np.max(np.abs(got - ref) / tol)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("lens,news", [([3000, 100], [1, 1]), ([400, 300], [200, 300])])
+def test_out_may_be_q_and_capture(dtype, lens, news):
+    import torch
+    g, c, table = make(lens, 2, 128, 10)
+    start = starts(news)
+    q = queries(g, start[-1], 8, 128)
+    cg, s = to_gpu(c), seqs(table, lens, start)
+    want = attend(cg, s, q, dtype)
+    dt = torch.float32 if dtype == "f32" else torch.bfloat16
+    first = torch.from_numpy(q).cuda().to(dt)
+    qd = first.clone()
+    ws = S.workspace(S.qmv_kv_attend_workspace(cg, s, qd))
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=st):
+        S.qmv_kv_attend(cg, s, qd, qd, workspace=ws, stream=st)
+    for _ in range(3):
+        qd.copy_(first)
+        ws.fill_(0xFF)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert np.array_equal(qd.float().cpu().numpy(), want)
+
+
+def test_two_calls_at_once():
+    """Two streams, a workspace each, over one cache: as one after the other."""
+    import torch
+    g, c, table = make([6000, 900], 2, 128, 11)
+    cg, s = to_gpu(c), seqs(table, [6000, 900], [0, 1, 2])
+    qs = [queries(g, 2, 8, 128) for _ in range(2)]
+    want = [attend(cg, s, q, "f32") for q in qs]
+    qd = [torch.from_numpy(q).cuda() for q in qs]
+    out = [torch.empty_like(x) for x in qd]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    ws = [S.workspace(S.qmv_kv_attend_workspace(cg, s, qd[0])) for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for i in range(2):
+            S.qmv_kv_attend(cg, s, qd[i], out[i], workspace=ws[i], stream=streams[i])
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert np.array_equal(out[i].cpu().numpy(), want[i])
+
+
+def test_cache_past_four_gib():
+    """Pages whose codes lie beyond 32-bit offsets."""
+    import torch
+    heads, dim = 8, 256
+    pages = (5 << 30) // (heads * PAGE * dim)
+    c = S.KvCache.empty(pages, heads, dim)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    ids = [pages - 1, 3, pages - 2, pages // 2 + 7]
+    small = R.Cache(4, heads, dim)
+    for i, p in enumerate(ids):
+        for t in (c.k, c.v):
+            t[p] = torch.randint(-127, 128, t[p].shape, generator=g, device="cuda", dtype=torch.int32).to(torch.int8)
+        c.k_scale[p], c.v_scale[p] = 2.0 ** -7, 2.0 ** -6
+        small.k[i], small.v[i] = c.k[p].cpu().numpy(), c.v[p].cpu().numpy().transpose(0, 2, 1)
+    small.k_scale[:], small.v_scale[:] = 2.0 ** -7, 2.0 ** -6
+    lens, rng = [250], np.random.default_rng(12)
+    for dtype, new in (("f32", 1), ("bf16", 1), ("bf16", 100)):
+        q = queries(rng, new, 16, dim)
+        got = attend(c, seqs([ids], lens, [0, new]), q, dtype)
+        ref, b = R.attend(small, [[0, 1, 2, 3]], lens, [0, new], q, dim ** -0.5, 0)
+        tol = R.attend_bound(b, q, dim ** -0.5, 250, dtype)
+        if dtype == "bf16":
+            tol = tol + 2.0 ** -8 * (np.abs(ref) + tol)
+        assert np.all(np.abs(got - ref) <= tol)
+
+
+def test_refuses_what_it_cannot_take():
+    import torch
+    g, c, table = make([5000], 2, 64, 13)
+    cg, s = to_gpu(c), seqs(table, [5000], [0, 1])
+    q = torch.zeros(1, 4, 64, device="cuda")
+    with pytest.raises(Q.QmvError) as e:
+        S.qmv_kv_attend(cg, s, torch.zeros(1, 3, 64, device="cuda"), q[:, :3].contiguous())
+    assert e.value.status == Q.QMV_E_SHAPE
+    with pytest.raises(Q.QmvError) as e:
+        S.qmv_kv_attend(cg, s, q, q.clone(), workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+    assert e.value.status == Q.QMV_E_ARG
+    with pytest.raises(Q.QmvError):
+        S.qmv_kv_attend(cg, s, q, q.clone(), scale=float("nan"))
+    with pytest.raises(TypeError):
+        S.qmv_kv_attend(cg, s, q, q.bfloat16())
+    with pytest.raises(ValueError):
+        S.qmv_kv_attend(cg, s, torch.zeros(1, 4, 128, device="cuda"), q)
+    with pytest.raises(ValueError):
+        S.qmv_kv_attend(cg, s, q[0], q)

@@ -1,0 +1,130 @@
+"""CPU checks of the calls of include/qmv_serve.h: exports, and every refusal
+that is made on the host before anything is launched."""
+import ctypes
+import os
+import re
+
+import pytest
+
+from block_quant_weight_amd import qmv as Q
+from block_quant_weight_amd import serve as S
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+P = 1 << 20           # an aligned address that is never used
+OK, ARG, SHAPE = Q.QMV_OK, Q.QMV_E_ARG, Q.QMV_E_SHAPE
+
+
+def test_library_exports_every_declared_function():
+    txt = open(os.path.join(ROOT, "include", "qmv_serve.h")).read()
+    txt = re.sub(r"/\*.*?\*/", "", txt, flags=re.S)
+    declared = set(re.findall(r"\b(qmv_[a-z0-9_]+)\s*\(", txt))
+    assert declared == set(S.EXPORTS)
+    for name in declared:
+        assert hasattr(S.lib(), name), name
+
+
+def cache(**kw):
+    a = dict(k=P, v=P, k_scale=P, v_scale=P, pages=8, kv_heads=2, head_dim=64)
+    a.update(kw)
+    return ctypes.byref(S._Cache(*[a[f] for f, _ in S._Cache._fields_]))
+
+
+def seqs(**kw):
+    a = dict(table=P, len=P, start=P, seqs=2, table_stride=4, rows=3, max_new=2, max_len=200)
+    a.update(kw)
+    return ctypes.byref(S._Seqs(*[a[f] for f, _ in S._Seqs._fields_]))
+
+
+BAD_KV = [
+    (dict(k=None), {}, ARG), (dict(v=None), {}, ARG), (dict(k_scale=None), {}, ARG),
+    (dict(v_scale=None), {}, ARG), (dict(k=P + 8), {}, ARG), (dict(v=P + 4), {}, ARG),
+    (dict(k_scale=P + 4), {}, ARG), (dict(v_scale=P + 8), {}, ARG), (dict(pages=0), {}, ARG),
+    (dict(kv_heads=0), {}, ARG), (dict(head_dim=0), {}, SHAPE), (dict(head_dim=32), {}, SHAPE),
+    (dict(head_dim=96), {}, SHAPE), (dict(head_dim=512), {}, SHAPE), (dict(kv_heads=65536), {}, SHAPE),
+    (dict(pages=1 << 31), {}, SHAPE),
+    ({}, dict(table=None), ARG), ({}, dict(len=None), ARG), ({}, dict(start=None), ARG),
+    ({}, dict(table=P + 2), ARG), ({}, dict(len=P + 1), ARG), ({}, dict(start=P + 3), ARG),
+    ({}, dict(seqs=0), ARG), ({}, dict(table_stride=0), ARG), ({}, dict(rows=0), ARG),
+    ({}, dict(rows=1 << 31), SHAPE), ({}, dict(seqs=1 << 30), SHAPE),
+]
+
+
+@pytest.mark.parametrize("c,s,want", BAD_KV)
+def test_kv_refusals(c, s, want):
+    L = S.lib()
+    n = ctypes.c_uint64(7)
+    assert L.qmv_kv_write(cache(**c), seqs(**s), 0, P, P, None) == want
+    assert L.qmv_kv_read(cache(**c), seqs(**s), 0, P, P, None) == want
+    assert L.qmv_kv_attend_workspace(cache(**c), seqs(**s), 0, 4, 0, ctypes.byref(n)) == want
+    assert n.value == 0
+    assert L.qmv_kv_attend(cache(**c), seqs(**s), 0, 4, 1.0, 0, P, P, P, 1 << 40, None) == want
+
+
+def test_kv_call_refusals():
+    L = S.lib()
+    c, s = cache(), seqs()
+    n = ctypes.c_uint64(0)
+    assert L.qmv_kv_write(None, s, 0, P, P, None) == ARG
+    assert L.qmv_kv_write(c, None, 0, P, P, None) == ARG
+    assert L.qmv_kv_write(c, s, 2, P, P, None) == ARG
+    assert L.qmv_kv_write(c, s, 0, None, P, None) == ARG
+    assert L.qmv_kv_write(c, s, 0, P, None, None) == ARG
+    assert L.qmv_kv_write(c, s, 1, P + 2, P, None) == ARG
+    assert L.qmv_kv_write(c, s, 0, P, P + 4, None) == ARG
+    assert L.qmv_kv_read(c, s, 0, None, None, None) == ARG
+    assert L.qmv_kv_read(c, s, 0, P + 8, P, None) == ARG
+    assert L.qmv_kv_read(c, s, 3, P, P, None) == ARG
+    assert L.qmv_kv_attend_workspace(c, s, 0, 4, 0, None) == ARG
+    for heads in (0, 1, 3, 5, 1 << 25):
+        assert L.qmv_kv_attend_workspace(c, s, 0, heads, 0, ctypes.byref(n)) == SHAPE
+        assert L.qmv_kv_attend(c, s, 0, heads, 1.0, 0, P, P, P, 1 << 40, None) == SHAPE
+    assert L.qmv_kv_attend(c, s, 2, 4, 1.0, 0, P, P, P, 1 << 40, None) == ARG
+    for q, out, ws, scale in ((None, P, P, 1.0), (P, None, P, 1.0), (P + 2, P, P, 1.0), (P, P + 8, P, 1.0),
+                              (P, P, P + 4, 1.0), (P, P, P, float("nan")), (P, P, P, float("inf"))):
+        assert L.qmv_kv_attend(c, s, 0, 4, scale, 0, q, out, ws, 1 << 40, None) == ARG
+    # a workspace that is needed and too small, or missing
+    long = seqs(max_len=100000, table_stride=2000)
+    assert L.qmv_kv_attend_workspace(c, long, 0, 4, 0, ctypes.byref(n)) == OK and n.value > 0
+    assert L.qmv_kv_attend(c, long, 0, 4, 1.0, 0, P, P, P, n.value - 1, None) == ARG
+    assert L.qmv_kv_attend(c, long, 0, 4, 1.0, 0, P, P, None, n.value, None) == ARG
+
+
+def test_norm_refusals():
+    def call(x=P, res=P, w=P, eps=1e-5, rows=2, cols=64, sum=P, y=P, yb=None, q=None, d=None):
+        return S.lib().qmv_rms_norm(x, res, w, eps, rows, cols, sum, y, yb, q, d, None)
+    assert call(x=None) == ARG and call(w=None) == ARG and call(rows=0) == ARG
+    assert call(sum=None, y=None) == ARG
+    assert call(q=P) == ARG and call(d=P) == ARG
+    assert call(eps=-1e-9) == ARG and call(eps=float("nan")) == ARG and call(eps=float("inf")) == ARG
+    for name in ("x", "res", "w", "sum", "y", "yb"):
+        assert call(**{name: P + 4}) == ARG, name
+    assert call(q=P + 8, d=P) == ARG and call(q=P, d=P + 8) == ARG
+    for cols in (0, 1, 31, 48, (1 << 24) + 32):
+        assert call(cols=cols) == SHAPE, cols
+
+
+def test_logprobs_refusals():
+    L = S.lib()
+    n = ctypes.c_uint64(0)
+
+    def call(x=P, rows=2, vocab=1000, ids=P, n_ids=1, top=3, lp=P, h=P, ti=P, tl=P, ws=P, nb=1 << 40):
+        return L.qmv_logprobs(x, rows, vocab, ids, n_ids, top, lp, h, ti, tl, ws, nb, None)
+    assert L.qmv_logprobs_workspace(2, 1000, 3, None) == ARG
+    for rows, vocab, top, want in ((0, 10, 0, ARG), (1, 0, 0, ARG), (1, (1 << 24) + 1, 0, SHAPE),
+                                   (1, 10, 11, SHAPE), (1, 1000, 33, SHAPE), ((1 << 22) + 1, 10, 0, SHAPE)):
+        assert L.qmv_logprobs_workspace(rows, vocab, top, ctypes.byref(n)) == want
+        assert call(rows=rows, vocab=vocab, top=top) == want
+    assert L.qmv_logprobs_workspace(2, 1000, 3, ctypes.byref(n)) == OK and n.value > 0
+    assert call(x=None) == ARG
+    assert call(lp=None, h=None, ti=None, tl=None, top=0) == ARG
+    assert call(ids=None) == ARG and call(n_ids=0) == ARG
+    assert call(ti=None) == ARG and call(tl=None) == ARG and call(top=0) == ARG
+    assert call(ti=None, tl=None, top=3) == ARG
+    assert call(ws=None) == ARG and call(ws=P + 8) == ARG and call(nb=n.value - 1) == ARG
+    for name in ("x", "ids", "lp", "h", "ti", "tl"):
+        assert call(**{name: P + 2}) == ARG, name
+
+
+def test_structs_match_the_header():
+    assert ctypes.sizeof(S._Cache) == 48 and ctypes.sizeof(S._Seqs) == 48
+    assert S.QMV_KV_PAGE == 64 and (S.QMV_F32, S.QMV_BF16) == (0, 1)
