@@ -29,6 +29,7 @@
 // fourth page and keeps its own running maximum, sum and output, joined in
 // shared memory at the end.  The pieces of a sequence are joined by a second
 // kernel, in their order.
+#include <cstdlib>
 #include "kv_common.h"
 
 namespace qmv {
@@ -39,23 +40,26 @@ typedef int i32x4 __attribute__((ext_vector_type(4)));
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kPScale = 127.0f * 65536.0f;   // p = 1 as a whole number
 constexpr int kCols = 16;                      // columns of a workgroup
+constexpr uint32_t kTarget = 1024;             // workgroups that a launch aims at
 
 struct AttendArgs {
     qmv_kv_cache c;
     qmv_kv_seqs s;
     const void* q;
     void* out;
-    float* part;        // [pieces][rows * heads][D + 2]: output sum, maximum, sum
+    float* part;        // [pieces][rows * heads][D]: output sums
+    float2* stat;       // [pieces][rows * heads]: maximum, sum
     float scale_log2;   // scale * log2(e)
     uint32_t heads, group, window, pieces;
+    uint32_t per;       // pages of a piece, at least
 };
 
 // Three signed digits of each of four whole numbers |x| <= 127 * 2^16, as
-// dwords of four bytes: x = d0 + 256 d1 + 65536 d2.
-__device__ __forceinline__ void digits4(const int x[4], uint32_t d[3]) {
+// dwords of four bytes: x = d0 + 256 d1 + 65536 d2.  Given are x + 0x8080.
+__device__ __forceinline__ void digits4(const uint32_t x[4], uint32_t d[3]) {
     uint32_t u[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) u[i] = static_cast<uint32_t>(x[i] + 0x8080) ^ 0x8080u;
+    for (int i = 0; i < 4; ++i) u[i] = x[i] ^ 0x8080u;
     // bytes 0 of (u0, u1) and (u2, u3), bytes 1, bytes 2
     const uint32_t a = __builtin_amdgcn_perm(u[1], u[0], 0x05010400u);  // b0 b0' b1 b1'
     const uint32_t b = __builtin_amdgcn_perm(u[3], u[2], 0x05010400u);
@@ -66,31 +70,48 @@ __device__ __forceinline__ void digits4(const int x[4], uint32_t d[3]) {
     d[2] = __builtin_amdgcn_perm(f, e, 0x07060100u);
 }
 
+// The number that three digits' products stand for, times 2^-16: the lower
+// two are joined as whole numbers (below 2^30 in sum).
+__device__ __forceinline__ float join3(int c0, int c1, int c2) {
+    return fmaf(static_cast<float>(c1 * 256 + c0), 0x1p-16f, static_cast<float>(c2));
+}
+
 __device__ __forceinline__ float xor_lane(float v, int m) { return __shfl_xor(v, m); }
 
-// What a workgroup's columns are.
+// First position that a row at position p sees.
+__device__ __forceinline__ int32_t sees_from(uint32_t window, int32_t p) {
+    return window == 0 || window > static_cast<uint32_t>(max(p, 0)) ? 0 : p - static_cast<int32_t>(window) + 1;
+}
+
+// What a workgroup's columns are.  Columns of a sequence and key/value head
+// (rows * group, below 2^31) are numbered row first.
 struct Columns {
-    int64_t row, pos;      // this lane's query row and position (row -1: none)
+    int32_t row;                 // this lane's query row, -1: none
+    int32_t pos;                 // its position
     uint32_t head;
-    int64_t lo, hi;        // positions that any of the 16 columns sees: [lo, hi)
+    int32_t first_pos, last_pos; // smallest and largest position of the columns
+    int32_t lo, hi;              // positions that any of the columns sees: [lo, hi)
 };
-__device__ __forceinline__ Columns columns(const AttendArgs& a, const SeqRows& r, uint32_t kvh, int64_t tile,
-                                           int col) {
+template <uint32_t COLS>
+__device__ __forceinline__ Columns columns(const AttendArgs& a, const SeqRows& r, uint32_t kvh, uint32_t tile,
+                                           uint32_t col) {
     Columns o;
-    const int64_t n = r.count * a.group, c = tile * kCols + col;
-    const int64_t t0 = tile * kCols / a.group;
-    const int64_t t1 = min(tile * kCols + kCols - 1, n - 1) / a.group;
-    o.row = c < n ? r.first + c / a.group : -1;
-    o.pos = r.base + c / a.group;
-    o.head = kvh * a.group + static_cast<uint32_t>(c % a.group);
-    const int64_t first = max(r.base + t0, int64_t{0});
-    o.hi = max(r.base + t1 + 1, int64_t{0});
-    o.lo = a.window != 0 ? max(first - static_cast<int64_t>(a.window) + 1, int64_t{0}) : 0;
+    const uint32_t n = static_cast<uint32_t>(r.count) * a.group, c = tile * COLS + col;
+    const uint32_t t0 = tile * COLS / a.group;
+    const uint32_t t1 = min(tile * COLS + COLS - 1, n - 1) / a.group;
+    const uint32_t t = c / a.group;
+    o.row = c < n ? r.first + static_cast<int32_t>(t) : -1;
+    o.pos = r.base + static_cast<int32_t>(t);
+    o.head = kvh * a.group + (c - t * a.group);
+    o.first_pos = r.base + static_cast<int32_t>(t0);
+    o.last_pos = r.base + static_cast<int32_t>(t1);
+    o.hi = max(o.last_pos + 1, 0);
+    o.lo = sees_from(a.window, max(o.first_pos, 0));
     return o;
 }
 
 template <uint32_t DT, int D>
-__global__ __launch_bounds__(256) void attend_few_kernel(AttendArgs a) {
+__global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attend_few_kernel(AttendArgs a) {
     typedef typename Elem<DT>::type T;
     constexpr int KS = D / 64;     // k-steps of a score tile
     constexpr int ET = D / 16;     // tiles of output dims
@@ -101,14 +122,51 @@ __global__ __launch_bounds__(256) void attend_few_kernel(AttendArgs a) {
     const uint32_t seq = blockIdx.x / a.c.kv_heads, kvh = blockIdx.x % a.c.kv_heads;
     const uint32_t piece = blockIdx.z;
     const SeqRows r = seq_rows(a.s, seq);
-    const int64_t tiles = (r.count * a.group + kCols - 1) / kCols;
-    for (int64_t tile = blockIdx.y; tile < tiles; tile += gridDim.y) {
-        const Columns w = columns(a, r, kvh, tile, col);
+    const uint32_t all = static_cast<uint32_t>(r.count) * a.group;
+    const uint32_t tiles = (all + kCols - 1) / kCols;
+    for (uint32_t tile = blockIdx.y; tile < tiles; tile += gridDim.y) {
+        const Columns w = columns<kCols>(a, r, kvh, tile, col);
         // pages of this piece
-        const int64_t p_lo = w.lo / kPage, p_hi = (w.hi + kPage - 1) / kPage;
-        const int64_t per = (p_hi - p_lo + a.pieces - 1) / a.pieces;
-        const int64_t p0 = p_lo + piece * per, p1 = min(p0 + per, p_hi);
-        const int64_t see_lo = a.window != 0 ? max(w.pos - static_cast<int64_t>(a.window) + 1, int64_t{0}) : 0;
+        const int32_t p_lo = w.lo / kPage, p_hi = (w.hi + kPage - 1) / kPage;
+        const int32_t per = max((p_hi - p_lo + static_cast<int32_t>(a.pieces) - 1) / static_cast<int32_t>(a.pieces),
+                                static_cast<int32_t>(a.per));
+        const int64_t begin = p_lo + static_cast<int64_t>(piece) * per;
+        const int32_t p0 = static_cast<int32_t>(min(begin, static_cast<int64_t>(p_hi)));
+        const int32_t p1 = min(p_hi - p0, per) + p0;
+        const int32_t see_lo = sees_from(a.window, w.pos);
+        // pages that every column sees whole: from full_lo up to full_hi
+        const int32_t full_lo = (sees_from(a.window, w.last_pos) + kPage - 1) / kPage;
+        const int32_t full_hi = max(w.first_pos + 1, 0) / kPage;
+
+        // Lane i has the page ids and scales of the wave's next pages, 64 of
+        // them from one trip to memory.  Keys of the next page are requested
+        // as soon as this page's have been multiplied, its values while the
+        // scores are formed: a wave always has keys or values on the way.
+        i32x4 kf[4][KS];
+        int32_t ids = -1, id = -1;
+        float kss = 0.f, vss = 0.f;
+        const int krow = 16 * (col >> 2) + (col & 3);
+        auto look = [&](int32_t p) {
+            const int32_t mine = p + 4 * lane;
+            ids = mine < p1 ? page_id(a.c, a.s, seq, mine) : -1;
+            if (ids >= 0) {
+                const uint64_t at = static_cast<uint64_t>(ids) * a.c.kv_heads + kvh;
+                kss = a.c.k_scale[at];
+                vss = a.c.v_scale[at];
+            }
+        };
+        auto fetch = [&](int n) {
+            id = __builtin_amdgcn_readlane(ids, n);
+            if (id < 0) return;
+            const int8_t* kp = a.c.k + (static_cast<uint64_t>(id) * a.c.kv_heads + kvh) * (kPage * D) + krow * D + 16 * quad;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int s = 0; s < KS; ++s)
+                    kf[j][s] = *reinterpret_cast<const i32x4*>(kp + 4 * j * D + 64 * s);
+        };
+        int n = 0;                               // the page's lane
+        look(p0 + wave);
 
         // the query's digits
         uint32_t qd[KS][3][4];
@@ -126,24 +184,27 @@ __global__ __launch_bounds__(256) void attend_few_kernel(AttendArgs a) {
 #pragma unroll
                     for (int i = 0; i < 16; ++i) v[s][i] = 0.f;
                 }
+            }
+            fetch(0);
+#pragma unroll
+            for (int s = 0; s < KS; ++s)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) m = max(m, __builtin_bit_cast(uint32_t, v[s][i]) & 0x7FFFFFFFu);
-            }
             m = max(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), 16)));
             m = max(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), 32)));
             const float amax = __builtin_bit_cast(float, m);
             int e = 0;
             const bool zero = m == 0 || m >= 0x7F800000u;
             if (!zero) (void)frexpf(amax, &e);       // amax in [2^(e-1), 2^e)
-            qs = m >= 0x7F800000u ? __builtin_nanf("") : (zero ? 0.f : ldexpf(1.f, e - 22));
+            qs = m >= 0x7F800000u ? __builtin_nanf("") : (zero ? 0.f : ldexpf(1.f, e - 6));  // 2^(e-22) 2^16
 #pragma unroll
             for (int s = 0; s < KS; ++s)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    int x[4];
+                    uint32_t x[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        x[i] = zero ? 0 : static_cast<int>(rintf(ldexpf(v[s][4 * j + i], 22 - e)));
+                        x[i] = (zero ? 0 : static_cast<int>(rintf(ldexpf(v[s][4 * j + i], 22 - e)))) + 0x8080;
                     uint32_t d[3];
                     digits4(x, d);
 #pragma unroll
@@ -158,51 +219,61 @@ __global__ __launch_bounds__(256) void attend_few_kernel(AttendArgs a) {
             for (int i = 0; i < 4; ++i) o[e][i] = 0.f;
         float m_run = -__builtin_inff(), l_run = 0.f;
 
-        for (int64_t p = p0 + wave; p < p1; p += 4) {
-            const int64_t id = page_id(a.c, a.s, seq, p);
-            if (id < 0) continue;
-            const uint64_t at = static_cast<uint64_t>(id) * a.c.kv_heads + kvh;
-            const int8_t* kp = a.c.k + at * (kPage * D);
-            const int8_t* vp = a.c.v + at * (kPage * D);
-            const float ks = a.c.k_scale[at], vs = a.c.v_scale[at];
+        for (int32_t p = p0 + wave; p < p1; p += 4, n = (n + 1) & 63) {
+            const int32_t at_id = id;
+            const float kscale = read_lane(kss, n) * a.scale_log2, vscale = read_lane(vss, n);
+            if (n == 63) look(p + 4);
+            if (at_id < 0) {
+                fetch((n + 1) & 63);
+                continue;
+            }
+            const int8_t* vp = a.c.v + (static_cast<uint64_t>(at_id) * a.c.kv_heads + kvh) * (kPage * D);
+            i32x4 vf[ET];
+#pragma unroll
+            for (int e = 0; e < ET; ++e)
+                vf[e] = *reinterpret_cast<const i32x4*>(vp + (16 * e + col) * kPage + 16 * quad);
             // scores
             float sc[4][4];
+            const float qk = qs * kscale;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const int8_t* kr = kp + (16 * (col >> 2) + 4 * j + (col & 3)) * D + 16 * quad;
                 i32x4 c[3];
 #pragma unroll
                 for (int k = 0; k < 3; ++k) c[k] = i32x4{0, 0, 0, 0};
 #pragma unroll
-                for (int s = 0; s < KS; ++s) {
-                    const i32x4 kf = *reinterpret_cast<const i32x4*>(kr + 64 * s);
+                for (int s = 0; s < KS; ++s)
 #pragma unroll
                     for (int k = 0; k < 3; ++k) {
                         const i32x4 b = {static_cast<int>(qd[s][k][0]), static_cast<int>(qd[s][k][1]),
                                          static_cast<int>(qd[s][k][2]), static_cast<int>(qd[s][k][3])};
-                        c[k] = __builtin_amdgcn_mfma_i32_16x16x64_i8(kf, b, c[k], 0, 0, 0);
+                        c[k] = __builtin_amdgcn_mfma_i32_16x16x64_i8(kf[j][s], b, c[k], 0, 0, 0);
                     }
-                }
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float t = fmaf(static_cast<float>(c[2][i]), 65536.f,
-                                         fmaf(static_cast<float>(c[1][i]), 256.f, static_cast<float>(c[0][i])));
-                    sc[j][i] = (t * qs) * (ks * a.scale_log2);
-                }
+                for (int i = 0; i < 4; ++i) sc[j][i] = join3(c[0][i], c[1][i], c[2][i]) * qk;
             }
-            // what this column sees of the page: tokens [from, to)
-            const int from = static_cast<int>(min(max(see_lo - p * kPage, int64_t{0}), int64_t{kPage}));
-            const int to = w.row < 0 ? 0 : static_cast<int>(min(max(w.pos + 1 - p * kPage, int64_t{0}), int64_t{kPage}));
-            const bool any = from < to;
+            __builtin_amdgcn_sched_barrier(0);
+            fetch((n + 1) & 63);
+            __builtin_amdgcn_sched_barrier(0);
+            // what this column sees of the page: all of it in the middle of a
+            // sequence, else the tokens [from, to)
+            bool any = true;
+            if (p < full_lo || p >= full_hi) {
+                const int from = max(see_lo - p * kPage, 0);
+                const int to = w.row < 0 ? 0 : min(w.pos + 1 - p * kPage, kPage);
+                any = from < to;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int t = 16 * quad + 4 * j + i;
+                        sc[j][i] = t >= from && t < to ? sc[j][i] : -__builtin_inff();
+                    }
+            }
             float mt = -__builtin_inff();
 #pragma unroll
             for (int j = 0; j < 4; ++j)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int t = 16 * quad + 4 * j + i;
-                    sc[j][i] = t >= from && t < to ? sc[j][i] : -__builtin_inff();
-                    mt = fmaxf(mt, sc[j][i]);
-                }
+                for (int i = 0; i < 4; ++i) mt = fmaxf(mt, sc[j][i]);
             mt = fmaxf(mt, xor_lane(mt, 16));
             mt = fmaxf(mt, xor_lane(mt, 32));
             // nothing seen, or only NaN: the maximum counts as 0 (NaN scores
@@ -212,12 +283,14 @@ __global__ __launch_bounds__(256) void attend_few_kernel(AttendArgs a) {
             uint32_t pd[3][4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                int x[4];
+                uint32_t x[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float pr = exp2f(sc[j][i] - ref);
+                    const float pr = __builtin_amdgcn_exp2f(sc[j][i] - ref);
                     lt += pr;
-                    x[i] = static_cast<int>(rintf(fminf(pr, 1.f) * kPScale));
+                    // the whole number nearest to p 127 2^16 < 2^23 lies in
+                    // the low bits of its sum with 2^23
+                    x[i] = __builtin_bit_cast(uint32_t, fmaf(pr, kPScale, 0x1p23f)) - (0x4B000000u - 0x8080u);
                 }
                 uint32_t d[3];
                 digits4(x, d);
@@ -226,30 +299,36 @@ __global__ __launch_bounds__(256) void attend_few_kernel(AttendArgs a) {
             }
             lt += xor_lane(lt, 16);
             lt += xor_lane(lt, 32);
-            // join with what came before; a page that this column does not
-            // see leaves everything as it is, whatever its scales are
-            const float m_new = any ? fmaxf(m_run, ref) : m_run;
-            const float keep = m_run == m_new ? 1.f : exp2f(m_run - m_new);
-            const float add = any ? exp2f(ref - m_new) : 0.f;
-            const float put = any ? add * (vs * (1.f / kPScale)) : 0.f;
-            l_run = l_run * keep + (any ? add * lt : 0.f);
-            m_run = m_new;
+            // Sums are kept relative to the maximum of the first page seen
+            // and moved to a larger one only where that is 2^40 away; a page
+            // that this column does not see leaves everything as it is,
+            // whatever its scales are.
+            const float off = ref - m_run;
+            if (__any(any && !(off <= 40.f))) {
+                const float m_new = any && !(off <= 40.f) ? ref : m_run;
+                const float keep = m_run == m_new ? 1.f : __builtin_amdgcn_exp2f(m_run - m_new);
+                l_run *= keep;
+                m_run = m_new;
+#pragma unroll
+                for (int e = 0; e < ET; ++e)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) o[e][i] *= keep;
+            }
+            const float add = any ? __builtin_amdgcn_exp2f(ref - m_run) : 0.f;
+            const float put = any ? add * (vscale * (65536.f / kPScale)) : 0.f;
+            l_run += any ? add * lt : 0.f;
 #pragma unroll
             for (int e = 0; e < ET; ++e) {
-                const i32x4 vf = *reinterpret_cast<const i32x4*>(vp + (16 * e + col) * kPage + 16 * quad);
                 i32x4 c[3];
 #pragma unroll
                 for (int k = 0; k < 3; ++k) {
                     const i32x4 b = {static_cast<int>(pd[k][0]), static_cast<int>(pd[k][1]),
                                      static_cast<int>(pd[k][2]), static_cast<int>(pd[k][3])};
-                    c[k] = __builtin_amdgcn_mfma_i32_16x16x64_i8(vf, b, i32x4{0, 0, 0, 0}, 0, 0, 0);
+                    c[k] = __builtin_amdgcn_mfma_i32_16x16x64_i8(vf[e], b, i32x4{0, 0, 0, 0}, 0, 0, 0);
                 }
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float t = fmaf(static_cast<float>(c[2][i]), 65536.f,
-                                         fmaf(static_cast<float>(c[1][i]), 256.f, static_cast<float>(c[0][i])));
-                    o[e][i] = fmaf(t, put, o[e][i] * keep);
-                }
+                for (int i = 0; i < 4; ++i) o[e][i] = fmaf(join3(c[0][i], c[1][i], c[2][i]), put, o[e][i]);
+                if (e % 4 == 3) __builtin_amdgcn_sched_barrier(0);
             }
         }
 
@@ -263,11 +342,10 @@ __global__ __launch_bounds__(256) void attend_few_kernel(AttendArgs a) {
             stat[wave][col][1] = l_run;
         }
         __syncthreads();
-        const int64_t n = r.count * a.group;
         for (int i = threadIdx.x; i < kCols * D; i += 256) {
             const int cc = i / D, dim = i % D;
-            const int64_t gc = tile * kCols + cc;
-            if (gc >= n) continue;
+            const uint32_t gc = tile * kCols + cc;
+            if (gc >= all) break;
             float m = stat[0][cc][0], l = 0.f, v = 0.f;
 #pragma unroll
             for (int u = 1; u < 4; ++u) m = fmaxf(m, stat[u][cc][0]);
@@ -277,76 +355,98 @@ __global__ __launch_bounds__(256) void attend_few_kernel(AttendArgs a) {
                 l += f * stat[u][cc][1];
                 v += f * acc[u][cc][dim];
             }
-            const uint64_t at = static_cast<uint64_t>(r.first + gc / a.group) * a.heads + kvh * a.group + gc % a.group;
+            const uint64_t at = static_cast<uint64_t>(r.first + static_cast<int32_t>(gc / a.group)) * a.heads + kvh * a.group + gc % a.group;
             if (a.pieces == 1) {
                 const float res = l == 0.f ? 0.f : v / l;
                 if constexpr (DT == QMV_F32) static_cast<float*>(a.out)[at * D + dim] = res;
                 else static_cast<__bf16*>(a.out)[at * D + dim] = static_cast<__bf16>(res);
             } else {
-                float* pp = a.part + (static_cast<uint64_t>(piece) * a.s.rows * a.heads + at) * (D + 2);
-                pp[dim] = v;
-                if (dim == 0) {
-                    pp[D] = m;
-                    pp[D + 1] = l;
-                }
+                // (of a piece without pages only the statistics are read)
+                const uint64_t slot = static_cast<uint64_t>(piece) * a.s.rows * a.heads + at;
+                if (p0 < p1) a.part[slot * D + dim] = v;
+                if (dim == 0) a.stat[slot] = make_float2(m, l);
             }
         }
         __syncthreads();
     }
 }
 
-// Joins the pieces of each column: a workgroup has the 16 columns that the
-// kernel before it had.
+// Joins the pieces of each column, one wave a column: lane z has piece z's
+// maximum and sum (at most 64 pieces), and the pieces' outputs are added in
+// their order, D / 64 values a lane.
 template <uint32_t DT, int D>
 __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a) {
+    constexpr int V = D / 64;
     const uint32_t seq = blockIdx.x / a.c.kv_heads, kvh = blockIdx.x % a.c.kv_heads;
+    const int lane = threadIdx.x & 63;
     const SeqRows r = seq_rows(a.s, seq);
-    const int64_t n = r.count * a.group;
-    const int64_t tiles = (n + kCols - 1) / kCols;
-    const uint64_t step = static_cast<uint64_t>(a.s.rows) * a.heads * (D + 2);
-    for (int64_t tile = blockIdx.y; tile < tiles; tile += gridDim.y) {
-        for (int i = threadIdx.x; i < kCols * D; i += 256) {
-            const int64_t gc = tile * kCols + i / D;
-            const int dim = i % D;
-            if (gc >= n) continue;
-            const uint64_t at = static_cast<uint64_t>(r.first + gc / a.group) * a.heads + kvh * a.group + gc % a.group;
-            const float* pp = a.part + at * (D + 2);
-            float m = -__builtin_inff();
-            for (uint32_t z = 0; z < a.pieces; ++z) m = fmaxf(m, pp[z * step + D]);
-            float l = 0.f, v = 0.f;
-            for (uint32_t z = 0; z < a.pieces; ++z) {
-                const float mz = pp[z * step + D];
-                const float f = mz == m ? 1.f : exp2f(mz - m);
-                l += f * pp[z * step + D + 1];
-                v += f * pp[z * step + dim];
+    const uint32_t n = static_cast<uint32_t>(r.count) * a.group;
+    const uint64_t step = static_cast<uint64_t>(a.s.rows) * a.heads;
+    for (uint32_t gc = blockIdx.y * 4 + (threadIdx.x >> 6); gc < n; gc += gridDim.y * 4) {
+        const uint64_t at = static_cast<uint64_t>(r.first + static_cast<int32_t>(gc / a.group)) * a.heads + kvh * a.group + gc % a.group;
+        float2 st = make_float2(-__builtin_inff(), 0.f);
+        if (static_cast<uint32_t>(lane) < a.pieces) st = a.stat[lane * step + at];
+        float m = st.x;
+#pragma unroll
+        for (int k = 1; k < 64; k <<= 1) m = fmaxf(m, xor_lane(m, k));
+        // pieces that saw nothing have the maximum -infinity and the sum 0
+        const float f = st.x == m ? 1.f : __builtin_amdgcn_exp2f(st.x - m);
+        float l = f * st.y;
+#pragma unroll
+        for (int k = 1; k < 64; k <<= 1) l += xor_lane(l, k);
+        const uint64_t used = __ballot(st.y != 0.f);
+        float v[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] = 0.f;
+        const float* pp = a.part + at * D + lane * V;
+        for (uint32_t z = 0; z < a.pieces; z += 8) {
+            float x[8][V];
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+                    x[u][i] = (used >> (z + u) & 1) != 0 ? pp[(z + u) * step * D + i] : 0.f;
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const float g = read_lane(f, (z + u) & 63);
+                if ((used >> (z + u) & 1) != 0) {
+#pragma unroll
+                    for (int i = 0; i < V; ++i) v[i] = fmaf(g, x[u][i], v[i]);
+                }
             }
-            const float res = l == 0.f ? 0.f : v / l;
-            if constexpr (DT == QMV_F32) static_cast<float*>(a.out)[at * D + dim] = res;
-            else static_cast<__bf16*>(a.out)[at * D + dim] = static_cast<__bf16>(res);
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const float res = l == 0.f ? 0.f : v[i] / l;
+            if constexpr (DT == QMV_F32) static_cast<float*>(a.out)[at * D + lane * V + i] = res;
+            else static_cast<__bf16*>(a.out)[at * D + lane * V + i] = static_cast<__bf16>(res);
         }
     }
 }
 
 // The launch: tiles of 16 columns of a sequence and head, and pieces of its
-// pages so that about two workgroups a compute unit run, with at least two
-// pages for each wave of a piece.
+// pages, so that a few workgroups a compute unit run and short sequences do
+// not leave the long ones behind, with at least two pages for each wave of a
+// piece.
 struct Plan {
-    uint32_t tiles, pieces;
+    uint32_t tiles, pieces, per;
 };
 Plan plan_few(const qmv_kv_cache& c, const qmv_kv_seqs& s, uint32_t heads, uint32_t window) {
     const uint64_t group = heads / c.kv_heads;
     const uint64_t most = s.max_new < s.rows ? (s.max_new == 0 ? 1 : s.max_new) : s.rows;
     uint64_t tiles = (most * group + kCols - 1) / kCols;
-    if (tiles > 16384) tiles = 16384;
+    if (tiles > 8192) tiles = 8192;
     uint64_t span = s.max_len;
     if (window != 0 && span > uint64_t{window} + kCols) span = uint64_t{window} + kCols;
     const uint64_t pages = (span + kPage - 1) / kPage + 1;
     const uint64_t wgs = uint64_t{s.seqs} * c.kv_heads * tiles;
-    uint64_t pieces = (512 + wgs - 1) / wgs;
-    if (pieces > (pages + 7) / 8) pieces = (pages + 7) / 8;
-    if (pieces > 256) pieces = 256;
+    static const uint64_t T1 = getenv("QT") ? atoi(getenv("QT")) : 512, T2 = getenv("QP") ? atoi(getenv("QP")) : 8;
+    uint64_t pieces = (T1 + wgs - 1) / wgs;
+    if (pieces > (pages + T2 - 1) / T2) pieces = (pages + T2 - 1) / T2;
+    if (pieces > 64) pieces = 64;
     if (pieces < 1) pieces = 1;
-    return Plan{static_cast<uint32_t>(tiles), static_cast<uint32_t>(pieces)};
+    return Plan{static_cast<uint32_t>(tiles), static_cast<uint32_t>(pieces),
+                static_cast<uint32_t>((pages + pieces - 1) / pieces)};
 }
 
 template <uint32_t DT, int D>
@@ -355,7 +455,7 @@ hipError_t go_few(const AttendArgs& a, const Plan& p, hipStream_t s) {
     hipLaunchKernelGGL((attend_few_kernel<DT, D>), grid, block, 0, s, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.pieces == 1) return e;
-    hipLaunchKernelGGL((attend_join_kernel<DT, D>), dim3(grid.x, p.tiles), block, 0, s, a);
+    hipLaunchKernelGGL((attend_join_kernel<DT, D>), dim3(grid.x, p.tiles * (kCols / 4)), block, 0, s, a);
     return hipGetLastError();
 }
 
@@ -365,15 +465,17 @@ uint64_t kv_attend_workspace_bytes(const qmv_kv_cache& c, const qmv_kv_seqs& s, 
                                    uint32_t window) {
     const Plan p = plan_few(c, s, heads, window);
     if (p.pieces == 1) return 0;
-    return uint64_t{p.pieces} * s.rows * heads * (c.head_dim + 2) * 4;
+    return uint64_t{p.pieces} * s.rows * heads * (c.head_dim + 2) * 4;  // outputs, then statistics
 }
 
 hipError_t launch_kv_attend(const qmv_kv_cache& c, const qmv_kv_seqs& s, uint32_t dtype, uint32_t heads,
                             float scale, uint32_t window, const void* q, void* out, void* workspace,
                             hipStream_t stream) {
     const Plan p = plan_few(c, s, heads, window);
-    const AttendArgs a{c, s, q, out, static_cast<float*>(workspace), scale * kLog2e, heads,
-                       heads / c.kv_heads, window, p.pieces};
+    float* part = static_cast<float*>(workspace);
+    const uint64_t outputs = uint64_t{p.pieces} * s.rows * heads * c.head_dim;
+    const AttendArgs a{c, s, q, out, part, reinterpret_cast<float2*>(part + outputs), scale * kLog2e, heads,
+                       heads / c.kv_heads, window, p.pieces, p.per};
     if (dtype == QMV_F32) {
         if (c.head_dim == 64) return go_few<QMV_F32, 64>(a, p, stream);
         if (c.head_dim == 128) return go_few<QMV_F32, 128>(a, p, stream);

@@ -81,15 +81,15 @@ __global__ __launch_bounds__(256) void kv_write_kernel(qmv_kv_cache c, qmv_kv_se
     const int tid = threadIdx.x;
     const SeqRows r = seq_rows(s, seq);
     if (r.count == 0 || r.len == 0) return;
-    const int64_t from = max(r.base, int64_t{0});               // first new position
-    const int64_t last = (r.len - 1) / kPage;
+    const int32_t from = max(r.base, 0);               // first new position
+    const int32_t last = (r.len - 1) / kPage;
     const typename Elem<DT>::type* src = values ? v : k;
-    for (int64_t p = from / kPage + blockIdx.y; p <= last; p += gridDim.y) {
-        const int64_t id = page_id(c, s, seq, p);
+    for (int32_t p = from / kPage + blockIdx.y; p <= last; p += gridDim.y) {
+        const int32_t id = page_id(c, s, seq, p);
         if (id < 0) continue;
-        const int lo = static_cast<int>(max(from - p * kPage, int64_t{0}));
-        const int hi = static_cast<int>(min(r.len - p * kPage, static_cast<int64_t>(kPage)));
-        const int64_t row0 = r.first + (p * kPage - r.base);      // row of the page's token 0
+        const int lo = max(from - p * kPage, 0);
+        const int hi = min(r.len - p * kPage, kPage);
+        const int32_t row0 = r.first + (p * kPage - r.base);      // row of the page's token 0
         float x[PER][8];
         uint32_t m = 0;
 #pragma unroll
@@ -186,13 +186,13 @@ __global__ __launch_bounds__(256) void kv_read_kernel(qmv_kv_cache c, qmv_kv_seq
     if (r.count == 0) return;
     // pages that hold the rows, from the one below position 0 that rows
     // without a place count as (floor division)
-    const int64_t first = (r.base >= 0 ? r.base : r.base - (kPage - 1)) / kPage;
-    const int64_t last = (r.len + kPage - 1) / kPage - 1;
-    for (int64_t p = first + blockIdx.y; p <= last; p += gridDim.y) {
-        const int64_t id = page_id(c, s, seq, p);
-        const int lo = static_cast<int>(max(r.base - p * kPage, int64_t{0}));
-        const int hi = static_cast<int>(min(r.len - p * kPage, static_cast<int64_t>(kPage)));
-        const int64_t row0 = r.first + (p * kPage - r.base);
+    const int32_t first = (r.base >= 0 ? r.base : r.base - (kPage - 1)) / kPage;
+    const int32_t last = (r.len + kPage - 1) / kPage - 1;
+    for (int32_t p = first + blockIdx.y; p <= last; p += gridDim.y) {
+        const int32_t id = page_id(c, s, seq, p);
+        const int lo = max(r.base - p * kPage, 0);
+        const int hi = min(r.len - p * kPage, kPage);
+        const int32_t row0 = r.first + (p * kPage - r.base);
         const uint64_t at = static_cast<uint64_t>(id < 0 ? 0 : id) * c.kv_heads + head;
         const float d = id < 0 ? 0.f : (values ? c.v_scale : c.k_scale)[at];
         const uint8_t* page = reinterpret_cast<const uint8_t*>(values ? c.v : c.k) + at * (kPage * D);

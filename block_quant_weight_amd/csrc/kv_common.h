@@ -9,22 +9,23 @@ namespace qmv {
 constexpr int kPage = QMV_KV_PAGE;
 
 // Rows [first, first + count) of sequence i, at positions base + 0 ..
-// count - 1 (base may be negative), of `len` tokens.
+// count - 1 (base may be negative), of `len` tokens.  All below 2^31; base
+// >= -2^31 + 1 as count <= rows < 2^31.
 struct SeqRows {
-    int64_t first, count, base, len;
+    int32_t first, count, base, len;
 };
 __device__ __forceinline__ SeqRows seq_rows(const qmv_kv_seqs& s, uint32_t i) {
-    const int64_t rows = s.rows;
-    const int64_t a = min(max(static_cast<int64_t>(s.start[i]), int64_t{0}), rows);
-    const int64_t b = min(max(static_cast<int64_t>(s.start[i + 1]), a), rows);
-    const int64_t len = max(static_cast<int64_t>(s.len[i]), int64_t{0});
+    const int32_t rows = static_cast<int32_t>(s.rows);
+    const int32_t a = min(max(s.start[i], 0), rows);
+    const int32_t b = min(max(s.start[i + 1], a), rows);
+    // (lengths end 2^31 - 2^16 early, so that a page past one is counted without overflow)
+    const int32_t len = min(max(s.len[i], 0), 0x7FFF0000);
     return SeqRows{a, b - a, len - (b - a), len};
 }
 
 // Page id of a sequence's page number p, or -1 where there is none.
-__device__ __forceinline__ int64_t page_id(const qmv_kv_cache& c, const qmv_kv_seqs& s, uint32_t seq,
-                                           int64_t p) {
-    if (p < 0 || p >= static_cast<int64_t>(s.table_stride)) return -1;
+__device__ __forceinline__ int32_t page_id(const qmv_kv_cache& c, const qmv_kv_seqs& s, uint32_t seq, int32_t p) {
+    if (p < 0 || static_cast<uint32_t>(p) >= s.table_stride) return -1;
     const int32_t id = s.table[static_cast<uint64_t>(seq) * s.table_stride + p];
     return id >= 0 && static_cast<uint32_t>(id) < c.pages ? id : -1;
 }

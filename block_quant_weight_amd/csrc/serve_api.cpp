@@ -33,14 +33,15 @@ int check_kv(const qmv_kv_cache* c, const qmv_kv_seqs* s, uint32_t dtype) {
     if (c->pages == 0 || c->kv_heads == 0 || s->seqs == 0 || s->table_stride == 0 || s->rows == 0)
         return QMV_E_ARG;
     if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) return QMV_E_SHAPE;
-    if (c->kv_heads > 65535 || c->pages > 0x7FFFFFFFu || s->rows > 0x7FFFFFFFu ||
+    if (c->kv_heads > 65535 || c->pages > 0x7FFFFFFFu || s->rows > 0x7FFF0000u ||
         uint64_t{s->seqs} * c->kv_heads > 0x7FFFFFFFu)
         return QMV_E_SHAPE;
     return QMV_OK;
 }
 
-int check_heads(const qmv_kv_cache* c, uint32_t heads) {
-    return heads == 0 || heads % c->kv_heads != 0 || heads > kDimLimit ? QMV_E_SHAPE : QMV_OK;
+int check_heads(const qmv_kv_cache* c, const qmv_kv_seqs* s, uint32_t heads) {
+    if (heads == 0 || heads % c->kv_heads != 0) return QMV_E_SHAPE;
+    return uint64_t{s->rows} * heads > 0x7FFF0000u ? QMV_E_SHAPE : QMV_OK;
 }
 
 }  // namespace
@@ -88,7 +89,7 @@ int qmv_kv_attend_workspace(const qmv_kv_cache* cache, const qmv_kv_seqs* seqs, 
     if (bytes == nullptr) return QMV_E_ARG;
     *bytes = 0;
     int st = check_kv(cache, seqs, dtype);
-    if (st == QMV_OK) st = check_heads(cache, heads);
+    if (st == QMV_OK) st = check_heads(cache, seqs, heads);
     if (st != QMV_OK) return st;
     *bytes = qmv::kv_attend_workspace_bytes(*cache, *seqs, dtype, heads, window);
     return QMV_OK;
@@ -98,7 +99,7 @@ int qmv_kv_attend(const qmv_kv_cache* cache, const qmv_kv_seqs* seqs, uint32_t d
                   uint32_t heads, float scale, uint32_t window, const void* q, void* out,
                   void* workspace, uint64_t workspace_bytes, void* stream) {
     int st = check_kv(cache, seqs, dtype);
-    if (st == QMV_OK) st = check_heads(cache, heads);
+    if (st == QMV_OK) st = check_heads(cache, seqs, heads);
     if (st != QMV_OK) return st;
     if (q == nullptr || out == nullptr || !std::isfinite(scale)) return QMV_E_ARG;
     if (!aligned(q, 16) || !aligned(out, 16) || !aligned(workspace, 16)) return QMV_E_ARG;
