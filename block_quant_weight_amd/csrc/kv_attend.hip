@@ -78,6 +78,23 @@ __device__ __forceinline__ float join3(int c0, int c1, int c2) {
 
 __device__ __forceinline__ float xor_lane(float v, int m) { return __shfl_xor(v, m); }
 
+// Largest over the lanes 32 apart, and over those 16, 32 and 48 apart.  With
+// both operands alike, a swap leaves one half of the wave (one row of each
+// pair) in the first and the other in the second.  (The results go through
+// variables of their own: a bit cast of a vector's element takes element 0.)
+__device__ __forceinline__ float max_halves(float v) {
+    const uint32_t u = __builtin_bit_cast(uint32_t, v);
+    const auto a = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    const uint32_t x = a[0], y = a[1];
+    return fmaxf(__builtin_bit_cast(float, x), __builtin_bit_cast(float, y));
+}
+__device__ __forceinline__ float max_quads(float v) {
+    const uint32_t u = __builtin_bit_cast(uint32_t, v);
+    const auto a = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+    const uint32_t x = a[0], y = a[1];
+    return max_halves(fmaxf(__builtin_bit_cast(float, x), __builtin_bit_cast(float, y)));
+}
+
 // First position that a row at position p sees.
 __device__ __forceinline__ int32_t sees_from(uint32_t window, int32_t p) {
     return window == 0 || window > static_cast<uint32_t>(max(p, 0)) ? 0 : p - static_cast<int32_t>(window) + 1;
@@ -156,9 +173,11 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attend_few_kernel(Atten
             }
         };
         auto fetch = [&](int n) {
+            // (where there is no page, page 0, which every cache has, is read
+            // and not used: a branch here would keep two sets of registers)
             id = __builtin_amdgcn_readlane(ids, n);
-            if (id < 0) return;
-            const int8_t* kp = a.c.k + (static_cast<uint64_t>(id) * a.c.kv_heads + kvh) * (kPage * D) + krow * D + 16 * quad;
+            const uint64_t at = static_cast<uint64_t>(max(id, 0)) * a.c.kv_heads + kvh;
+            const int8_t* kp = a.c.k + at * (kPage * D) + krow * D + 16 * quad;
 #pragma unroll
             for (int j = 0; j < 4; ++j)
 #pragma unroll
@@ -274,12 +293,11 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attend_few_kernel(Atten
             for (int j = 0; j < 4; ++j)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) mt = fmaxf(mt, sc[j][i]);
-            mt = fmaxf(mt, xor_lane(mt, 16));
-            mt = fmaxf(mt, xor_lane(mt, 32));
+            mt = max_quads(mt);
             // nothing seen, or only NaN: the maximum counts as 0 (NaN scores
             // still make the sum NaN, and so does a score of +infinity)
             const float ref = mt > -__builtin_inff() ? mt : 0.f;
-            float lt = 0.f;
+            float lt[4] = {0.f, 0.f, 0.f, 0.f};
             uint32_t pd[3][4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -287,7 +305,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attend_few_kernel(Atten
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const float pr = __builtin_amdgcn_exp2f(sc[j][i] - ref);
-                    lt += pr;
+                    lt[i] += pr;
                     // the whole number nearest to p 127 2^16 < 2^23 lies in
                     // the low bits of its sum with 2^23
                     x[i] = __builtin_bit_cast(uint32_t, fmaf(pr, kPScale, 0x1p23f)) - (0x4B000000u - 0x8080u);
@@ -297,9 +315,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attend_few_kernel(Atten
 #pragma unroll
                 for (int k = 0; k < 3; ++k) pd[k][j] = d[k];
             }
-            lt += xor_lane(lt, 16);
-            lt += xor_lane(lt, 32);
-            // Sums are kept relative to the maximum of the first page seen
+            // Sums (of this lane's tokens; the lanes' are added at the end) are kept relative to the maximum of the first page seen
             // and moved to a larger one only where that is 2^40 away; a page
             // that this column does not see leaves everything as it is,
             // whatever its scales are.
@@ -316,7 +332,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attend_few_kernel(Atten
             }
             const float add = any ? __builtin_amdgcn_exp2f(ref - m_run) : 0.f;
             const float put = any ? add * (vscale * (65536.f / kPScale)) : 0.f;
-            l_run += any ? add * lt : 0.f;
+            l_run += any ? add * ((lt[0] + lt[1]) + (lt[2] + lt[3])) : 0.f;
 #pragma unroll
             for (int e = 0; e < ET; ++e) {
                 i32x4 c[3];
@@ -332,6 +348,8 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attend_few_kernel(Atten
             }
         }
 
+        l_run += xor_lane(l_run, 16);
+        l_run += xor_lane(l_run, 32);
         // the four waves' results
 #pragma unroll
         for (int e = 0; e < ET; ++e)
