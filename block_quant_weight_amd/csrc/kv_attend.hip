@@ -29,7 +29,6 @@
 // fourth page and keeps its own running maximum, sum and output, joined in
 // shared memory at the end.  The pieces of a sequence are joined by a second
 // kernel, in their order.
-#include <cstdlib>
 #include "kv_common.h"
 
 namespace qmv {
@@ -40,7 +39,7 @@ typedef int i32x4 __attribute__((ext_vector_type(4)));
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kPScale = 127.0f * 65536.0f;   // p = 1 as a whole number
 constexpr int kCols = 16;                      // columns of a workgroup
-constexpr uint32_t kTarget = 1024;             // workgroups that a launch aims at
+constexpr uint32_t kTarget = 256;              // workgroups that a launch aims at
 
 struct AttendArgs {
     qmv_kv_cache c;
@@ -389,6 +388,346 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attend_few_kernel(Atten
     }
 }
 
+// ---- many queries a key/value head (bfloat16 prompts) -------------------------
+//
+// Products on v_mfma_f32_32x32x16_f16: a workgroup of NW waves has 32 NW
+// columns, each wave 32, and walks the pages that any of them sees.  A page's
+// codes come from memory into registers one page ahead, are made f16 once for
+// all waves on the way into shared memory (1024 + 128 + code is the f16 with
+// the bits 0x6400 | (code ^ 0x80); one packed operation takes the 1152 off
+// again) and lie there twice, so that one barrier a page is enough.
+//
+// All operands are exact: a query row is scaled by a power of two to a largest
+// magnitude in [2^14, 2^15) (bfloat16's 8 bits fit f16's 11), codes are whole
+// numbers.  The values' scales enter as powers of two relative to a reference
+// exponent that follows the pages' largest: code 2^(e - ref), exact from
+// 2^-19 up; probabilities are rounded to f16 and their sum is taken from the
+// rounded ones, so that numerator and denominator agree.  Sums are relative
+// to a running reference that is moved (and the outputs scaled) only when a
+// page's maximum is more than 2^8 above it: p <= 2^8, times 2^7 so that f16
+// keeps 2^-29 of the maximum at full precision.
+//
+// Rows and columns are arranged as above: the 32 x 32 output gives lane l,
+// register 4 a + b the row 8 a + 4 (l / 32) + b and takes the k-indexes 8 (l /
+// 32) + .. from it, so with row r of a tile read from token 16 (a / 2) + 8 (l
+// / 32) + 4 (a % 2) + b the probabilities stay in their lanes.
+//
+// Shared memory: 16-byte chunks of a row are permuted by the row's number so
+// that eight neighbouring lanes, which read eight different rows, fall into
+// eight different 16-byte columns.
+
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+
+constexpr float kPBias = 7.0f;         // probabilities times 2^7
+constexpr float kMoveAt = 8.0f;        // reference moved when a maximum is 2^8 above
+
+// Row r of a score tile: its token.
+__device__ __forceinline__ int token_of_row(int r) {
+    const int a = r >> 3, h = (r >> 2) & 1, b = r & 3;
+    return 16 * (a >> 1) + 8 * h + 4 * (a & 1) + b;
+}
+// Column permutation of a row of keys (rows are read in token_of_row's order).
+__device__ __forceinline__ int k_swizzle(int row) { return (row & 3) | ((row >> 1) & 4); }
+
+// 16 codes as f16, each times mul: x * mul - 1152 mul.
+__device__ __forceinline__ void codes_to_f16(i32x4 c, _Float16 mul, f16x8 out[2]) {
+    const f16x2 m = {mul, mul};
+    const f16x2 s = {static_cast<_Float16>(mul * static_cast<_Float16>(-1152.f)), static_cast<_Float16>(mul * static_cast<_Float16>(-1152.f))};
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        const uint32_t u = static_cast<uint32_t>(c[w]) ^ 0x80808080u;
+        const f16x2 lo = __builtin_elementwise_fma(
+            __builtin_bit_cast(f16x2, __builtin_amdgcn_perm(0x64646464u, u, 0x04010400u)), m, s);
+        const f16x2 hi = __builtin_elementwise_fma(
+            __builtin_bit_cast(f16x2, __builtin_amdgcn_perm(0x64646464u, u, 0x04030402u)), m, s);
+        out[w >> 1][4 * (w & 1)] = lo[0];
+        out[w >> 1][4 * (w & 1) + 1] = lo[1];
+        out[w >> 1][4 * (w & 1) + 2] = hi[0];
+        out[w >> 1][4 * (w & 1) + 3] = hi[1];
+    }
+}
+
+// Exponent of a scale (a power of two, possibly from another hand: then its
+// own exponent), kNone for 0.
+constexpr int kNone = -1000;
+__device__ __forceinline__ int exponent_of(float s) {
+    const uint32_t b = __builtin_bit_cast(uint32_t, s) & 0x7FFFFFFFu;
+    return b < 0x00800000u ? kNone : static_cast<int>(b >> 23) - 127;
+}
+
+template <int D, int NW>
+__global__ __launch_bounds__(NW * 64, NW / 4) void attend_many_kernel(AttendArgs a) {
+    constexpr int NT = NW * 64;
+    constexpr int COLS = 32 * NW;
+    constexpr int KC = D / 8;                    // 16-byte chunks of a key row
+    constexpr int UNITS = 2 * kPage * D / 16;    // 16-code pieces of a page: keys, then values
+    constexpr int PER = UNITS / NT;
+    constexpr int QS = D / 16;                   // k-steps of a score
+    constexpr int ET = D / 32;                   // tiles of output dims
+    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+    f16x8* const kbuf = reinterpret_cast<f16x8*>(lds);                       // [2][64][KC]
+    f16x8* const vbuf = kbuf + 2 * kPage * KC;                               // [2][D][8]
+    const int tid = threadIdx.x, lane = tid & 63, col = lane & 31, half = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const uint32_t seq = blockIdx.x / a.c.kv_heads, kvh = blockIdx.x % a.c.kv_heads;
+    const uint32_t piece = blockIdx.z;
+    const SeqRows r = seq_rows(a.s, seq);
+    const uint32_t all = static_cast<uint32_t>(r.count) * a.group;
+    const uint32_t tiles = (all + COLS - 1) / COLS;
+    // the last tiles see the most: they begin first
+    for (uint32_t turn = blockIdx.y; turn < tiles; turn += gridDim.y) {
+        const uint32_t tile = tiles - 1 - turn;
+        const Columns w = columns<COLS>(a, r, kvh, tile, wave * 32 + col);
+        const int32_t p_lo = w.lo / kPage, p_hi = (w.hi + kPage - 1) / kPage;
+        const int32_t per = max((p_hi - p_lo + static_cast<int32_t>(a.pieces) - 1) / static_cast<int32_t>(a.pieces),
+                                static_cast<int32_t>(a.per));
+        const int64_t begin = p_lo + static_cast<int64_t>(piece) * per;
+        const int32_t p0 = static_cast<int32_t>(min(begin, static_cast<int64_t>(p_hi)));
+        const int32_t p1 = min(p_hi - p0, per) + p0;
+        const int32_t see_lo = sees_from(a.window, w.pos);
+        // this wave's columns: what any sees, and the pages that all see whole
+        const uint32_t c0 = tile * COLS + wave * 32;
+        const uint32_t n_cols = c0 < all ? min(all - c0, 32u) : 0u;
+        const int32_t wf = r.base + static_cast<int32_t>(c0 / a.group);
+        const int32_t wl = r.base + static_cast<int32_t>((c0 + max(n_cols, 1u) - 1) / a.group);
+        const int32_t w_lo = sees_from(a.window, max(wf, 0));
+        const int32_t w_hi = n_cols != 0 ? max(wl + 1, 0) : 0;
+        const int32_t full_lo = sees_from(a.window, wl), full_hi = wf + 1;
+
+        // the queries, f16, as the second operand of the scores
+        f16x8 qf[QS];
+        float qs;
+        {
+            const uint16_t* qp = static_cast<const uint16_t*>(a.q) +
+                                 (static_cast<uint64_t>(w.row < 0 ? 0 : w.row) * a.heads + w.head) * D;
+            uint4 raw[QS];
+            uint32_t m = 0;
+#pragma unroll
+            for (int s = 0; s < QS; ++s) {
+                raw[s] = make_uint4(0, 0, 0, 0);
+                if (w.row >= 0) raw[s] = *reinterpret_cast<const uint4*>(qp + 16 * s + 8 * half);
+            }
+#pragma unroll
+            for (int s = 0; s < QS; ++s) {
+                const uint32_t u[4] = {raw[s].x, raw[s].y, raw[s].z, raw[s].w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) m = max(m, max(u[i] & 0x7FFFu, (u[i] >> 16) & 0x7FFFu));
+            }
+            m = max(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), 32)));
+            const bool zero = m == 0 || m >= 0x7F80u;
+            int e = 0;
+            if (!zero) (void)frexpf(__builtin_bit_cast(float, m << 16), &e);   // |q| < 2^e
+            qs = m >= 0x7F80u ? __builtin_nanf("") : (zero ? 0.f : ldexpf(1.f, e - 15));
+#pragma unroll
+            for (int s = 0; s < QS; ++s) {
+                const uint32_t u[4] = {raw[s].x, raw[s].y, raw[s].z, raw[s].w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float x = __builtin_bit_cast(float, u[i] << 16), y = __builtin_bit_cast(float, u[i] & 0xFFFF0000u);
+                    qf[s][2 * i] = static_cast<_Float16>(zero ? 0.f : ldexpf(x, 15 - e));
+                    qf[s][2 * i + 1] = static_cast<_Float16>(zero ? 0.f : ldexpf(y, 15 - e));
+                }
+            }
+        }
+        const float q_log2 = qs * a.scale_log2;
+
+        f32x16 o[ET];
+#pragma unroll
+        for (int e = 0; e < ET; ++e)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[e][i] = 0.f;
+        float m_run = -__builtin_inff(), l_run = 0.f;   // this lane's part of the sum
+        int e_ref = kNone;
+
+        // a page's codes, one page ahead of their use
+        i32x4 st[PER];
+        int32_t next_id = -1;
+        float next_ks = 0.f, next_vs = 0.f;
+        auto fetch = [&](int32_t p) {
+            next_id = p < p1 ? page_id(a.c, a.s, seq, p) : -1;
+            const uint64_t at = static_cast<uint64_t>(max(next_id, 0)) * a.c.kv_heads + kvh;
+            next_ks = a.c.k_scale[at];
+            next_vs = a.c.v_scale[at];
+#pragma unroll
+            for (int u = 0; u < PER; ++u) {
+                const int i = tid + u * NT;
+                const int8_t* src = i < UNITS / 2 ? a.c.k + at * (kPage * D) + 16 * i
+                                                  : a.c.v + at * (kPage * D) + 16 * (i - UNITS / 2);
+                st[u] = *reinterpret_cast<const i32x4*>(src);
+            }
+        };
+        // The codes into shared memory; the values by 2^(their exponent -
+        // the reference), which moves up where that would pass 2^5 (the
+        // packed conversion stays below f16's 65504 up to there).
+        auto stage = [&](int b, int e_page) {
+            const int up = max(min(e_page - e_ref, 5), -24);
+            const _Float16 vmul = static_cast<_Float16>(e_page == kNone ? 0.f : ldexpf(1.f, up));
+#pragma unroll
+            for (int u = 0; u < PER; ++u) {
+                const int i = tid + u * NT;
+                f16x8 x[2];
+                codes_to_f16(st[u], i < UNITS / 2 ? static_cast<_Float16>(1.f) : vmul, x);
+                if (i < UNITS / 2) {
+                    const int row = i / (D / 16), c = 2 * (i % (D / 16));
+                    f16x8* d = kbuf + (b * kPage + row) * KC;
+                    d[c ^ k_swizzle(row)] = x[0];
+                    d[(c + 1) ^ k_swizzle(row)] = x[1];
+                } else {
+                    const int k = i - UNITS / 2, row = k >> 2, c = 2 * (k & 3);
+                    f16x8* d = vbuf + (b * D + row) * 8;
+                    d[c ^ (row & 7)] = x[0];
+                    d[(c + 1) ^ (row & 7)] = x[1];
+                }
+            }
+        };
+        auto settle = [&](float vs) {            // the reference exponent with a new page; by how much it moves
+            const int e = exponent_of(vs);
+            if (e == kNone || vs != vs) return 0;
+            if (e_ref == kNone) e_ref = e;
+            const int move = e - e_ref > 5 ? e - e_ref : 0;
+            e_ref += move;
+            return move;
+        };
+
+        if (p0 < p1) {
+            fetch(p0);
+            int32_t id = next_id;
+            float ks = next_ks, vs = next_vs;
+            int move = id >= 0 ? settle(vs) : 0;
+            stage(0, exponent_of(vs));
+            __syncthreads();
+            for (int32_t p = p0; p < p1; ++p) {
+                const int b = (p - p0) & 1;
+                fetch(p + 1);
+                // outputs so far follow the reference exponent
+                if (move != 0) {
+                    const float f = ldexpf(1.f, -move);
+#pragma unroll
+                    for (int e = 0; e < ET; ++e)
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) o[e][i] *= f;
+                }
+                const int32_t t0 = p * kPage;
+                if (id >= 0 && t0 < w_hi && t0 + kPage > w_lo) {
+                    f32x16 sc[2];
+                    const f16x8* kb = kbuf + b * kPage * KC;
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) sc[t][i] = 0.f;
+                        const int row = 32 * t + token_of_row(col);
+#pragma unroll
+                        for (int s = 0; s < QS; ++s)
+                            sc[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
+                                kb[row * KC + ((2 * s + half) ^ k_swizzle(row))], qf[s], sc[t], 0, 0, 0);
+                    }
+                    const float f = q_log2 * ks;
+                    bool any = true;
+                    if (t0 < full_lo || t0 + kPage > full_hi || n_cols != 32) {
+                        // (scaled first: a masked score is no longer touched)
+                        const int from = max(see_lo - t0, 0), to = w.row < 0 ? 0 : min(w.pos + 1 - t0, kPage);
+                        any = from < to;
+#pragma unroll
+                        for (int t = 0; t < 2; ++t)
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) {
+                                const int k = 32 * t + 16 * (i >> 3) + 8 * half + (i & 7);
+                                sc[t][i] = k >= from && k < to ? sc[t][i] * f : -__builtin_inff();
+                            }
+                    } else {
+#pragma unroll
+                        for (int t = 0; t < 2; ++t)
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) sc[t][i] *= f;
+                    }
+                    float mt = -__builtin_inff();
+#pragma unroll
+                    for (int t = 0; t < 2; ++t)
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) mt = fmaxf(mt, sc[t][i]);
+                    mt = max_halves(mt);
+                    // (of a page that shows only NaN the reference is 0)
+                    const float ref = mt > -__builtin_inff() ? mt : (any && m_run == -__builtin_inff() ? 0.f : m_run);
+                    if (__any(any && !(ref - m_run <= kMoveAt))) {
+                        const float m_new = any && !(ref - m_run <= kMoveAt) ? ref : m_run;
+                        const float keep = m_run == m_new ? 1.f : __builtin_amdgcn_exp2f(m_run - m_new);
+                        l_run *= keep;
+                        m_run = m_new;
+#pragma unroll
+                        for (int e = 0; e < ET; ++e)
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) o[e][i] *= keep;
+                    }
+                    // (a column that has seen nothing yet: e^-inf, not inf - inf)
+                    const float base = (m_run > -__builtin_inff() ? m_run : 0.f) - kPBias;
+                    const bool vnan = vs != vs;
+                    f16x8 pf[4];
+#pragma unroll
+                    for (int t = 0; t < 2; ++t)
+#pragma unroll
+                        for (int i = 0; i < 16; i += 2) {
+                            const float x = __builtin_amdgcn_exp2f(sc[t][i] - base);
+                            const float y = __builtin_amdgcn_exp2f(sc[t][i + 1] - base);
+                            const f16x2 h = {static_cast<_Float16>(x), static_cast<_Float16>(y)};
+                            const f16x2 one = {static_cast<_Float16>(1.f), static_cast<_Float16>(1.f)};
+                            l_run = __builtin_amdgcn_fdot2(h, one, l_run, false);
+                            pf[2 * t + (i >> 3)][i & 7] = h[0];
+                            pf[2 * t + (i >> 3)][(i & 7) + 1] = h[1];
+                        }
+                    if (vnan && any) l_run = __builtin_nanf("");
+                    const f16x8* vb = vbuf + b * D * 8;
+#pragma unroll
+                    for (int e = 0; e < ET; ++e) {
+                        const int row = 32 * e + col;
+#pragma unroll
+                        for (int s = 0; s < 4; ++s)
+                            o[e] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vb[row * 8 + ((2 * s + half) ^ (row & 7))],
+                                                                          pf[s], o[e], 0, 0, 0);
+                    }
+                }
+                id = next_id;
+                ks = next_ks;
+                vs = next_vs;
+                move = id >= 0 ? settle(vs) : 0;
+                stage(b ^ 1, exponent_of(vs));
+                __syncthreads();
+            }
+        }
+
+        // Outputs: a lane has, for its column, four dims at a time.
+        const float l = l_run + xor_lane(l_run, 32);
+        if (w.row >= 0) {
+            const uint64_t at = static_cast<uint64_t>(w.row) * a.heads + w.head;
+            const float v_scale = e_ref == kNone ? 0.f : ldexpf(1.f, e_ref);
+            if (a.pieces == 1) {
+                const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+                for (int e = 0; e < ET; ++e)
+#pragma unroll
+                    for (int i = 0; i < 16; i += 4) {
+                        typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+                        bf16x4 x;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) x[k] = static_cast<__bf16>((o[e][i + k] * inv) * v_scale);
+                        *reinterpret_cast<bf16x4*>(static_cast<__bf16*>(a.out) + at * D + 32 * e + 2 * i + 4 * half) = x;
+                    }
+            } else {
+                const uint64_t slot = static_cast<uint64_t>(piece) * a.s.rows * a.heads + at;
+                if (p0 < p1) {
+#pragma unroll
+                    for (int e = 0; e < ET; ++e)
+#pragma unroll
+                        for (int i = 0; i < 16; i += 4)
+                            *reinterpret_cast<float4*>(a.part + slot * D + 32 * e + 2 * i + 4 * half) =
+                                make_float4(o[e][i] * v_scale, o[e][i + 1] * v_scale, o[e][i + 2] * v_scale, o[e][i + 3] * v_scale);
+                }
+                if (half == 0) a.stat[slot] = make_float2(m_run, l);
+            }
+        }
+    }
+}
+
 // Joins the pieces of each column, one wave a column: lane z has piece z's
 // maximum and sum (at most 64 pieces), and the pieces' outputs are added in
 // their order, D / 64 values a lane.
@@ -443,9 +782,9 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a) {
 }
 
 // The launch: tiles of 16 columns of a sequence and head, and pieces of its
-// pages, so that a few workgroups a compute unit run and short sequences do
-// not leave the long ones behind, with at least two pages for each wave of a
-// piece.
+// pages, so that every compute unit has a workgroup, with at least two pages
+// for each wave of a piece.  (One workgroup of four waves a compute unit:
+// 2 x 131072 tokens 63 us, two 69, four 75; 32 x 4000 38, 40 and 43.)
 struct Plan {
     uint32_t tiles, pieces, per;
 };
@@ -458,13 +797,58 @@ Plan plan_few(const qmv_kv_cache& c, const qmv_kv_seqs& s, uint32_t heads, uint3
     if (window != 0 && span > uint64_t{window} + kCols) span = uint64_t{window} + kCols;
     const uint64_t pages = (span + kPage - 1) / kPage + 1;
     const uint64_t wgs = uint64_t{s.seqs} * c.kv_heads * tiles;
-    static const uint64_t T1 = getenv("QT") ? atoi(getenv("QT")) : 512, T2 = getenv("QP") ? atoi(getenv("QP")) : 8;
-    uint64_t pieces = (T1 + wgs - 1) / wgs;
-    if (pieces > (pages + T2 - 1) / T2) pieces = (pages + T2 - 1) / T2;
+    uint64_t pieces = (kTarget + wgs - 1) / wgs;
+    if (pieces > (pages + 7) / 8) pieces = (pages + 7) / 8;
     if (pieces > 64) pieces = 64;
     if (pieces < 1) pieces = 1;
     return Plan{static_cast<uint32_t>(tiles), static_cast<uint32_t>(pieces),
                 static_cast<uint32_t>((pages + pieces - 1) / pieces)};
+}
+
+// bfloat16 queries with at least this many columns a sequence go to the
+// kernel for many.  Measured with 32 heads on 8 (four columns a row), us for
+// many / few: 64 columns, 8 sequences of 3000: 40 / 32, one of 16000: 33 / 28;
+// 128 columns: 44 / 44 and 36 / 39; 256 columns: 54 / 77 and 45 / 62.
+constexpr uint32_t kManyCols = 128;
+
+bool is_many(const qmv_kv_cache& c, const qmv_kv_seqs& s, uint32_t dtype, uint32_t heads) {
+    const uint64_t most = s.max_new < s.rows ? s.max_new : s.rows;
+    return dtype == QMV_BF16 && most * (heads / c.kv_heads) >= kManyCols;
+}
+
+Plan plan_many(const qmv_kv_cache& c, const qmv_kv_seqs& s, uint32_t heads, uint32_t window, uint32_t cols) {
+    const uint64_t group = heads / c.kv_heads;
+    const uint64_t most = s.max_new < s.rows ? s.max_new : s.rows;
+    uint64_t tiles = (most * group + cols - 1) / cols;
+    if (tiles > 65535) tiles = 65535;
+    if (tiles < 1) tiles = 1;
+    uint64_t span = s.max_len;
+    if (window != 0 && span > uint64_t{window} + cols) span = uint64_t{window} + cols;
+    const uint64_t pages = (span + kPage - 1) / kPage + 1;
+    const uint64_t wgs = uint64_t{s.seqs} * c.kv_heads * tiles;
+    uint64_t pieces = 256 / wgs;
+    if (pieces > pages / 8) pieces = pages / 8;
+    if (pieces > 64) pieces = 64;
+    if (pieces < 1) pieces = 1;
+    return Plan{static_cast<uint32_t>(tiles), static_cast<uint32_t>(pieces),
+                static_cast<uint32_t>((pages + pieces - 1) / pieces)};
+}
+
+template <int D, int NW>
+hipError_t go_many(const AttendArgs& a, const Plan& p, hipStream_t s) {
+    const dim3 grid(a.s.seqs * a.c.kv_heads, p.tiles, p.pieces), block(NW * 64);
+    constexpr uint32_t bytes = 2 * 2 * kPage * D * 2;    // keys and values, f16, twice
+    if (bytes > 65536) {
+        const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(attend_many_kernel<D, NW>),
+                                                 hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e != hipSuccess) return e;
+    }
+    hipLaunchKernelGGL((attend_many_kernel<D, NW>), grid, block, bytes, s, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || p.pieces == 1) return e;
+    const uint32_t joins = p.tiles * (32 * NW / 4) < 65535 ? p.tiles * (32 * NW / 4) : 65535;
+    hipLaunchKernelGGL((attend_join_kernel<QMV_BF16, D>), dim3(grid.x, joins), dim3(256), 0, s, a);
+    return hipGetLastError();
 }
 
 template <uint32_t DT, int D>
@@ -477,11 +861,15 @@ hipError_t go_few(const AttendArgs& a, const Plan& p, hipStream_t s) {
     return hipGetLastError();
 }
 
+Plan plan_of(const qmv_kv_cache& c, const qmv_kv_seqs& s, uint32_t dtype, uint32_t heads, uint32_t window) {
+    return is_many(c, s, dtype, heads) ? plan_many(c, s, heads, window, c.head_dim <= 128 ? 256 : 128) : plan_few(c, s, heads, window);
+}
+
 }  // namespace
 
-uint64_t kv_attend_workspace_bytes(const qmv_kv_cache& c, const qmv_kv_seqs& s, uint32_t, uint32_t heads,
+uint64_t kv_attend_workspace_bytes(const qmv_kv_cache& c, const qmv_kv_seqs& s, uint32_t dtype, uint32_t heads,
                                    uint32_t window) {
-    const Plan p = plan_few(c, s, heads, window);
+    const Plan p = plan_of(c, s, dtype, heads, window);
     if (p.pieces == 1) return 0;
     return uint64_t{p.pieces} * s.rows * heads * (c.head_dim + 2) * 4;  // outputs, then statistics
 }
@@ -489,11 +877,16 @@ uint64_t kv_attend_workspace_bytes(const qmv_kv_cache& c, const qmv_kv_seqs& s, 
 hipError_t launch_kv_attend(const qmv_kv_cache& c, const qmv_kv_seqs& s, uint32_t dtype, uint32_t heads,
                             float scale, uint32_t window, const void* q, void* out, void* workspace,
                             hipStream_t stream) {
-    const Plan p = plan_few(c, s, heads, window);
+    const Plan p = plan_of(c, s, dtype, heads, window);
     float* part = static_cast<float*>(workspace);
     const uint64_t outputs = uint64_t{p.pieces} * s.rows * heads * c.head_dim;
     const AttendArgs a{c, s, q, out, part, reinterpret_cast<float2*>(part + outputs), scale * kLog2e, heads,
                        heads / c.kv_heads, window, p.pieces, p.per};
+    if (is_many(c, s, dtype, heads)) {
+        if (c.head_dim == 64) return go_many<64, 8>(a, p, stream);
+        if (c.head_dim == 128) return go_many<128, 8>(a, p, stream);
+        return go_many<256, 4>(a, p, stream);
+    }
     if (dtype == QMV_F32) {
         if (c.head_dim == 64) return go_few<QMV_F32, 64>(a, p, stream);
         if (c.head_dim == 128) return go_few<QMV_F32, 128>(a, p, stream);
