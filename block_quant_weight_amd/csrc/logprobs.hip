@@ -7,18 +7,20 @@
 //
 // One pass over the logits, bound by their reading: a workgroup holds a
 // piece of the row in registers and leaves its maximum, S0 and S1 relative
-// to it, and for every group of four lanes the group's best element as one
-// 64-bit key (the value's order, then the lower index).  A second kernel, one
+// to it, and for every group of 128 elements (of 4 or 16 lanes) its best element as
+// one 64-bit key (the value's order, then the lower index).  A second kernel, one
 // workgroup a row, joins the pieces and finds the top n: the n groups with
 // the best keys hold the n best elements (an element outside them has n
 // better ones, the groups' own bests), so only their elements are read again.
+// Both searches list what reaches a bound that few pass, and place each listed
+// key by counting the larger ones.
 #include "device_common.h"
 #include "serve_kernels.h"
 
 namespace qmv {
 namespace {
 
-constexpr int kGroupLanes = 4;
+constexpr uint32_t kGroup = 128;   // elements of a group: 4 lanes' of 32, or 16 lanes' of 8
 constexpr int kMaxTop = 32;
 constexpr float kInf = __builtin_inff();
 
@@ -46,23 +48,6 @@ __device__ __forceinline__ uint64_t dpp_u64(uint64_t v) {
 }
 __device__ __forceinline__ uint64_t max64(uint64_t a, uint64_t b) { return a > b ? a : b; }
 
-__device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
-    v = max(v, dpp_u32<0xB1>(v));   // lanes 1 apart
-    v = max(v, dpp_u32<0x4E>(v));   // 2 apart
-    v = max(v, dpp_u32<0x141>(v));  // the other half of eight
-    v = max(v, dpp_u32<0x140>(v));  // the other half of sixteen
-    const uint32_t a = max(static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(v), 0)),
-                           static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(v), 16)));
-    const uint32_t b = max(static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(v), 32)),
-                           static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(v), 48)));
-    return max(a, b);
-}
-// The largest of the 64 lanes' keys, in every lane.
-__device__ __forceinline__ uint64_t wave_max_u64(uint64_t k) {
-    const uint32_t hi = static_cast<uint32_t>(k >> 32);
-    const uint32_t mh = wave_max_u32(hi);
-    return (static_cast<uint64_t>(mh) << 32) | wave_max_u32(hi == mh ? static_cast<uint32_t>(k) : 0u);
-}
 __device__ __forceinline__ float wave_max_f32(float v) {
     v = fmaxf(v, dpp_mov<0xB1>(v));
     v = fmaxf(v, dpp_mov<0x4E>(v));
@@ -117,7 +102,12 @@ __global__ __launch_bounds__(256) void logits_kernel(const float* __restrict__ x
             uint64_t k = i < vocab ? key_of(m, i) : 0;
             k = max64(k, dpp_u64<0xB1>(k));
             k = max64(k, dpp_u64<0x4E>(k));
-            if ((tid & 3) == 0) keys[g * (256 / kGroupLanes) + (tid >> 2)] = k;
+            if constexpr (E == 8) {
+                k = max64(k, dpp_u64<0x141>(k));
+                k = max64(k, dpp_u64<0x140>(k));
+            }
+            constexpr int kLanes = kGroup / E;
+            if (tid % kLanes == 0) keys[g * (256 / kLanes) + tid / kLanes] = k;
         }
         m = wave_max_f32(m);
         if ((tid & 63) == 0) red[0][wave] = m;
@@ -144,31 +134,70 @@ __global__ __launch_bounds__(256) void logits_kernel(const float* __restrict__ x
     }
 }
 
-// The wave's n largest of its lanes' R keys each, in order, to list.
+// The largest u with at least n of the set lanes' values >= u (0 if fewer
+// than n lanes are set), from the highest bit down.
+__device__ __forceinline__ uint32_t nth_u32(uint32_t v, bool set, uint32_t n) {
+    uint32_t u = 0;
+#pragma unroll 4
+    for (uint32_t bit = 0x80000000u; bit != 0; bit >>= 1)
+        u |= __builtin_popcountll(__ballot(set && v >= (u | bit))) >= static_cast<int>(n) ? bit : 0u;
+    return u;
+}
+// The n-th largest of the wave's 64 keys, 0 if fewer than n are not 0.
+__device__ __forceinline__ uint64_t wave_nth(uint64_t k, uint32_t n) {
+    const uint32_t hi = static_cast<uint32_t>(k >> 32);
+    const uint32_t h = nth_u32(hi, k != 0, n);
+    if (h == 0) return 0;   // (an element's order is never 0)
+    const uint32_t above = __builtin_popcountll(__ballot(hi > h)), with = __builtin_popcountll(__ballot(hi >= h));
+    // equal values: by their indexes
+    const uint32_t l = with == n ? 0 : nth_u32(static_cast<uint32_t>(k), hi == h, n - above);
+    return (static_cast<uint64_t>(h) << 32) | l;
+}
+
+constexpr uint32_t kList = 4096;   // candidates that a workgroup holds
+
+// Appends the wave's keys that are at least `from` (and not 0) to the list.
 template <int R>
-__device__ __forceinline__ void wave_top(uint64_t (&k)[R], uint32_t n, uint64_t* list) {
-    for (uint32_t i = 0; i < n; ++i) {
-        uint64_t b = k[0];
+__device__ __forceinline__ void collect(const uint64_t (&k)[R], uint64_t from, uint64_t* list, uint32_t* count) {
+    uint64_t take[R];
+    uint32_t all = 0;
 #pragma unroll
-        for (int r = 1; r < R; ++r) b = max64(b, k[r]);
-        b = wave_max_u64(b);
+    for (int r = 0; r < R; ++r) {
+        take[r] = __ballot(k[r] >= from && k[r] != 0);
+        all += __builtin_popcountll(take[r]);
+    }
+    if (all == 0) return;
+    uint32_t at = 0;
+    if ((threadIdx.x & 63) == 0) at = atomicAdd(count, all);
+    at = static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<int>(at)));
 #pragma unroll
-        for (int r = 0; r < R; ++r) k[r] = k[r] == b ? 0 : k[r];
-        if ((threadIdx.x & 63) == 0) list[i] = b;
+    for (int r = 0; r < R; ++r) {
+        if (take[r] == 0) continue;
+        const uint32_t before = __builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(take[r] >> 32),
+                                                          __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(take[r]), 0));
+        if ((take[r] >> (threadIdx.x & 63) & 1) != 0) list[at + before] = k[r];
+        at += __builtin_popcountll(take[r]);
     }
 }
 
-// The n largest of the four waves' lists (n in each, keys distinct but for
-// 0), in order, to best.  Ends with a barrier.
-__device__ __forceinline__ void join_top(const uint64_t (&lists)[4][kMaxTop], uint32_t n, uint64_t* best) {
+// The n largest of the list's keys (all distinct), in order, to best: every
+// key's place is the number of larger ones, whatever the list's order.  The
+// list is read eight keys at a time, zeros after its end.
+__device__ __forceinline__ void place(uint64_t* list, uint32_t count, uint32_t n, uint64_t* best) {
+    const uint32_t end = (count + 7) & ~7u;
+    if (threadIdx.x < end - count) list[count + threadIdx.x] = 0;
     __syncthreads();
-    const uint32_t tid = threadIdx.x;
-    if (tid < 4 * n) {
-        const uint64_t k = lists[tid / n][tid % n];
+    for (uint32_t i = threadIdx.x; i < count; i += 256) {
+        const uint64_t k = list[i];
         uint32_t rank = 0;
-        for (uint32_t w = 0; w < 4; ++w)
-            for (uint32_t i = 0; i < n; ++i) rank += lists[w][i] > k ? 1 : 0;
-        if (k != 0 && rank < n) best[rank] = k;
+        for (uint32_t j = 0; j < end; j += 8) {
+            uint64_t o[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) o[u] = list[j + u];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) rank += o[u] > k ? 1 : 0;
+        }
+        if (rank < n) best[rank] = k;
     }
     __syncthreads();
 }
@@ -177,14 +206,31 @@ template <int E>
 __global__ __launch_bounds__(256) void logprobs_kernel(LogprobArgs a, uint32_t pieces,
                                                        const Piece* __restrict__ stat,
                                                        const uint64_t* __restrict__ keys) {
-    constexpr int R = 16;                       // keys a thread takes at once
-    constexpr uint32_t kElems = kGroupLanes * E;  // elements of a group
+    constexpr int R = 8, RE = 10;                 // keys, elements a thread takes at once (20 groups: 10)
+    constexpr uint32_t kLanes = kGroup / E;       // lanes of a group
+    static_assert(4 * kMaxTop * R + kMaxTop <= kList && kMaxTop * kGroup <= kList, "candidates fit the list");
     __shared__ float red[3][4];
-    __shared__ uint64_t lists[4][kMaxTop];
-    __shared__ uint64_t groups[kMaxTop], best[kMaxTop];
+    __shared__ __attribute__((aligned(16))) uint64_t list[kList + 8];
+    __shared__ uint64_t groups[kMaxTop], best[kMaxTop], bound[4];
+    __shared__ uint32_t count;
     const uint64_t row = blockIdx.x;
     const uint32_t tid = threadIdx.x, wave = tid >> 6;
     const float* x = a.logits + row * a.vocab;
+    // the groups' keys are on the way while the sums are joined
+    const uint64_t* gk = keys + row * pieces * (256 / kLanes);
+    const uint32_t n_groups = pieces * (256 / kLanes);
+    uint64_t k[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const uint32_t i = r * 256 + tid;
+        k[r] = a.top != 0 && i < n_groups ? gk[i] : 0;
+    }
+    int32_t id = -1;
+    float xid = 0.f;
+    if (tid < a.n_ids) {
+        id = a.ids[row * a.n_ids + tid];
+        if (id >= 0 && static_cast<uint32_t>(id) < a.vocab) xid = x[id];
+    }
     // the row's maximum and sums
     const Piece* st = stat + row * pieces;
     float m = -kInf;
@@ -215,51 +261,68 @@ __global__ __launch_bounds__(256) void logprobs_kernel(LogprobArgs a, uint32_t p
     const float ln = s0 > 0.f ? logf(s0) : __builtin_nanf("");
     if (a.entropy != nullptr && tid == 0) a.entropy[row] = ln - s1 / s0;
     for (uint32_t i = tid; i < a.n_ids; i += 256) {
-        const int32_t id = a.ids[row * a.n_ids + i];
-        const bool in = id >= 0 && static_cast<uint32_t>(id) < a.vocab;
-        a.lp[row * a.n_ids + i] = in ? (x[id] - m) - ln : 0.f;
+        if (i >= 256) {
+            id = a.ids[row * a.n_ids + i];
+            if (id >= 0 && static_cast<uint32_t>(id) < a.vocab) xid = x[id];
+        }
+        a.lp[row * a.n_ids + i] = id >= 0 && static_cast<uint32_t>(id) < a.vocab ? (xid - m) - ln : 0.f;
     }
     if (a.top == 0) return;
 
-    // the n best groups, then the n best of their elements
-    const uint64_t* gk = keys + row * pieces * (256 / kGroupLanes);
-    const uint32_t n_groups = pieces * (256 / kGroupLanes);
+    // The n best groups.  Of each wave's lanes, the n with the best keys hold
+    // its n best, so the n-th of them is a bound that at least n keys reach
+    // and few others; the largest of the four waves' bounds is taken.  At most
+    // n lanes of a wave reach it, so at most 4 n R keys are listed.
     if (tid < kMaxTop) {
         groups[tid] = 0;
         best[tid] = 0;
     }
-    __syncthreads();
-    for (uint32_t base = 0; base < n_groups; base += 256 * R - kMaxTop) {
-        uint64_t k[R];
+    for (uint32_t base = 0; base < n_groups; base += 256 * R) {
+        uint64_t b = 0;
+        if (base != 0) {
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-            const uint32_t i = r * 256 + tid;    // the best so far come first
-            k[r] = i < kMaxTop ? groups[i] : (base + i - kMaxTop < n_groups ? gk[base + i - kMaxTop] : 0);
-        }
-        wave_top<R>(k, a.top, lists[wave]);
-        join_top(lists, a.top, groups);
-    }
-    const uint32_t all = a.top * kElems;
-    for (uint32_t base = 0; base < all; base += 256 * R - kMaxTop) {
-        uint64_t k[R];
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-            const uint32_t i = r * 256 + tid, j = base + i - kMaxTop;
-            k[r] = 0;
-            if (i < kMaxTop) {
-                k[r] = best[i];
-            } else if (j < all && groups[j / kElems] != 0) {
-                // the group of a best element: its piece and four lanes
-                const uint32_t e = 0xFFFFFFFFu - static_cast<uint32_t>(groups[j / kElems]);
-                const uint32_t piece = e / (256 * E), lane4 = (e % 1024) / (4 * kGroupLanes);
-                const uint32_t o = j % kElems;
-                const uint32_t index = piece * (256 * E) + (o / 16) * 1024 + lane4 * 16 + (o % 16);
-                if (index < a.vocab) k[r] = key_of(x[index], index);
+            for (int r = 0; r < R; ++r) {
+                const uint32_t i = base + r * 256 + tid;
+                k[r] = i < n_groups ? gk[i] : 0;
             }
         }
-        wave_top<R>(k, a.top, lists[wave]);
-        join_top(lists, a.top, best);
+#pragma unroll
+        for (int r = 0; r < R; ++r) b = max64(b, k[r]);
+        b = wave_nth(b, a.top);
+        if ((tid & 63) == 0) bound[wave] = b;
+        if (tid == 0) count = 0;
+        __syncthreads();
+        b = max64(max64(bound[0], bound[1]), max64(bound[2], bound[3]));
+        collect<R>(k, b, list, &count);
+        // the best of the batches before
+        if (base != 0 && tid < a.top && groups[tid] != 0) list[atomicAdd(&count, 1)] = groups[tid];
+        __syncthreads();
+        place(list, count, a.top, groups);
     }
+    // Their elements that reach the last of them.
+    const uint64_t last = groups[a.top - 1];
+    if (tid == 0) count = 0;
+    __syncthreads();
+    const uint32_t all = a.top * kGroup;
+    for (uint32_t base = 0; base < all; base += 256 * RE) {
+        uint64_t k[RE];
+#pragma unroll
+        for (int r = 0; r < RE; ++r) {
+            const uint32_t j = base + r * 256 + tid;
+            // the group of a best element: its piece and lanes
+            const uint64_t g = j < all ? groups[j / kGroup] : 0;
+            const uint32_t e = 0xFFFFFFFFu - static_cast<uint32_t>(g);
+            const uint32_t piece = e / (256 * E), lanes = (e % 1024) / (4 * kLanes);
+            const uint32_t o = j % kGroup;
+            const uint32_t index = piece * (256 * E) + (o / (4 * kLanes)) * 1024 + lanes * (4 * kLanes) + o % (4 * kLanes);
+            const bool there = g != 0 && index < a.vocab;
+            const float v = x[there ? index : 0];
+            k[r] = there ? key_of(v, index) : 0;
+        }
+        collect<RE>(k, last, list, &count);
+    }
+    __syncthreads();
+    place(list, count, a.top, best);
     if (tid < a.top) {
         const uint64_t k = best[tid];
         a.top_ids[row * a.top + tid] = static_cast<int32_t>(0xFFFFFFFFu - static_cast<uint32_t>(k));
@@ -278,7 +341,7 @@ int values(uint64_t rows, uint32_t vocab) {
 uint64_t logprobs_workspace_bytes(uint32_t rows, uint32_t vocab, uint32_t top) {
     const uint64_t per = 256ull * values(rows, vocab);
     const uint64_t pieces = (vocab + per - 1) / per * rows;
-    return pieces * sizeof(Piece) + (top != 0 ? pieces * (256 / kGroupLanes) * 8 : 0);
+    return pieces * sizeof(Piece) + (top != 0 ? pieces * per / kGroup * 8 : 0);
 }
 
 hipError_t launch_logprobs(const LogprobArgs& a, void* workspace, hipStream_t s) {
