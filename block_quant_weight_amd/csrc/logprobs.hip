@@ -7,7 +7,7 @@
 //
 // One pass over the logits, bound by their reading: a workgroup holds a
 // piece of the row in registers and leaves its maximum, S0 and S1 relative
-// to it, and for every group of 128 elements (of 4 or 16 lanes) its best element as
+// to it, and for every group of 128 elements (of 8 or 16 lanes) its best element as
 // one 64-bit key (the value's order, then the lower index).  A second kernel, one
 // workgroup a row, joins the pieces and finds the top n: the n groups with
 // the best keys hold the n best elements (an element outside them has n
@@ -20,7 +20,7 @@
 namespace qmv {
 namespace {
 
-constexpr uint32_t kGroup = 128;   // elements of a group: 4 lanes' of 32, or 16 lanes' of 8
+constexpr uint32_t kGroup = 128;   // elements of a group: 8 lanes' of 16, or 16 lanes' of 8
 constexpr int kMaxTop = 32;
 constexpr float kInf = __builtin_inff();
 
@@ -102,10 +102,8 @@ __global__ __launch_bounds__(256) void logits_kernel(const float* __restrict__ x
             uint64_t k = i < vocab ? key_of(m, i) : 0;
             k = max64(k, dpp_u64<0xB1>(k));
             k = max64(k, dpp_u64<0x4E>(k));
-            if constexpr (E == 8) {
-                k = max64(k, dpp_u64<0x141>(k));
-                k = max64(k, dpp_u64<0x140>(k));
-            }
+            if constexpr (E <= 16) k = max64(k, dpp_u64<0x141>(k));
+            if constexpr (E == 8) k = max64(k, dpp_u64<0x140>(k));
             constexpr int kLanes = kGroup / E;
             if (tid % kLanes == 0) keys[g * (256 / kLanes) + tid / kLanes] = k;
         }
@@ -330,10 +328,10 @@ __global__ __launch_bounds__(256) void logprobs_kernel(LogprobArgs a, uint32_t p
     }
 }
 
-// Values a thread of the first kernel holds: 32, or 8 where that would leave
-// compute units idle.
+// Values a thread of the first kernel holds: 16 (64 x 248320: 13.4 us, 32
+// 13.8, 8 14.9), or 8 where that would leave compute units idle.
 int values(uint64_t rows, uint32_t vocab) {
-    return rows * ((vocab + 8191) / 8192) >= 512 ? 32 : 8;
+    return rows * ((vocab + 4095) / 4096) >= 512 ? 16 : 8;
 }
 
 }  // namespace
@@ -352,14 +350,14 @@ hipError_t launch_logprobs(const LogprobArgs& a, void* workspace, hipStream_t s)
     Piece* stat = static_cast<Piece*>(workspace);
     uint64_t* keys = a.top != 0 ? reinterpret_cast<uint64_t*>(stat + total) : nullptr;
     const dim3 grid(static_cast<uint32_t>(total < 0x7FFFFFFFull ? total : 0x7FFFFFFFull)), block(256);
-    if (e == 32)
-        hipLaunchKernelGGL(logits_kernel<32>, grid, block, 0, s, a.logits, a.rows, a.vocab, pieces, stat, keys);
+    if (e == 16)
+        hipLaunchKernelGGL(logits_kernel<16>, grid, block, 0, s, a.logits, a.rows, a.vocab, pieces, stat, keys);
     else
         hipLaunchKernelGGL(logits_kernel<8>, grid, block, 0, s, a.logits, a.rows, a.vocab, pieces, stat, keys);
     const hipError_t err = hipGetLastError();
     if (err != hipSuccess) return err;
-    if (e == 32)
-        hipLaunchKernelGGL(logprobs_kernel<32>, dim3(a.rows), block, 0, s, a, pieces, stat, keys);
+    if (e == 16)
+        hipLaunchKernelGGL(logprobs_kernel<16>, dim3(a.rows), block, 0, s, a, pieces, stat, keys);
     else
         hipLaunchKernelGGL(logprobs_kernel<8>, dim3(a.rows), block, 0, s, a, pieces, stat, keys);
     return hipGetLastError();
