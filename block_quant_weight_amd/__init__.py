@@ -6,6 +6,3 @@ from .qmv import (EXPORTS, QMV_Q4_0, QMV_Q8_0, QmvError, QmvHandle,  # noqa: F40
                   qmv_block_dots, qmv_class_wtype, qmv_create, qmv_destroy,
                   qmv_embed_rows, qmv_gemm, qmv_gemv, qmv_gemv_group, qmv_quantize_q8,
                   qmv_span, qmv_status_str, qmv_upload)
-from .serve import (KvCache, KvSeqs, qmv_kv_attend, qmv_kv_attend_workspace,  # noqa: F401
-                    qmv_kv_read, qmv_kv_write, qmv_logprobs, qmv_logprobs_workspace,
-                    qmv_rms_norm)

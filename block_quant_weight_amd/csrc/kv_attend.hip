@@ -8,7 +8,7 @@
 // products.  The int8 matrix cores take the codes as they lie in the cache,
 // with no conversion and no shared memory; the other operand is split into
 // three signed base-256 digits:
-//   q = x 2^(E-22), x = rint(q 2^(22-E)) with |q| < 2^E the row's largest;
+//   q = x |q|max / (127 2^16), |q|max the row's largest magnitude;
 //   p = x / (127 2^16), p = e^{s - m} relative to its page's own maximum m.
 // A digit's products are exact int32 sums (at most 128 * 127 * 256 < 2^23, so
 // exact as float32 too), combined in float32.  Digits relative to the page's
@@ -213,8 +213,9 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attend_few_kernel(Atten
             const float amax = __builtin_bit_cast(float, m);
             int e = 0;
             const bool zero = m == 0 || m >= 0x7F800000u;
-            if (!zero) (void)frexpf(amax, &e);       // amax in [2^(e-1), 2^e)
-            qs = m >= 0x7F800000u ? __builtin_nanf("") : (zero ? 0.f : ldexpf(1.f, e - 6));  // 2^(e-22) 2^16
+            const float top = zero ? 1.f : frexpf(amax, &e);  // amax = top 2^e
+            const float mul = kPScale / top;
+            qs = m >= 0x7F800000u ? __builtin_nanf("") : (zero ? 0.f : ldexpf(top / 127.f, e));  // 2^16 / (mul 2^-e)
 #pragma unroll
             for (int s = 0; s < KS; ++s)
 #pragma unroll
@@ -222,7 +223,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attend_few_kernel(Atten
                     uint32_t x[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        x[i] = (zero ? 0 : static_cast<int>(rintf(ldexpf(v[s][4 * j + i], 22 - e)))) + 0x8080;
+                        x[i] = (zero ? 0 : static_cast<int>(rintf(ldexpf(v[s][4 * j + i], -e) * mul))) + 0x8080;
                     uint32_t d[3];
                     digits4(x, d);
 #pragma unroll

@@ -40,7 +40,7 @@ int check_kv(const qmv_kv_cache* c, const qmv_kv_seqs* s, uint32_t dtype) {
 }
 
 int check_heads(const qmv_kv_cache* c, const qmv_kv_seqs* s, uint32_t heads) {
-    if (heads == 0 || heads % c->kv_heads != 0) return QMV_E_SHAPE;
+    if (heads == 0 || heads % c->kv_heads != 0 || heads > kDimLimit) return QMV_E_SHAPE;
     return uint64_t{s->rows} * heads > 0x7FFF0000u ? QMV_E_SHAPE : QMV_OK;
 }
 

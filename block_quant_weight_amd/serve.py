@@ -7,8 +7,11 @@ from __future__ import annotations
 
 import ctypes
 
+import torch
+
 from . import qmv as _qmv
-from .qmv import QMV_E_ARG, QmvError, _check, _stream
+from .qmv import QMV_E_ARG, QmvError, _check
+from .qmv import _stream as _stream_of
 
 QMV_F32 = 0
 QMV_BF16 = 1
@@ -59,9 +62,23 @@ def lib():
     return _lib
 
 
+_device = torch.cuda.current_device
+# The current stream's handle without a Stream object around it (0.1 us, not
+# 3); a torch without it takes the long way.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream(stream):
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(_device())
+    return _stream_of(stream)
+
+
 def _dev(t, dtype, numel, what):
     """Address of a contiguous tensor of the current GPU with at least numel elements."""
-    import torch
+    if (t.dtype is dtype and t.is_cuda and t.is_contiguous() and t.numel() >= numel
+            and t.get_device() == _device()):
+        return t.data_ptr()
     if not t.is_cuda:
         raise ValueError(f"{what} must be a GPU tensor")
     if t.dtype != dtype:
@@ -70,14 +87,11 @@ def _dev(t, dtype, numel, what):
         raise ValueError(f"{what} must be contiguous")
     if t.numel() < numel:
         raise ValueError(f"{what} holds {t.numel()} elements, needs {numel}")
-    if t.get_device() != torch.cuda.current_device():
-        raise ValueError(f"{what} is not on the current device")
-    return t.data_ptr()
+    raise ValueError(f"{what} is not on the current device")
 
 
 def _dtype(t, what):
     """QMV_F32 or QMV_BF16 of a tensor."""
-    import torch
     if t.dtype == torch.float32:
         return QMV_F32
     if t.dtype == torch.bfloat16:
@@ -87,7 +101,6 @@ def _dtype(t, what):
 
 def workspace(nbytes, device="cuda"):
     """A scratch tensor of nbytes for the calls that take one (never empty)."""
-    import torch
     return torch.empty(max(int(nbytes), 16), dtype=torch.uint8, device=device)
 
 
@@ -97,7 +110,6 @@ class KvCache:
     float32 [pages, kv_heads].  KvCache.empty allocates them."""
 
     def __init__(self, k, v, k_scale, v_scale):
-        import torch
         if k.dim() != 4 or k.shape[2] != QMV_KV_PAGE:
             raise ValueError("k must be [pages, kv_heads, 64, head_dim]")
         self.pages, self.kv_heads, _, self.head_dim = k.shape
@@ -115,7 +127,6 @@ class KvCache:
 
     @classmethod
     def empty(cls, pages, kv_heads, head_dim, device="cuda"):
-        import torch
         return cls(torch.empty(pages, kv_heads, QMV_KV_PAGE, head_dim, dtype=torch.int8, device=device),
                    torch.empty(pages, kv_heads, head_dim, QMV_KV_PAGE, dtype=torch.int8, device=device),
                    torch.empty(pages, kv_heads, dtype=torch.float32, device=device),
@@ -130,7 +141,6 @@ class KvSeqs:
     the launch only.  One object serves all layers of a step."""
 
     def __init__(self, table, len, start, max_new, max_len):
-        import torch
         if table.dim() != 2:
             raise ValueError("table must be [seqs, table_stride]")
         self.seqs = table.shape[0]
@@ -154,7 +164,6 @@ def qmv_rms_norm(x, w, eps, res=None, sum=None, y=None, q=None, d=None, stream=N
     """x, res, sum: float32 [rows, cols]; w: float32 [cols]; y: float32 or
     bfloat16 [rows, cols]; q int8 [rows, cols] with d float32 [rows, cols/32].
     Outputs that are None are not computed; sum may be res or x."""
-    import torch
     if x.dim() != 2:
         raise ValueError("x must be [rows, cols]")
     rows, cols = x.shape
@@ -212,7 +221,6 @@ def qmv_kv_attend(cache: KvCache, seqs: KvSeqs, q, out, scale=None, window=0, wo
     head_dim ** -0.5.  workspace: a uint8 GPU tensor of at least
     qmv_kv_attend_workspace bytes; None allocates one, for use on the current
     stream."""
-    import torch
     dt = _dtype(q, "q")
     if q.dim() != 3:
         raise ValueError("q must be [rows, heads, head_dim]")
@@ -243,7 +251,6 @@ def qmv_logprobs(logits, ids=None, lp=None, entropy=None, top_ids=None, top_lp=N
     """logits: float32 [rows, vocab]; ids int32 and lp float32 [rows, n];
     entropy float32 [rows]; top_ids int32 and top_lp float32 [rows, top].
     workspace as for qmv_kv_attend."""
-    import torch
     if logits.dim() != 2:
         raise ValueError("logits must be [rows, vocab]")
     rows, vocab = logits.shape
