@@ -50,6 +50,11 @@ __device__ __forceinline__ float dpp_mov(float v) {
         float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), CTRL, 0xF, 0xF, true));
 }
 
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp_u32(uint32_t v) {
+    return static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(v), CTRL, 0xF, 0xF, true));
+}
+
 __device__ __forceinline__ float read_lane(float v, int lane) {
     return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), lane));
 }
@@ -63,6 +68,19 @@ __device__ __forceinline__ float wave_reduce(float v) {
     v += dpp_mov<0x124>(v);  // row_ror:4
     v += dpp_mov<0x128>(v);  // row_ror:8
     return (read_lane(v, 0) + read_lane(v, 16)) + (read_lane(v, 32) + read_lane(v, 48));
+}
+
+// The largest over the 64 lanes of a wavefront, in every lane.
+__device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
+    v = max(v, dpp_u32<0xB1>(v));   // lanes 1 apart
+    v = max(v, dpp_u32<0x4E>(v));   // 2 apart
+    v = max(v, dpp_u32<0x141>(v));  // half rows mirrored: the other four of eight
+    v = max(v, dpp_u32<0x140>(v));  // rows mirrored: the other eight of sixteen
+    const uint32_t a = max(static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(v), 0)),
+                           static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(v), 16)));
+    const uint32_t b = max(static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(v), 32)),
+                           static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(v), 48)));
+    return max(a, b);
 }
 
 }  // namespace qmv

@@ -15,9 +15,11 @@
 // One workgroup owns (page, head, keys or values): it finds amax of the new
 // tokens, settles the scale, rescales the earlier tokens where the scale
 // grew, and writes the new codes, so nothing is shared between workgroups
-// and the result does not depend on their order.  Values are turned through
-// shared memory, whose rows of 64 tokens are 68 bytes apart (17 words: odd,
-// so that neighbouring dims fall into different banks).
+// and the result does not depend on their order.  A thread has 4 tokens x 8
+// dims: rows are read and written in whole lines, and the values' codes are
+// turned 4 x 4 in registers (two byte permutations a word) on their way
+// through shared memory, whose rows of 64 tokens are 68 bytes apart (17
+// words: odd, so that neighbouring dims fall into different banks).
 #include "kv_common.h"
 
 namespace qmv {
@@ -39,11 +41,18 @@ __device__ __forceinline__ float scale_for(uint32_t amax_bits) {
     return __builtin_bit_cast(float, static_cast<uint32_t>(e + 127) << 23);
 }
 
-// x / d to the nearest whole number, in -127 .. 127; 0 where d is 0 or NaN.
-__device__ __forceinline__ uint32_t code(float x, float inv, bool none) {
-    if (none) return 0;
-    const float r = fminf(fmaxf(rintf(x * inv), -127.f), 127.f);
-    return static_cast<uint32_t>(static_cast<int>(r)) & 0xFFu;
+// Codes of four values: x / d to the nearest whole number, in -127 .. 127.
+// Added to 1.5 2^23, the whole number is the sum's low bits (the quotient
+// by a power of two is exact, so the sum rounds once).
+__device__ __forceinline__ uint32_t code4(const float* x, float inv) {
+    constexpr float kMagic = 12582912.f;
+    uint32_t u[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        u[j] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_fmed3f(fmaf(x[j], inv, kMagic), kMagic - 127.f, kMagic + 127.f));
+    const uint32_t a = __builtin_amdgcn_perm(u[1], u[0], 0x00000400u);
+    const uint32_t b = __builtin_amdgcn_perm(u[3], u[2], 0x04000000u);
+    return __builtin_amdgcn_perm(b, a, 0x07060100u);
 }
 
 // Four codes rescaled by old / new.
@@ -58,58 +67,94 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t w, float ratio) {
     return o;
 }
 
+// Four words of four bytes turned: byte i of out[b] is byte b of in[i].
+__device__ __forceinline__ void turn4(const uint32_t in[4], uint32_t out[4]) {
+    const uint32_t a = __builtin_amdgcn_perm(in[1], in[0], 0x05010400u);
+    const uint32_t b = __builtin_amdgcn_perm(in[3], in[2], 0x05010400u);
+    const uint32_t c = __builtin_amdgcn_perm(in[1], in[0], 0x07030602u);
+    const uint32_t d = __builtin_amdgcn_perm(in[3], in[2], 0x07030602u);
+    out[0] = __builtin_amdgcn_perm(b, a, 0x05040100u);
+    out[1] = __builtin_amdgcn_perm(b, a, 0x07060302u);
+    out[2] = __builtin_amdgcn_perm(d, c, 0x05040100u);
+    out[3] = __builtin_amdgcn_perm(d, c, 0x07060302u);
+}
+
+// Threads of a workgroup, and pieces of 4 tokens x 8 dims each has.
+template <int D>
+struct Shape {
+    static constexpr int NT = D == 64 ? 128 : 256;
+    static constexpr int PER = 2 * D / NT;
+};
+
+template <int NT>
 __device__ __forceinline__ uint32_t wg_max(uint32_t v, uint32_t* lds) {
-#pragma unroll
-    for (int m = 1; m < 64; m <<= 1) v = max(v, static_cast<uint32_t>(__shfl_xor(static_cast<int>(v), m)));
+    v = wave_max_u32(v);
     if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
     __syncthreads();
-    return max(max(lds[0], lds[1]), max(lds[2], lds[3]));
+    v = lds[0];
+#pragma unroll
+    for (int w = 1; w < NT / 64; ++w) v = max(v, lds[w]);
+    return v;
 }
 
 // grid: x = sequence * kv_heads + head, y = the sequence's touched pages
 // (strided), z = 0 keys, 1 values.
 template <uint32_t DT, int D>
-__global__ __launch_bounds__(256) void kv_write_kernel(qmv_kv_cache c, qmv_kv_seqs s,
-                                                       const typename Elem<DT>::type* __restrict__ k,
-                                                       const typename Elem<DT>::type* __restrict__ v) {
-    constexpr int CPT = D / 8;                    // chunks of 8 values a token
-    constexpr int PER = kPage * CPT / 256;        // chunks a thread
-    __shared__ uint32_t red[4];
+__global__ __launch_bounds__(Shape<D>::NT) void kv_write_kernel(qmv_kv_cache c, qmv_kv_seqs s,
+                                                                const typename Elem<DT>::type* __restrict__ k,
+                                                                const typename Elem<DT>::type* __restrict__ v) {
+    constexpr int NT = Shape<D>::NT, PER = Shape<D>::PER, CPT = D / 8;
+    __shared__ uint32_t red[NT / 64];
     __shared__ __attribute__((aligned(16))) uint8_t turn[D * kPitch];
     const uint32_t seq = blockIdx.x / c.kv_heads, head = blockIdx.x % c.kv_heads;
     const bool values = blockIdx.z != 0;
     const int tid = threadIdx.x;
     const SeqRows r = seq_rows(s, seq);
     if (r.count == 0 || r.len == 0) return;
-    const int32_t from = max(r.base, 0);               // first new position
+    const int32_t from = max(r.base, 0);                        // first new position
     const int32_t last = (r.len - 1) / kPage;
     const typename Elem<DT>::type* src = values ? v : k;
     for (int32_t p = from / kPage + blockIdx.y; p <= last; p += gridDim.y) {
-        const int32_t id = page_id(c, s, seq, p);
-        if (id < 0) continue;
         const int lo = max(from - p * kPage, 0);
         const int hi = min(r.len - p * kPage, kPage);
         const int32_t row0 = r.first + (p * kPage - r.base);      // row of the page's token 0
-        float x[PER][8];
-        uint32_t m = 0;
+        // the rows and the page's id are on the way together
+        float x[PER][4][8];
 #pragma unroll
         for (int u = 0; u < PER; ++u) {
-            const int ch = tid + 256 * u, t = ch / CPT, dim = (ch % CPT) * 8;
-            if (t >= lo && t < hi) {
-                load8<DT>(src + (static_cast<uint64_t>(row0 + t) * c.kv_heads + head) * D + dim, x[u]);
-            } else {
+            const int ch = tid + NT * u, t = ch / CPT * 4, dim = ch % CPT * 8;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) x[u][j] = 0.f;
+            for (int i = 0; i < 4; ++i) {
+                if (t + i >= lo && t + i < hi) {
+                    load8<DT>(src + (static_cast<uint64_t>(row0 + t + i) * c.kv_heads + head) * D + dim, x[u][i]);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) x[u][i][j] = 0.f;
+                }
             }
         }
-#pragma unroll
-        for (int u = 0; u < PER; ++u)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) m = max(m, __builtin_bit_cast(uint32_t, x[u][j]) & 0x7FFFFFFFu);
-        m = wg_max(m, red);
+        const int32_t id = page_id(c, s, seq, p);
+        if (id < 0) continue;
         const uint64_t at = static_cast<uint64_t>(id) * c.kv_heads + head;
         float* sp = (values ? c.v_scale : c.k_scale) + at;
         const float old = lo == 0 ? 0.f : *sp;
+        uint8_t* page = reinterpret_cast<uint8_t*>(values ? c.v : c.k) + at * (kPage * D);
+        // values: words of four tokens that hold earlier tokens or later
+        // places beside new ones, the first and the last that are written
+        uint32_t was[2] = {0, 0};
+        if (values && tid < D) {
+            const uint32_t* q = reinterpret_cast<const uint32_t*>(page + tid * kPage);
+            if ((lo & 3) != 0) was[0] = q[lo >> 2];
+            if ((hi & 3) != 0) was[1] = q[hi >> 2];
+        }
+        uint32_t m = 0;
+#pragma unroll
+        for (int u = 0; u < PER; ++u)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) m = max(m, __builtin_bit_cast(uint32_t, x[u][i][j]) & 0x7FFFFFFFu);
+        m = wg_max<NT>(m, red);
         const float need = scale_for(m);
         // a NaN, of now or of before, stays
         const float d = need != need ? need : (old != old ? old : fmaxf(old, need));
@@ -119,51 +164,61 @@ __global__ __launch_bounds__(256) void kv_write_kernel(qmv_kv_cache c, qmv_kv_se
         const float inv = none ? 0.f : 1.f / d;
         __syncthreads();                          // every thread has read the old scale and `red`
         if (tid == 0) *sp = d;
-        uint8_t* page = reinterpret_cast<uint8_t*>(values ? c.v : c.k) + at * (kPage * D);
-        if (!values) {
 #pragma unroll
-            for (int u = 0; u < PER; ++u) {
-                const int ch = tid + 256 * u, t = ch / CPT, dim = (ch % CPT) * 8;
-                uint2* q = reinterpret_cast<uint2*>(page + t * D + dim);
-                if (t >= lo && t < hi) {
-                    uint32_t w[2] = {0, 0};
+        for (int u = 0; u < PER; ++u) {
+            const int ch = tid + NT * u, t = ch / CPT * 4, dim = ch % CPT * 8;
+            uint32_t w[2][4];                     // codes of dims 0 .. 3, 4 .. 7 of each token
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) w[j >> 2] |= code(x[u][j], inv, none) << (8 * (j & 3));
-                    *q = make_uint2(w[0], w[1]);
-                } else if (grew && t < lo) {
-                    const uint2 w = *q;
-                    *q = make_uint2(rescale4(w.x, ratio), rescale4(w.y, ratio));
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    w[h][i] = none ? 0u : code4(&x[u][i][4 * h], inv);
                 }
-            }
-        } else {
+            if (!values) {
 #pragma unroll
-            for (int u = 0; u < PER; ++u) {
-                const int ch = tid + 256 * u, t = ch / CPT, dim = (ch % CPT) * 8;
-                if (t >= lo && t < hi) {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        turn[(dim + j) * kPitch + t] = static_cast<uint8_t>(code(x[u][j], inv, none));
-                }
-            }
-            __syncthreads();
-            for (int i = tid; i < D * (kPage / 4); i += 256) {
-                const int dim = i / (kPage / 4), t = (i % (kPage / 4)) * 4;  // tokens t .. t + 3
-                if (t >= hi || (t + 4 <= lo && !grew)) continue;
-                uint32_t* q = reinterpret_cast<uint32_t*>(page + dim * kPage + t);
-                uint32_t fresh = *reinterpret_cast<const uint32_t*>(&turn[dim * kPitch + t]);
-                if (t < lo || t + 4 > hi) {
-                    // bytes of earlier tokens (rescaled) and of later places (kept)
-                    const uint32_t was = *q;
-                    const uint32_t early = grew ? rescale4(was, ratio) : was;
-                    uint32_t w = 0;
-#pragma unroll
-                    for (int b = 0; b < 4; ++b) {
-                        const uint32_t pick = t + b < lo ? early : (t + b < hi ? fresh : was);
-                        w |= pick & (0xFFu << (8 * b));
+                for (int i = 0; i < 4; ++i) {
+                    uint2* q = reinterpret_cast<uint2*>(page + (t + i) * D + dim);
+                    if (t + i >= lo && t + i < hi) {
+                        *q = make_uint2(w[0][i], w[1][i]);
+                    } else if (grew && t + i < lo) {
+                        const uint2 o = *q;
+                        *q = make_uint2(rescale4(o.x, ratio), rescale4(o.y, ratio));
                     }
-                    fresh = w;
                 }
-                *q = fresh;
+            } else if (t < hi && t + 4 > lo) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t o[4];
+                    turn4(w[h], o);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        *reinterpret_cast<uint32_t*>(&turn[(dim + 4 * h + j) * kPitch + t]) = o[j];
+                }
+            }
+        }
+        if (values) {
+            __syncthreads();
+            // whole words of new tokens, and of earlier ones if they change
+            const int w_lo = (lo + 3) >> 2, w_hi = hi >> 2, w_from = grew ? 0 : w_lo;
+            for (int i = tid; i < D * (kPage / 4); i += NT) {
+                const int dim = i / (kPage / 4), w = i % (kPage / 4);
+                uint32_t* q = reinterpret_cast<uint32_t*>(page + dim * kPage) + w;
+                if (w >= w_lo && w < w_hi) *q = *reinterpret_cast<const uint32_t*>(&turn[dim * kPitch + 4 * w]);
+                else if (w >= w_from && w < lo >> 2) *q = rescale4(*q, ratio);
+            }
+            // words that hold both, and later places, which stay
+            if (tid < D) {
+                uint32_t* q = reinterpret_cast<uint32_t*>(page + tid * kPage);
+                const uint32_t* n = reinterpret_cast<const uint32_t*>(&turn[tid * kPitch]);
+                const uint32_t early = grew ? rescale4(was[0], ratio) : was[0];
+                // bytes below lo, and from hi on
+                const uint32_t below = (1u << (8 * (lo & 3))) - 1, above = ~((1u << (8 * (hi & 3))) - 1);
+                if ((lo & 3) != 0 && lo >> 2 == hi >> 2) {   // (hi is then no multiple of 4)
+                    q[lo >> 2] = (early & below) | (n[lo >> 2] & ~below & ~above) | (was[1] & above);
+                } else {
+                    if ((lo & 3) != 0) q[lo >> 2] = (early & below) | (n[lo >> 2] & ~below);
+                    if ((hi & 3) != 0) q[hi >> 2] = (n[hi >> 2] & ~above) | (was[1] & above);
+                }
             }
             __syncthreads();                      // `turn` is used again
         }
@@ -171,11 +226,10 @@ __global__ __launch_bounds__(256) void kv_write_kernel(qmv_kv_cache c, qmv_kv_se
 }
 
 template <uint32_t DT, int D>
-__global__ __launch_bounds__(256) void kv_read_kernel(qmv_kv_cache c, qmv_kv_seqs s,
-                                                      typename Elem<DT>::type* __restrict__ k,
-                                                      typename Elem<DT>::type* __restrict__ v) {
-    constexpr int CPT = D / 8;
-    constexpr int PER = kPage * CPT / 256;
+__global__ __launch_bounds__(Shape<D>::NT) void kv_read_kernel(qmv_kv_cache c, qmv_kv_seqs s,
+                                                               typename Elem<DT>::type* __restrict__ k,
+                                                               typename Elem<DT>::type* __restrict__ v) {
+    constexpr int NT = Shape<D>::NT, PER = Shape<D>::PER, CPT = D / 8;
     __shared__ __attribute__((aligned(16))) uint8_t turn[D * kPitch];
     const uint32_t seq = blockIdx.x / c.kv_heads, head = blockIdx.x % c.kv_heads;
     const bool values = blockIdx.z != 0;
@@ -193,36 +247,50 @@ __global__ __launch_bounds__(256) void kv_read_kernel(qmv_kv_cache c, qmv_kv_seq
         const int lo = max(r.base - p * kPage, 0);
         const int hi = min(r.len - p * kPage, kPage);
         const int32_t row0 = r.first + (p * kPage - r.base);
-        const uint64_t at = static_cast<uint64_t>(id < 0 ? 0 : id) * c.kv_heads + head;
+        // (without a page: page 0 times 0)
+        const uint64_t at = static_cast<uint64_t>(max(id, 0)) * c.kv_heads + head;
         const float d = id < 0 ? 0.f : (values ? c.v_scale : c.k_scale)[at];
         const uint8_t* page = reinterpret_cast<const uint8_t*>(values ? c.v : c.k) + at * (kPage * D);
-        if (values && id >= 0) {
-            for (int i = tid; i < D * (kPage / 4); i += 256) {
-                const int dim = i / (kPage / 4), t = (i % (kPage / 4)) * 4;
-                *reinterpret_cast<uint32_t*>(&turn[dim * kPitch + t]) =
-                    *reinterpret_cast<const uint32_t*>(page + dim * kPage + t);
+        if (values) {
+            for (int i = tid; i < D * (kPage / 16); i += NT) {
+                const int dim = i / (kPage / 16), t = (i % (kPage / 16)) * 16;
+                const uint4 w = *reinterpret_cast<const uint4*>(page + dim * kPage + t);
+                uint32_t* o = reinterpret_cast<uint32_t*>(&turn[dim * kPitch + t]);
+                o[0] = w.x; o[1] = w.y; o[2] = w.z; o[3] = w.w;
             }
             __syncthreads();
         }
 #pragma unroll
         for (int u = 0; u < PER; ++u) {
-            const int ch = tid + 256 * u, t = ch / CPT, dim = (ch % CPT) * 8;
-            if (t < lo || t >= hi) continue;
-            float o[8];
-            if (id < 0) {
+            const int ch = tid + NT * u, t = ch / CPT * 4, dim = ch % CPT * 8;
+            if (t >= hi || t + 4 <= lo) continue;
+            uint32_t w[2][4];
+            if (!values) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) o[j] = 0.f;
-            } else if (!values) {
-                const uint2 w = *reinterpret_cast<const uint2*>(page + t * D + dim);
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    o[j] = static_cast<float>(static_cast<int8_t>((j < 4 ? w.x : w.y) >> (8 * (j & 3)))) * d;
+                for (int i = 0; i < 4; ++i) {
+                    const uint2 o = *reinterpret_cast<const uint2*>(page + (t + i) * D + dim);
+                    w[0][i] = o.x;
+                    w[1][i] = o.y;
+                }
             } else {
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    o[j] = static_cast<float>(static_cast<int8_t>(turn[(dim + j) * kPitch + t])) * d;
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t o[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        o[j] = *reinterpret_cast<const uint32_t*>(&turn[(dim + 4 * h + j) * kPitch + t]);
+                    turn4(o, w[h]);
+                }
             }
-            store8<DT>(dst + (static_cast<uint64_t>(row0 + t) * c.kv_heads + head) * D + dim, o);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (t + i < lo || t + i >= hi) continue;
+                float o[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    o[j] = id < 0 ? 0.f : static_cast<float>(static_cast<int8_t>(w[j >> 2][i] >> (8 * (j & 3)))) * d;
+                store8<DT>(dst + (static_cast<uint64_t>(row0 + t + i) * c.kv_heads + head) * D + dim, o);
+            }
         }
         if (values) __syncthreads();
     }
@@ -239,7 +307,7 @@ uint32_t pages_hint(const qmv_kv_seqs& s) {
 
 hipError_t launch_kv_write(const qmv_kv_cache& c, const qmv_kv_seqs& s, uint32_t dtype, const void* k,
                            const void* v, hipStream_t stream) {
-    const dim3 grid(s.seqs * c.kv_heads, pages_hint(s), 2), block(256);
+    const dim3 grid(s.seqs * c.kv_heads, pages_hint(s), 2), block(c.head_dim == 64 ? 128 : 256);
 #define QMV_KV_GO(DT, D)                                                                             \
     hipLaunchKernelGGL((kv_write_kernel<DT, D>), grid, block, 0, stream, c, s,                       \
                        static_cast<const Elem<DT>::type*>(k), static_cast<const Elem<DT>::type*>(v))
@@ -258,7 +326,7 @@ hipError_t launch_kv_write(const qmv_kv_cache& c, const qmv_kv_seqs& s, uint32_t
 
 hipError_t launch_kv_read(const qmv_kv_cache& c, const qmv_kv_seqs& s, uint32_t dtype, void* k, void* v,
                           hipStream_t stream) {
-    const dim3 grid(s.seqs * c.kv_heads, pages_hint(s), 2), block(256);
+    const dim3 grid(s.seqs * c.kv_heads, pages_hint(s), 2), block(c.head_dim == 64 ? 128 : 256);
 #define QMV_KV_GO(DT, D)                                                                             \
     hipLaunchKernelGGL((kv_read_kernel<DT, D>), grid, block, 0, stream, c, s,                        \
                        static_cast<Elem<DT>::type*>(k), static_cast<Elem<DT>::type*>(v))

@@ -38,10 +38,6 @@ __device__ __forceinline__ uint64_t key_of(float x, uint32_t index) {
 }
 
 template <int CTRL>
-__device__ __forceinline__ uint32_t dpp_u32(uint32_t v) {
-    return static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(v), CTRL, 0xF, 0xF, true));
-}
-template <int CTRL>
 __device__ __forceinline__ uint64_t dpp_u64(uint64_t v) {
     return (static_cast<uint64_t>(dpp_u32<CTRL>(static_cast<uint32_t>(v >> 32))) << 32) |
            dpp_u32<CTRL>(static_cast<uint32_t>(v));
