@@ -97,6 +97,55 @@ __device__ __forceinline__ uint32_t wg_max(uint32_t v, uint32_t* lds) {
     return v;
 }
 
+// Eight values as they come: their largest magnitude (as float bits), and
+// their codes.  bfloat16 stays packed until its codes are made.
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+template <uint32_t DT>
+struct Eight;
+template <>
+struct Eight<QMV_F32> {
+    float v[8];
+    __device__ __forceinline__ void load(const float* p) { load8<QMV_F32>(p, v); }
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = 0.f;
+    }
+    typedef uint32_t Max;
+    __device__ __forceinline__ void most(Max& m) const {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) m = max(m, __builtin_bit_cast(uint32_t, v[j]) & 0x7FFFFFFFu);
+    }
+    static __device__ __forceinline__ uint32_t bits(Max m) { return m; }
+    __device__ __forceinline__ uint32_t codes(int h, float inv) const { return code4(v + 4 * h, inv); }
+};
+template <>
+struct Eight<QMV_BF16> {
+    uint32_t w[4];
+    __device__ __forceinline__ void load(const uint16_t* p) {
+        const uint4 t = *reinterpret_cast<const uint4*>(p);
+        w[0] = t.x; w[1] = t.y; w[2] = t.z; w[3] = t.w;
+    }
+    __device__ __forceinline__ void clear() { w[0] = w[1] = w[2] = w[3] = 0; }
+    typedef u16x2 Max;
+    __device__ __forceinline__ void most(Max& m) const {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, w[j] & 0x7FFF7FFFu));
+    }
+    static __device__ __forceinline__ uint32_t bits(Max m) {
+        const uint32_t a = m[0], b = m[1];
+        return max(a, b) << 16;
+    }
+    __device__ __forceinline__ uint32_t codes(int h, float inv) const {
+        float v[4];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            v[2 * j] = __builtin_bit_cast(float, w[2 * h + j] << 16);
+            v[2 * j + 1] = __builtin_bit_cast(float, w[2 * h + j] & 0xFFFF0000u);
+        }
+        return code4(v, inv);
+    }
+};
+
 // grid: x = sequence * kv_heads + head, y = the sequence's touched pages
 // (strided), z = 0 keys, 1 values.
 template <uint32_t DT, int D>
@@ -119,18 +168,15 @@ __global__ __launch_bounds__(Shape<D>::NT) void kv_write_kernel(qmv_kv_cache c, 
         const int hi = min(r.len - p * kPage, kPage);
         const int32_t row0 = r.first + (p * kPage - r.base);      // row of the page's token 0
         // the rows and the page's id are on the way together
-        float x[PER][4][8];
+        Eight<DT> x[PER][4];
 #pragma unroll
         for (int u = 0; u < PER; ++u) {
             const int ch = tid + NT * u, t = ch / CPT * 4, dim = ch % CPT * 8;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                if (t + i >= lo && t + i < hi) {
-                    load8<DT>(src + (static_cast<uint64_t>(row0 + t + i) * c.kv_heads + head) * D + dim, x[u][i]);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) x[u][i][j] = 0.f;
-                }
+                x[u][i].clear();
+                if (t + i >= lo && t + i < hi)
+                    x[u][i].load(src + (static_cast<uint64_t>(row0 + t + i) * c.kv_heads + head) * D + dim);
             }
         }
         const int32_t id = page_id(c, s, seq, p);
@@ -147,14 +193,12 @@ __global__ __launch_bounds__(Shape<D>::NT) void kv_write_kernel(qmv_kv_cache c, 
             if ((lo & 3) != 0) was[0] = q[lo >> 2];
             if ((hi & 3) != 0) was[1] = q[hi >> 2];
         }
-        uint32_t m = 0;
+        typename Eight<DT>::Max most = {};
 #pragma unroll
         for (int u = 0; u < PER; ++u)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 8; ++j) m = max(m, __builtin_bit_cast(uint32_t, x[u][i][j]) & 0x7FFFFFFFu);
-        m = wg_max<NT>(m, red);
+            for (int i = 0; i < 4; ++i) x[u][i].most(most);
+        const uint32_t m = wg_max<NT>(Eight<DT>::bits(most), red);
         const float need = scale_for(m);
         // a NaN, of now or of before, stays
         const float d = need != need ? need : (old != old ? old : fmaxf(old, need));
@@ -172,7 +216,7 @@ __global__ __launch_bounds__(Shape<D>::NT) void kv_write_kernel(qmv_kv_cache c, 
             for (int i = 0; i < 4; ++i)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    w[h][i] = none ? 0u : code4(&x[u][i][4 * h], inv);
+                    w[h][i] = none ? 0u : x[u][i].codes(h, inv);
                 }
             if (!values) {
 #pragma unroll
