@@ -62,7 +62,7 @@ int qmv_rms_norm(const float* x, const float* res, const float* w, float eps, ui
         if (!aligned(p, 16)) return QMV_E_ARG;
     if (cols == 0 || cols % 32 != 0 || cols > kDimLimit) return QMV_E_SHAPE;
     (void)hipGetLastError();
-    const qmv::NormArgs a{x, res, w, sum, y, y_bf16, q, d, rows, cols, eps};
+    const qmv::NormArgs a{x, res, w, sum, y, y_bf16, q, d, rows, cols, eps, 1.0 / cols};
     return enqueue(qmv::launch_rms_norm(a, static_cast<hipStream_t>(stream)));
 }
 

@@ -19,6 +19,7 @@ struct NormArgs {
     float* d;
     uint32_t rows, cols;
     float eps;
+    double inv_cols;    // 1 / cols
 };
 hipError_t launch_rms_norm(const NormArgs& a, hipStream_t stream);
 
