@@ -526,12 +526,12 @@ __global__ __launch_bounds__(NW * 64, NW / 4) void attend_many_kernel(AttendArgs
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const float x = __builtin_bit_cast(float, u[i] << 16), y = __builtin_bit_cast(float, u[i] & 0xFFFF0000u);
-                    qf[s][2 * i] = static_cast<_Float16>(zero ? 0.f : ldexpf(x, 15 - e));
-                    qf[s][2 * i + 1] = static_cast<_Float16>(zero ? 0.f : ldexpf(y, 15 - e));
+                    qf[s][2 * i] = static_cast<_Float16>(zero ? 0.f : ldexpf(a.scale_log2 < 0.f ? -x : x, 15 - e));
+                    qf[s][2 * i + 1] = static_cast<_Float16>(zero ? 0.f : ldexpf(a.scale_log2 < 0.f ? -y : y, 15 - e));
                 }
             }
         }
-        const float q_log2 = qs * a.scale_log2;
+        const float q_log2 = qs * fabsf(a.scale_log2);   // (a negative scale's sign is in the queries)
 
         f32x16 o[ET];
 #pragma unroll
@@ -541,26 +541,34 @@ __global__ __launch_bounds__(NW * 64, NW / 4) void attend_many_kernel(AttendArgs
         float m_run = -__builtin_inff(), l_run = 0.f;   // this lane's part of the sum
         int e_ref = kNone;
 
-        // a page's codes, one page ahead of their use
+        // Lane i has the id and scales of page at + i.
+        int32_t at = p0, ids = -1;
+        float kss = 0.f, vss = 0.f;
+        auto look = [&](int32_t p) {
+            at = p;
+            ids = p + lane < p1 ? page_id(a.c, a.s, seq, p + lane) : -1;
+            if (ids >= 0) {
+                kss = a.c.k_scale[static_cast<uint64_t>(ids) * a.c.kv_heads + kvh];
+                vss = a.c.v_scale[static_cast<uint64_t>(ids) * a.c.kv_heads + kvh];
+            }
+        };
+        auto id_of = [&](int32_t p) { return __builtin_amdgcn_readlane(ids, p - at); };
+
+        // A page's codes, on the way from memory while the page before is
+        // computed (where there is no page, page 0 is read and not used).
         i32x4 st[PER];
-        int32_t next_id = -1;
-        float next_ks = 0.f, next_vs = 0.f;
         auto fetch = [&](int32_t p) {
-            next_id = p < p1 ? page_id(a.c, a.s, seq, p) : -1;
-            const uint64_t at = static_cast<uint64_t>(max(next_id, 0)) * a.c.kv_heads + kvh;
-            next_ks = a.c.k_scale[at];
-            next_vs = a.c.v_scale[at];
+            const uint64_t first = (static_cast<uint64_t>(max(id_of(p), 0)) * a.c.kv_heads + kvh) * (kPage * D);
 #pragma unroll
             for (int u = 0; u < PER; ++u) {
                 const int i = tid + u * NT;
-                const int8_t* src = i < UNITS / 2 ? a.c.k + at * (kPage * D) + 16 * i
-                                                  : a.c.v + at * (kPage * D) + 16 * (i - UNITS / 2);
+                const int8_t* src = i < UNITS / 2 ? a.c.k + first + 16 * i : a.c.v + first + 16 * (i - UNITS / 2);
                 st[u] = *reinterpret_cast<const i32x4*>(src);
             }
         };
-        // The codes into shared memory; the values by 2^(their exponent -
-        // the reference), which moves up where that would pass 2^5 (the
-        // packed conversion stays below f16's 65504 up to there).
+        // Into shared memory; the values by 2^(their exponent - the
+        // reference), which moves up where that would pass 2^5 (the packed
+        // conversion stays below f16's 65504 up to there).
         auto stage = [&](int b, int e_page) {
             const int up = max(min(e_page - e_ref, 5), -24);
             const _Float16 vmul = static_cast<_Float16>(e_page == kNone ? 0.f : ldexpf(1.f, up));
@@ -582,116 +590,130 @@ __global__ __launch_bounds__(NW * 64, NW / 4) void attend_many_kernel(AttendArgs
                 }
             }
         };
-        auto settle = [&](float vs) {            // the reference exponent with a new page; by how much it moves
+        int move = 0;                            // how far the reference exponent moves with the page staged
+        auto settle = [&](int32_t p) {
+            const float vs = read_lane(vss, p - at);
             const int e = exponent_of(vs);
-            if (e == kNone || vs != vs) return 0;
+            move = 0;
+            if (id_of(p) < 0 || e == kNone || vs != vs) return e;
             if (e_ref == kNone) e_ref = e;
-            const int move = e - e_ref > 5 ? e - e_ref : 0;
+            if (e - e_ref > 5) move = e - e_ref;
             e_ref += move;
-            return move;
+            return e;
+        };
+        // whether this wave's columns see anything of a page
+        auto seen = [&](int32_t p) { return p < p1 && id_of(p) >= 0 && p * kPage < w_hi && p * kPage + kPage > w_lo; };
+        auto scores = [&](int b, f32x16 (&sc)[2]) {
+            const f16x8* k = kbuf + b * kPage * KC;
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) sc[t][i] = 0.f;
+#pragma unroll
+            for (int s = 0; s < QS; ++s)
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    const int row = 32 * t + token_of_row(col);
+                    sc[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(k[row * KC + ((2 * s + half) ^ k_swizzle(row))],
+                                                                   qf[s], sc[t], 0, 0, 0);
+                }
+        };
+        auto values = [&](int b, const f16x8 (&pf)[4]) {
+            const f16x8* v = vbuf + b * D * 8;
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+#pragma unroll
+                for (int e = 0; e < ET; ++e) {
+                    const int row = 32 * e + col;
+                    o[e] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v[row * 8 + ((2 * s + half) ^ (row & 7))], pf[s],
+                                                                  o[e], 0, 0, 0);
+                }
+        };
+        float fm = 0.f, base = 0.f;              // p = e^(sc fm - base)
+        // Masks the page's scores, moves the reference if it has to, settles fm and base.
+        auto ready = [&](int32_t p, f32x16 (&sc)[2]) {
+            const int32_t t0 = p * kPage;
+            fm = q_log2 * read_lane(kss, p - at);
+            bool any = true;
+            if (t0 < full_lo || t0 + kPage > full_hi || n_cols != 32) {
+                const int from = max(see_lo - t0, 0), to = w.row < 0 ? 0 : min(w.pos + 1 - t0, kPage);
+                any = from < to;
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const int k = 32 * t + 16 * (i >> 3) + 8 * half + (i & 7);
+                        sc[t][i] = k >= from && k < to ? sc[t][i] * fm : -__builtin_inff();
+                    }
+                fm = 1.f;
+            }
+            float mt = -__builtin_inff();
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) mt = fmaxf(mt, sc[t][i]);
+            mt = max_halves(mt) * fm;
+            // (of a page that shows only NaN the reference is 0)
+            const float ref = mt > -__builtin_inff() ? mt : (any && m_run == -__builtin_inff() ? 0.f : m_run);
+            if (__any(any && !(ref - m_run <= kMoveAt))) {
+                const float m_new = any && !(ref - m_run <= kMoveAt) ? ref : m_run;
+                const float keep = m_run == m_new ? 1.f : __builtin_amdgcn_exp2f(m_run - m_new);
+                l_run *= keep;
+                m_run = m_new;
+#pragma unroll
+                for (int e = 0; e < ET; ++e)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) o[e][i] *= keep;
+            }
+            // (a column that has seen nothing yet: e^-inf, not inf - inf)
+            base = (m_run > -__builtin_inff() ? m_run : 0.f) - kPBias;
+            const float vs = read_lane(vss, p - at);
+            if (any && vs != vs) l_run = __builtin_nanf("");
+        };
+        auto weights = [&](const f32x16 (&sc)[2], f16x8 (&pf)[4]) {
+            float l[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int i = 0; i < 16; i += 2) {
+                    const float x = __builtin_amdgcn_exp2f(fmaf(sc[t][i], fm, -base));
+                    const float y = __builtin_amdgcn_exp2f(fmaf(sc[t][i + 1], fm, -base));
+                    const f16x2 h = {static_cast<_Float16>(x), static_cast<_Float16>(y)};
+                    const f16x2 one = {static_cast<_Float16>(1.f), static_cast<_Float16>(1.f)};
+                    l[(i >> 1) & 3] = __builtin_amdgcn_fdot2(h, one, l[(i >> 1) & 3], false);
+                    pf[2 * t + (i >> 3)][i & 7] = h[0];
+                    pf[2 * t + (i >> 3)][(i & 7) + 1] = h[1];
+                }
+            l_run += (l[0] + l[1]) + (l[2] + l[3]);
         };
 
         if (p0 < p1) {
+            look(p0);
             fetch(p0);
-            int32_t id = next_id;
-            float ks = next_ks, vs = next_vs;
-            int move = id >= 0 ? settle(vs) : 0;
-            stage(0, exponent_of(vs));
+            int e_page = settle(p0);
+            stage(0, e_page);
             __syncthreads();
             for (int32_t p = p0; p < p1; ++p) {
                 const int b = (p - p0) & 1;
+                if (p + 2 - at > 64) look(p);
                 fetch(p + 1);
-                // outputs so far follow the reference exponent
-                if (move != 0) {
+                if (move != 0) {                 // outputs so far follow the reference exponent
                     const float f = ldexpf(1.f, -move);
 #pragma unroll
                     for (int e = 0; e < ET; ++e)
 #pragma unroll
                         for (int i = 0; i < 16; ++i) o[e][i] *= f;
                 }
-                const int32_t t0 = p * kPage;
-                if (id >= 0 && t0 < w_hi && t0 + kPage > w_lo) {
+                if (seen(p)) {
                     f32x16 sc[2];
-                    const f16x8* kb = kbuf + b * kPage * KC;
-#pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) sc[t][i] = 0.f;
-                        const int row = 32 * t + token_of_row(col);
-#pragma unroll
-                        for (int s = 0; s < QS; ++s)
-                            sc[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
-                                kb[row * KC + ((2 * s + half) ^ k_swizzle(row))], qf[s], sc[t], 0, 0, 0);
-                    }
-                    const float f = q_log2 * ks;
-                    bool any = true;
-                    if (t0 < full_lo || t0 + kPage > full_hi || n_cols != 32) {
-                        // (scaled first: a masked score is no longer touched)
-                        const int from = max(see_lo - t0, 0), to = w.row < 0 ? 0 : min(w.pos + 1 - t0, kPage);
-                        any = from < to;
-#pragma unroll
-                        for (int t = 0; t < 2; ++t)
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) {
-                                const int k = 32 * t + 16 * (i >> 3) + 8 * half + (i & 7);
-                                sc[t][i] = k >= from && k < to ? sc[t][i] * f : -__builtin_inff();
-                            }
-                    } else {
-#pragma unroll
-                        for (int t = 0; t < 2; ++t)
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) sc[t][i] *= f;
-                    }
-                    float mt = -__builtin_inff();
-#pragma unroll
-                    for (int t = 0; t < 2; ++t)
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) mt = fmaxf(mt, sc[t][i]);
-                    mt = max_halves(mt);
-                    // (of a page that shows only NaN the reference is 0)
-                    const float ref = mt > -__builtin_inff() ? mt : (any && m_run == -__builtin_inff() ? 0.f : m_run);
-                    if (__any(any && !(ref - m_run <= kMoveAt))) {
-                        const float m_new = any && !(ref - m_run <= kMoveAt) ? ref : m_run;
-                        const float keep = m_run == m_new ? 1.f : __builtin_amdgcn_exp2f(m_run - m_new);
-                        l_run *= keep;
-                        m_run = m_new;
-#pragma unroll
-                        for (int e = 0; e < ET; ++e)
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) o[e][i] *= keep;
-                    }
-                    // (a column that has seen nothing yet: e^-inf, not inf - inf)
-                    const float base = (m_run > -__builtin_inff() ? m_run : 0.f) - kPBias;
-                    const bool vnan = vs != vs;
+                    scores(b, sc);
+                    ready(p, sc);
                     f16x8 pf[4];
-#pragma unroll
-                    for (int t = 0; t < 2; ++t)
-#pragma unroll
-                        for (int i = 0; i < 16; i += 2) {
-                            const float x = __builtin_amdgcn_exp2f(sc[t][i] - base);
-                            const float y = __builtin_amdgcn_exp2f(sc[t][i + 1] - base);
-                            const f16x2 h = {static_cast<_Float16>(x), static_cast<_Float16>(y)};
-                            const f16x2 one = {static_cast<_Float16>(1.f), static_cast<_Float16>(1.f)};
-                            l_run = __builtin_amdgcn_fdot2(h, one, l_run, false);
-                            pf[2 * t + (i >> 3)][i & 7] = h[0];
-                            pf[2 * t + (i >> 3)][(i & 7) + 1] = h[1];
-                        }
-                    if (vnan && any) l_run = __builtin_nanf("");
-                    const f16x8* vb = vbuf + b * D * 8;
-#pragma unroll
-                    for (int e = 0; e < ET; ++e) {
-                        const int row = 32 * e + col;
-#pragma unroll
-                        for (int s = 0; s < 4; ++s)
-                            o[e] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vb[row * 8 + ((2 * s + half) ^ (row & 7))],
-                                                                          pf[s], o[e], 0, 0, 0);
-                    }
+                    weights(sc, pf);
+                    values(b, pf);
                 }
-                id = next_id;
-                ks = next_ks;
-                vs = next_vs;
-                move = id >= 0 ? settle(vs) : 0;
-                stage(b ^ 1, exponent_of(vs));
+                e_page = p + 1 < p1 ? settle(p + 1) : kNone;
+                stage(b ^ 1, e_page);
                 __syncthreads();
             }
         }
@@ -699,7 +721,7 @@ __global__ __launch_bounds__(NW * 64, NW / 4) void attend_many_kernel(AttendArgs
         // Outputs: a lane has, for its column, four dims at a time.
         const float l = l_run + xor_lane(l_run, 32);
         if (w.row >= 0) {
-            const uint64_t at = static_cast<uint64_t>(w.row) * a.heads + w.head;
+            const uint64_t row_at = static_cast<uint64_t>(w.row) * a.heads + w.head;
             const float v_scale = e_ref == kNone ? 0.f : ldexpf(1.f, e_ref);
             if (a.pieces == 1) {
                 const float inv = l == 0.f ? 0.f : 1.f / l;
@@ -711,10 +733,10 @@ __global__ __launch_bounds__(NW * 64, NW / 4) void attend_many_kernel(AttendArgs
                         bf16x4 x;
 #pragma unroll
                         for (int k = 0; k < 4; ++k) x[k] = static_cast<__bf16>((o[e][i + k] * inv) * v_scale);
-                        *reinterpret_cast<bf16x4*>(static_cast<__bf16*>(a.out) + at * D + 32 * e + 2 * i + 4 * half) = x;
+                        *reinterpret_cast<bf16x4*>(static_cast<__bf16*>(a.out) + row_at * D + 32 * e + 2 * i + 4 * half) = x;
                     }
             } else {
-                const uint64_t slot = static_cast<uint64_t>(piece) * a.s.rows * a.heads + at;
+                const uint64_t slot = static_cast<uint64_t>(piece) * a.s.rows * a.heads + row_at;
                 if (p0 < p1) {
 #pragma unroll
                     for (int e = 0; e < ET; ++e)
