@@ -29,6 +29,8 @@
 // fourth page and keeps its own running maximum, sum and output, joined in
 // shared memory at the end.  The pieces of a sequence are joined by a second
 // kernel, in their order.
+#include <type_traits>
+
 #include "kv_common.h"
 
 namespace qmv {
@@ -419,8 +421,8 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attend_few_kernel(Atten
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 
-constexpr float kPBias = 7.0f;         // probabilities times 2^7
-constexpr float kMoveAt = 8.0f;        // reference moved when a maximum is 2^8 above
+constexpr float kPBias = 3.0f;         // probabilities times 2^3
+constexpr float kMoveAt = 6.0f;        // reference moved when a maximum is 2^6 above
 
 // Row r of a score tile: its token.
 __device__ __forceinline__ int token_of_row(int r) {
@@ -434,30 +436,34 @@ __device__ __forceinline__ int token_of_row(int r) {
 template <int CHUNKS>
 __device__ __forceinline__ int swizzle(int row) { return CHUNKS == 8 ? (row >> 1) & 7 : row & 15; }
 
-// 16 codes as f16, each times mul: x * mul - 1152 mul.
-__device__ __forceinline__ void codes_to_f16(i32x4 c, _Float16 mul, f16x8 out[2]) {
-    const f16x2 m = {mul, mul};
-    const f16x2 s = {static_cast<_Float16>(mul * static_cast<_Float16>(-1152.f)), static_cast<_Float16>(mul * static_cast<_Float16>(-1152.f))};
+// 16 codes as f16, each times mul (less = -1152 mul).
+__device__ __forceinline__ void codes_to_f16(i32x4 c, f16x2 mul, f16x2 less, f16x8 out[2]) {
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
         const uint32_t u = static_cast<uint32_t>(c[w]) ^ 0x80808080u;
         const f16x2 lo = __builtin_elementwise_fma(
-            __builtin_bit_cast(f16x2, __builtin_amdgcn_perm(0x64646464u, u, 0x04010400u)), m, s);
+            __builtin_bit_cast(f16x2, __builtin_amdgcn_perm(0x64646464u, u, 0x04010400u)), mul, less);
         const f16x2 hi = __builtin_elementwise_fma(
-            __builtin_bit_cast(f16x2, __builtin_amdgcn_perm(0x64646464u, u, 0x04030402u)), m, s);
+            __builtin_bit_cast(f16x2, __builtin_amdgcn_perm(0x64646464u, u, 0x04030402u)), mul, less);
         out[w >> 1][4 * (w & 1)] = lo[0];
         out[w >> 1][4 * (w & 1) + 1] = lo[1];
         out[w >> 1][4 * (w & 1) + 2] = hi[0];
         out[w >> 1][4 * (w & 1) + 3] = hi[1];
     }
 }
+// 2^up and -1152 2^up for up from -24 to 5, as f16 twice.
+__device__ __forceinline__ uint32_t f16_power(int up) {
+    return (up >= -14 ? static_cast<uint32_t>(up + 15) << 10 : 1u << (up + 24)) * 0x10001u;
+}
+__device__ __forceinline__ uint32_t f16_less(int up) {   // 1152 = 1.125 2^10
+    return (0x8080u | static_cast<uint32_t>(up + 25) << 10) * 0x10001u;
+}
 
-// Exponent of a scale (a power of two, possibly from another hand: then its
-// own exponent), kNone for 0.
-constexpr int kNone = -1000;
+// Exponent of a scale, a power of two; kNone for 0, kNan for what is no number.
+constexpr int kNone = -1000, kNan = 1000;
 __device__ __forceinline__ int exponent_of(float s) {
     const uint32_t b = __builtin_bit_cast(uint32_t, s) & 0x7FFFFFFFu;
-    return b < 0x00800000u ? kNone : static_cast<int>(b >> 23) - 127;
+    return b < 0x00800000u ? kNone : (b >= 0x7F800000u ? kNan : static_cast<int>(b >> 23) - 127);
 }
 
 template <int D, int NW>
@@ -497,7 +503,10 @@ __global__ __launch_bounds__(NW * 64, NW / 4) void attend_many_kernel(AttendArgs
         const int32_t wl = r.base + static_cast<int32_t>((c0 + max(n_cols, 1u) - 1) / a.group);
         const int32_t w_lo = sees_from(a.window, max(wf, 0));
         const int32_t w_hi = n_cols != 0 ? max(wl + 1, 0) : 0;
-        const int32_t full_lo = sees_from(a.window, wl), full_hi = wf + 1;
+        // (as page numbers: some seen, all seen by all)
+        const int32_t seen_lo = w_lo / kPage, seen_hi = (w_hi + kPage - 1) / kPage;
+        const int32_t full_lo = (sees_from(a.window, wl) + kPage - 1) / kPage;
+        const int32_t full_hi = n_cols == 32 ? max(wf + 1, 0) / kPage : 0;
 
         // the queries, f16, as the second operand of the scores
         f16x8 qf[QS];
@@ -544,70 +553,93 @@ __global__ __launch_bounds__(NW * 64, NW / 4) void attend_many_kernel(AttendArgs
         float m_run = -__builtin_inff(), l_run = 0.f;   // this lane's part of the sum
         int e_ref = kNone;
 
-        // Lane i has the id and scales of page at + i.
-        int32_t at = p0, ids = -1;
-        float kss = 0.f, vss = 0.f;
+        // Lane i has, of page at + i: its place (page id * kv_heads + head; -1:
+        // none), its keys' scale and its values' scale's exponent.
+        int32_t at = p0, places = -1, exps = kNone;
+        float kss = 0.f;
         auto look = [&](int32_t p) {
             at = p;
-            ids = p + lane < p1 ? page_id(a.c, a.s, seq, p + lane) : -1;
-            if (ids >= 0) {
-                kss = a.c.k_scale[static_cast<uint64_t>(ids) * a.c.kv_heads + kvh];
-                vss = a.c.v_scale[static_cast<uint64_t>(ids) * a.c.kv_heads + kvh];
+            const int32_t id = p + lane < p1 ? page_id(a.c, a.s, seq, p + lane) : -1;
+            places = -1;
+            if (id >= 0) {
+                places = id * static_cast<int32_t>(a.c.kv_heads) + static_cast<int32_t>(kvh);
+                kss = a.c.k_scale[places];
+                exps = exponent_of(a.c.v_scale[places]);
             }
         };
-        auto id_of = [&](int32_t p) { return __builtin_amdgcn_readlane(ids, p - at); };
+        auto place = [&](int32_t p) { return p < p1 ? __builtin_amdgcn_readlane(places, p - at) : -1; };
 
-        // A page's codes, on the way from memory while the page before is
-        // computed (where there is no page, page 0 is read and not used).
+        // The codes of one page's keys and one's values, on the way from memory
+        // while pages before are computed (where there is no page, page 0 is
+        // read and not used).  A wave's pieces are all keys or all values.
         i32x4 st[PER];
-        auto fetch = [&](int32_t p) {
-            const uint64_t first = (static_cast<uint64_t>(max(id_of(p), 0)) * a.c.kv_heads + kvh) * (kPage * D);
+        const int8_t* const k_from = a.c.k + 16 * tid;
+        const int8_t* const v_from = a.c.v + 16 * tid - 8 * UNITS;
+        auto fetch = [&](int32_t kp, int32_t vp) {
+            const int64_t k_at = static_cast<int64_t>(max(place(kp), 0)) * (kPage * D);
+            const int64_t v_at = static_cast<int64_t>(max(place(vp), 0)) * (kPage * D);
 #pragma unroll
-            for (int u = 0; u < PER; ++u) {
-                const int i = tid + u * NT;
-                const int8_t* src = i < UNITS / 2 ? a.c.k + first + 16 * i : a.c.v + first + 16 * (i - UNITS / 2);
-                st[u] = *reinterpret_cast<const i32x4*>(src);
-            }
+            for (int u = 0; u < PER; ++u)
+                st[u] = *reinterpret_cast<const i32x4*>((wave * 64 + u * NT < UNITS / 2 ? k_from + k_at : v_from + v_at) + 16 * u * NT);
         };
         // Into shared memory; the values by 2^(their exponent - the
         // reference), which moves up where that would pass 2^5 (the packed
         // conversion stays below f16's 65504 up to there).
-        auto stage = [&](int b, int e_page) {
+        auto stage = [&](int kb, int vb, int e_page) {
             const int up = max(min(e_page - e_ref, 5), -24);
-            const _Float16 vmul = static_cast<_Float16>(e_page == kNone ? 0.f : ldexpf(1.f, up));
+            const uint32_t v_mul = e_page == kNone ? 0u : f16_power(up), v_less = e_page == kNone ? 0u : f16_less(up);
 #pragma unroll
             for (int u = 0; u < PER; ++u) {
                 const int i = tid + u * NT;
                 f16x8 x[2];
-                codes_to_f16(st[u], i < UNITS / 2 ? static_cast<_Float16>(1.f) : vmul, x);
-                if (i < UNITS / 2) {
-                    const int row = i / (D / 16), c = 2 * (i % (D / 16));
-                    f16x8* d = kbuf + (b * kPage + row) * KC;
-                    d[c ^ swizzle<KC>(row)] = x[0];
-                    d[(c + 1) ^ swizzle<KC>(row)] = x[1];
+                if (wave * 64 + u * NT < UNITS / 2) {
+                    codes_to_f16(st[u], __builtin_bit_cast(f16x2, f16_power(0)), __builtin_bit_cast(f16x2, f16_less(0)), x);
+                    const int row = i / (D / 16), c = (2 * (i % (D / 16))) ^ swizzle<KC>(row);
+                    f16x8* d = kbuf + (kb * kPage + row) * KC;
+                    d[c] = x[0];
+                    d[c ^ 1] = x[1];
                 } else {
-                    const int k = i - UNITS / 2, row = k >> 2, c = 2 * (k & 3);
-                    f16x8* d = vbuf + (b * D + row) * 8;
-                    d[c ^ swizzle<8>(row)] = x[0];
-                    d[(c + 1) ^ swizzle<8>(row)] = x[1];
+                    codes_to_f16(st[u], __builtin_bit_cast(f16x2, v_mul), __builtin_bit_cast(f16x2, v_less), x);
+                    const int k = i - UNITS / 2, row = k >> 2, c = (2 * (k & 3)) ^ swizzle<8>(row);
+                    f16x8* d = vbuf + (vb * D + row) * 8;
+                    d[c] = x[0];
+                    d[c ^ 1] = x[1];
                 }
             }
         };
         int move = 0;                            // how far the reference exponent moves with the page staged
         auto settle = [&](int32_t p) {
-            const float vs = read_lane(vss, p - at);
-            const int e = exponent_of(vs);
-            move = 0;
-            if (id_of(p) < 0 || e == kNone || vs != vs) return e;
+            if (place(p) < 0) return kNone;
+            const int e = __builtin_amdgcn_readlane(exps, p - at);
+            if (e == kNone || e == kNan) return e;
             if (e_ref == kNone) e_ref = e;
             if (e - e_ref > 5) move = e - e_ref;
             e_ref += move;
             return e;
         };
         // whether this wave's columns see anything of a page
-        auto seen = [&](int32_t p) { return p < p1 && id_of(p) >= 0 && p * kPage < w_hi && p * kPage + kPage > w_lo; };
+        auto seen = [&](int32_t p) { return p >= seen_lo && p < seen_hi && place(p) >= 0; };
+        // Chunk 2 s + half of a row, permuted, is the row's chunk (half ^
+        // permutation) with the bits of 2 s flipped.  (The addresses are hidden
+        // from the compiler, which would keep one for every read in a register.)
+        const uint32_t k_row = static_cast<uint32_t>(token_of_row(col) * KC + (half ^ swizzle<KC>(token_of_row(col))));
+        const uint32_t v_row = static_cast<uint32_t>(col * 8 + (half ^ swizzle<8>(col)));
+        // Reads of shared memory run kAhead products ahead.
+        auto pipelined = [](auto n) {
+            constexpr int kAhead = 6, N = decltype(n)::value;
+            __builtin_amdgcn_sched_group_barrier(0x100, kAhead, 0);
+#pragma unroll
+            for (int i = 0; i < N - kAhead; ++i) {
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+            }
+            __builtin_amdgcn_sched_group_barrier(0x008, kAhead, 0);
+            __builtin_amdgcn_sched_barrier(0);
+        };
         auto scores = [&](int b, f32x16 (&sc)[2]) {
-            const f16x8* k = kbuf + b * kPage * KC;
+            __builtin_amdgcn_sched_barrier(0);
+            uint32_t from = k_row + b * kPage * KC;
+            asm volatile("" : "+v"(from));
 #pragma unroll
             for (int t = 0; t < 2; ++t)
 #pragma unroll
@@ -615,30 +647,28 @@ __global__ __launch_bounds__(NW * 64, NW / 4) void attend_many_kernel(AttendArgs
 #pragma unroll
             for (int s = 0; s < QS; ++s)
 #pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    const int row = 32 * t + token_of_row(col);
-                    sc[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(k[row * KC + ((2 * s + half) ^ swizzle<KC>(row))],
-                                                                   qf[s], sc[t], 0, 0, 0);
-                }
+                for (int t = 0; t < 2; ++t)
+                    sc[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kbuf[(from ^ (2 * s)) + 32 * t * KC], qf[s], sc[t], 0, 0, 0);
+            pipelined(std::integral_constant<int, 2 * QS>{});
         };
         auto values = [&](int b, const f16x8 (&pf)[4]) {
-            const f16x8* v = vbuf + b * D * 8;
+            __builtin_amdgcn_sched_barrier(0);
+            uint32_t from = v_row + b * D * 8;
+            asm volatile("" : "+v"(from));
 #pragma unroll
             for (int s = 0; s < 4; ++s)
 #pragma unroll
-                for (int e = 0; e < ET; ++e) {
-                    const int row = 32 * e + col;
-                    o[e] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v[row * 8 + ((2 * s + half) ^ swizzle<8>(row))], pf[s],
-                                                                  o[e], 0, 0, 0);
-                }
+                for (int e = 0; e < ET; ++e)
+                    o[e] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vbuf[(from ^ (2 * s)) + 32 * e * 8], pf[s], o[e], 0, 0, 0);
+            pipelined(std::integral_constant<int, 4 * ET>{});
         };
         float fm = 0.f, base = 0.f;              // p = e^(sc fm - base)
+        bool begun = false;                      // every column of the wave has a reference
         // Masks the page's scores, moves the reference if it has to, settles fm and base.
         auto ready = [&](int32_t p, f32x16 (&sc)[2]) {
             const int32_t t0 = p * kPage;
-            fm = q_log2 * read_lane(kss, p - at);
             bool any = true;
-            if (t0 < full_lo || t0 + kPage > full_hi || n_cols != 32) {
+            if (p < full_lo || p >= full_hi) {
                 const int from = max(see_lo - t0, 0), to = w.row < 0 ? 0 : min(w.pos + 1 - t0, kPage);
                 any = from < to;
 #pragma unroll
@@ -670,9 +700,10 @@ __global__ __launch_bounds__(NW * 64, NW / 4) void attend_many_kernel(AttendArgs
             }
             // (a column that has seen nothing yet: e^-inf, not inf - inf)
             base = (m_run > -__builtin_inff() ? m_run : 0.f) - kPBias;
-            const float vs = read_lane(vss, p - at);
-            if (any && vs != vs) l_run = __builtin_nanf("");
+            begun = __all(m_run > -__builtin_inff());
+            if (any && __builtin_amdgcn_readlane(exps, p - at) == kNan) l_run = __builtin_nanf("");
         };
+        // The probabilities, and this lane's sum of them.
         auto weights = [&](const f32x16 (&sc)[2], f16x8 (&pf)[4]) {
             float l[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -687,36 +718,55 @@ __global__ __launch_bounds__(NW * 64, NW / 4) void attend_many_kernel(AttendArgs
                     pf[2 * t + (i >> 3)][i & 7] = h[0];
                     pf[2 * t + (i >> 3)][(i & 7) + 1] = h[1];
                 }
-            l_run += (l[0] + l[1]) + (l[2] + l[3]);
+            return (l[0] + l[1]) + (l[2] + l[3]);
+        };
+        // In the middle of a sequence the maximum is not even sought: relative
+        // to the reference so far the probabilities either keep their sum
+        // below 2^14 (so each is at most 2^7 times that of the reference), or
+        // the page is done again with its maximum.
+        auto weigh = [&](int32_t p, f32x16 (&sc)[2], f16x8 (&pf)[4]) {
+            fm = q_log2 * read_lane(kss, p - at);
+            if (begun && p >= full_lo && p < full_hi && __builtin_amdgcn_readlane(exps, p - at) != kNan) {
+                const float l = weights(sc, pf);
+                if (__all(l < 32768.f)) {
+                    l_run += l;
+                    return;
+                }
+            }
+            ready(p, sc);
+            l_run += weights(sc, pf);
+        };
+
+        auto follow = [&]() {                    // outputs so far follow the reference exponent
+            if (move == 0) return;
+            const float f = ldexpf(1.f, -move);
+#pragma unroll
+            for (int e = 0; e < ET; ++e)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[e][i] *= f;
+            move = 0;
         };
 
         if (p0 < p1) {
             look(p0);
-            fetch(p0);
+            fetch(p0, p0);
             int e_page = settle(p0);
-            stage(0, e_page);
+            stage(0, 0, e_page);
             __syncthreads();
             for (int32_t p = p0; p < p1; ++p) {
                 const int b = (p - p0) & 1;
                 if (p + 2 - at > 64) look(p);
-                fetch(p + 1);
-                if (move != 0) {                 // outputs so far follow the reference exponent
-                    const float f = ldexpf(1.f, -move);
-#pragma unroll
-                    for (int e = 0; e < ET; ++e)
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) o[e][i] *= f;
-                }
+                fetch(p + 1, p + 1);
+                follow();
                 if (seen(p)) {
                     f32x16 sc[2];
                     scores(b, sc);
-                    ready(p, sc);
                     f16x8 pf[4];
-                    weights(sc, pf);
+                    weigh(p, sc, pf);
                     values(b, pf);
                 }
-                e_page = p + 1 < p1 ? settle(p + 1) : kNone;
-                stage(b ^ 1, e_page);
+                e_page = settle(p + 1);
+                stage(b ^ 1, b ^ 1, e_page);
                 __syncthreads();
             }
         }

@@ -120,8 +120,8 @@ typedef struct qmv_kv_seqs {
  * Two sequences must not write into one page in the same call.
  * Errors: QMV_E_ARG (a NULL or misaligned pointer, pages, kv_heads, seqs,
  * table_stride or rows 0, dtype unknown), QMV_E_SHAPE (head_dim, or a size that
- * a launch cannot hold: kv_heads above 65535, seqs * kv_heads or pages of
- * 2^31 or more, rows above 2^31 - 2^16), QMV_E_DEVICE.
+ * a launch cannot hold: kv_heads above 65535, seqs * kv_heads or
+ * pages * kv_heads of 2^31 or more, rows above 2^31 - 2^16), QMV_E_DEVICE.
  */
 int qmv_kv_write(const qmv_kv_cache *cache, const qmv_kv_seqs *seqs, uint32_t dtype, const void *k,
                  const void *v, void *stream);
