@@ -393,7 +393,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attend_few_kernel(Atten
 
 // ---- many queries a key/value head (bfloat16 prompts) -------------------------
 //
-// Products on v_mfma_f32_32x32x16_f16: a workgroup of NW waves has 32 NW
+// Products on v_mfma_f32_32x32x16_f16: a workgroup of eight waves has 256
 // columns, each wave 32, and walks the pages that any of them sees.  A page's
 // codes come from memory into registers one page ahead, are made f16 once for
 // all waves on the way into shared memory (1024 + 128 + code is the f16 with
@@ -406,9 +406,9 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attend_few_kernel(Atten
 // exponent that follows the pages' largest: code 2^(e - ref), exact from
 // 2^-19 up; probabilities are rounded to f16 and their sum is taken from the
 // rounded ones, so that numerator and denominator agree.  Sums are relative
-// to a running reference that is moved (and the outputs scaled) only when a
-// page's maximum is more than 2^8 above it: p <= 2^8, times 2^7 so that f16
-// keeps 2^-29 of the maximum at full precision.
+// to a running reference, times 2^3, that is moved (and the outputs scaled)
+// only when probabilities reach 2^10 or more, so that they stay f16; down to
+// 2^-17 of the reference they keep all of f16's bits, down to 2^-27 some.
 //
 // Rows and columns are arranged as above: the 32 x 32 output gives lane l,
 // register 4 a + b the row 8 a + 4 (l / 32) + b and takes the k-indexes 8 (l /
@@ -423,6 +423,9 @@ typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 
 constexpr float kPBias = 3.0f;         // probabilities times 2^3
 constexpr float kMoveAt = 6.0f;        // reference moved when a maximum is 2^6 above
+
+// Columns of a workgroup of eight waves.
+constexpr int many_cols(int d) { return d == 256 ? 128 : 256; }
 
 // Row r of a score tile: its token.
 __device__ __forceinline__ int token_of_row(int r) {
@@ -466,18 +469,30 @@ __device__ __forceinline__ int exponent_of(float s) {
     return b < 0x00800000u ? kNone : (b >= 0x7F800000u ? kNan : static_cast<int>(b >> 23) - 127);
 }
 
-template <int D, int NW>
-__global__ __launch_bounds__(NW * 64, NW / 4) void attend_many_kernel(AttendArgs a) {
-    constexpr int NT = NW * 64;
-    constexpr int COLS = 32 * NW;
+// Head dims of 256 hold too many registers for a wave of 32 columns: waves w
+// and w + 4 have the same 32.  Each scores and weighs half of a page's tokens,
+// they exchange the probabilities through shared memory, and each adds up half
+// of the output dims.  Whether a page is masked or its maximum is sought is
+// then decided for the workgroup, whose waves meet at the barriers.
+template <int D>
+__global__ __launch_bounds__(512, 2) void attend_many_kernel(AttendArgs a) {
+    constexpr int NT = 512;
+    constexpr bool PAIR = D == 256;
+    constexpr int COLS = many_cols(D);
+    constexpr int ST = PAIR ? 1 : 2;             // tiles of 32 tokens that a wave scores
     constexpr int KC = D / 8;                    // 16-byte chunks of a key row
     constexpr int UNITS = 2 * kPage * D / 16;    // 16-code pieces of a page: keys, then values
     constexpr int PER = UNITS / NT;
     constexpr int QS = D / 16;                   // k-steps of a score
-    constexpr int ET = D / 32;                   // tiles of output dims
+    constexpr int ET = D / (PAIR ? 64 : 32);     // tiles of output dims that a wave adds up
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
     f16x8* const kbuf = reinterpret_cast<f16x8*>(lds);                       // [2][64][KC]
     f16x8* const vbuf = kbuf + 2 * kPage * KC;                               // [2][D][8]
+    // (pairs) probabilities [4 column groups][4 k-steps][64 lanes], maxima and
+    // sums [4][2 halves][32], whether a page has to be done again
+    f16x8* const pbuf = vbuf + 2 * D * 8;
+    float* const mbuf = reinterpret_cast<float*>(pbuf + 4 * 4 * 64);
+    int* const again = reinterpret_cast<int*>(mbuf + 4 * 2 * 32);            // [2]
     const int tid = threadIdx.x, lane = tid & 63, col = lane & 31, half = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const uint32_t seq = blockIdx.x / a.c.kv_heads, kvh = blockIdx.x % a.c.kv_heads;
@@ -488,7 +503,8 @@ __global__ __launch_bounds__(NW * 64, NW / 4) void attend_many_kernel(AttendArgs
     // the last tiles see the most: they begin first
     for (uint32_t turn = blockIdx.y; turn < tiles; turn += gridDim.y) {
         const uint32_t tile = tiles - 1 - turn;
-        const Columns w = columns<COLS>(a, r, kvh, tile, wave * 32 + col);
+        const int group = PAIR ? wave & 3 : wave, part = PAIR ? wave >> 2 : 0;
+        const Columns w = columns<COLS>(a, r, kvh, tile, group * 32 + col);
         const int32_t p_lo = w.lo / kPage, p_hi = (w.hi + kPage - 1) / kPage;
         const int32_t per = max((p_hi - p_lo + static_cast<int32_t>(a.pieces) - 1) / static_cast<int32_t>(a.pieces),
                                 static_cast<int32_t>(a.per));
@@ -497,7 +513,7 @@ __global__ __launch_bounds__(NW * 64, NW / 4) void attend_many_kernel(AttendArgs
         const int32_t p1 = min(p_hi - p0, per) + p0;
         const int32_t see_lo = sees_from(a.window, w.pos);
         // this wave's columns: what any sees, and the pages that all see whole
-        const uint32_t c0 = tile * COLS + wave * 32;
+        const uint32_t c0 = tile * COLS + group * 32;
         const uint32_t n_cols = c0 < all ? min(all - c0, 32u) : 0u;
         const int32_t wf = r.base + static_cast<int32_t>(c0 / a.group);
         const int32_t wl = r.base + static_cast<int32_t>((c0 + max(n_cols, 1u) - 1) / a.group);
@@ -505,8 +521,9 @@ __global__ __launch_bounds__(NW * 64, NW / 4) void attend_many_kernel(AttendArgs
         const int32_t w_hi = n_cols != 0 ? max(wl + 1, 0) : 0;
         // (as page numbers: some seen, all seen by all)
         const int32_t seen_lo = w_lo / kPage, seen_hi = (w_hi + kPage - 1) / kPage;
-        const int32_t full_lo = (sees_from(a.window, wl) + kPage - 1) / kPage;
-        const int32_t full_hi = n_cols == 32 ? max(wf + 1, 0) / kPage : 0;
+        // (columns without a row have zero queries and may see anything)
+        const int32_t full_lo = (sees_from(a.window, PAIR ? w.last_pos : wl) + kPage - 1) / kPage;
+        const int32_t full_hi = PAIR || n_cols != 0 ? max((PAIR ? w.first_pos : wf) + 1, 0) / kPage : 0;
 
         // the queries, f16, as the second operand of the scores
         f16x8 qf[QS];
@@ -617,13 +634,13 @@ __global__ __launch_bounds__(NW * 64, NW / 4) void attend_many_kernel(AttendArgs
             e_ref += move;
             return e;
         };
-        // whether this wave's columns see anything of a page
-        auto seen = [&](int32_t p) { return p >= seen_lo && p < seen_hi && place(p) >= 0; };
+        // whether this wave's columns (a pair's workgroup's) see anything of a page
+        auto seen = [&](int32_t p) { return (PAIR || (p >= seen_lo && p < seen_hi)) && place(p) >= 0; };
         // Chunk 2 s + half of a row, permuted, is the row's chunk (half ^
         // permutation) with the bits of 2 s flipped.  (The addresses are hidden
         // from the compiler, which would keep one for every read in a register.)
-        const uint32_t k_row = static_cast<uint32_t>(token_of_row(col) * KC + (half ^ swizzle<KC>(token_of_row(col))));
-        const uint32_t v_row = static_cast<uint32_t>(col * 8 + (half ^ swizzle<8>(col)));
+        const uint32_t k_row = static_cast<uint32_t>((32 * part + token_of_row(col)) * KC + (half ^ swizzle<KC>(token_of_row(col))));
+        const uint32_t v_row = static_cast<uint32_t>((32 * ET * part + col) * 8 + (half ^ swizzle<8>(col)));
         // Reads of shared memory run kAhead products ahead.
         auto pipelined = [](auto n) {
             constexpr int kAhead = 6, N = decltype(n)::value;
@@ -636,20 +653,20 @@ __global__ __launch_bounds__(NW * 64, NW / 4) void attend_many_kernel(AttendArgs
             __builtin_amdgcn_sched_group_barrier(0x008, kAhead, 0);
             __builtin_amdgcn_sched_barrier(0);
         };
-        auto scores = [&](int b, f32x16 (&sc)[2]) {
+        auto scores = [&](int b, f32x16 (&sc)[ST]) {
             __builtin_amdgcn_sched_barrier(0);
             uint32_t from = k_row + b * kPage * KC;
             asm volatile("" : "+v"(from));
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
+            for (int t = 0; t < ST; ++t)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) sc[t][i] = 0.f;
 #pragma unroll
             for (int s = 0; s < QS; ++s)
 #pragma unroll
-                for (int t = 0; t < 2; ++t)
+                for (int t = 0; t < ST; ++t)
                     sc[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kbuf[(from ^ (2 * s)) + 32 * t * KC], qf[s], sc[t], 0, 0, 0);
-            pipelined(std::integral_constant<int, 2 * QS>{});
+            pipelined(std::integral_constant<int, ST * QS>{});
         };
         auto values = [&](int b, const f16x8 (&pf)[4]) {
             __builtin_amdgcn_sched_barrier(0);
@@ -665,27 +682,32 @@ __global__ __launch_bounds__(NW * 64, NW / 4) void attend_many_kernel(AttendArgs
         float fm = 0.f, base = 0.f;              // p = e^(sc fm - base)
         bool begun = false;                      // every column of the wave has a reference
         // Masks the page's scores, moves the reference if it has to, settles fm and base.
-        auto ready = [&](int32_t p, f32x16 (&sc)[2]) {
+        auto ready = [&](int32_t p, f32x16 (&sc)[ST]) {
             const int32_t t0 = p * kPage;
             bool any = true;
             if (p < full_lo || p >= full_hi) {
                 const int from = max(see_lo - t0, 0), to = w.row < 0 ? 0 : min(w.pos + 1 - t0, kPage);
                 any = from < to;
 #pragma unroll
-                for (int t = 0; t < 2; ++t)
+                for (int t = 0; t < ST; ++t)
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
-                        const int k = 32 * t + 16 * (i >> 3) + 8 * half + (i & 7);
+                        const int k = 32 * (t + part) + 16 * (i >> 3) + 8 * half + (i & 7);
                         sc[t][i] = k >= from && k < to ? sc[t][i] * fm : -__builtin_inff();
                     }
                 fm = 1.f;
             }
             float mt = -__builtin_inff();
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
+            for (int t = 0; t < ST; ++t)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) mt = fmaxf(mt, sc[t][i]);
             mt = max_halves(mt) * fm;
+            if constexpr (PAIR) {
+                if (half == 0) mbuf[(2 * group + part) * 32 + col] = mt;
+                __syncthreads();
+                mt = fmaxf(mt, mbuf[(2 * group + (part ^ 1)) * 32 + col]);
+            }
             // (of a page that shows only NaN the reference is 0)
             const float ref = mt > -__builtin_inff() ? mt : (any && m_run == -__builtin_inff() ? 0.f : m_run);
             if (__any(any && !(ref - m_run <= kMoveAt))) {
@@ -700,14 +722,16 @@ __global__ __launch_bounds__(NW * 64, NW / 4) void attend_many_kernel(AttendArgs
             }
             // (a column that has seen nothing yet: e^-inf, not inf - inf)
             base = (m_run > -__builtin_inff() ? m_run : 0.f) - kPBias;
-            begun = __all(m_run > -__builtin_inff());
+            // (a page that all see has given every column one)
+            if constexpr (PAIR) begun |= p >= full_lo && p < full_hi;
+            else begun = __all(m_run > -__builtin_inff());
             if (any && __builtin_amdgcn_readlane(exps, p - at) == kNan) l_run = __builtin_nanf("");
         };
         // The probabilities, and this lane's sum of them.
-        auto weights = [&](const f32x16 (&sc)[2], f16x8 (&pf)[4]) {
+        auto weights = [&](const f32x16 (&sc)[ST], f16x8 (&pf)[2 * ST]) {
             float l[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
+            for (int t = 0; t < ST; ++t)
 #pragma unroll
                 for (int i = 0; i < 16; i += 2) {
                     const float x = __builtin_amdgcn_exp2f(fmaf(sc[t][i], fm, -base));
@@ -722,19 +746,34 @@ __global__ __launch_bounds__(NW * 64, NW / 4) void attend_many_kernel(AttendArgs
         };
         // In the middle of a sequence the maximum is not even sought: relative
         // to the reference so far the probabilities either keep their sum
-        // below 2^14 (so each is at most 2^7 times that of the reference), or
+        // below 2^15 (so each is at most 2^12 times that of the reference), or
         // the page is done again with its maximum.
-        auto weigh = [&](int32_t p, f32x16 (&sc)[2], f16x8 (&pf)[4]) {
+        auto weigh = [&](int32_t p, f32x16 (&sc)[ST], f16x8 (&pf)[2 * ST]) {
             fm = q_log2 * read_lane(kss, p - at);
-            if (begun && p >= full_lo && p < full_hi && __builtin_amdgcn_readlane(exps, p - at) != kNan) {
+            const bool plain = begun && p >= full_lo && p < full_hi && __builtin_amdgcn_readlane(exps, p - at) != kNan;
+            if (plain) {
                 const float l = weights(sc, pf);
-                if (__all(l < 32768.f)) {
+                if constexpr (PAIR) {
+                    if (!__all(l < 32768.f) && lane == 0) again[p & 1] = 1;
+#pragma unroll
+                    for (int s = 0; s < 2; ++s) pbuf[(4 * group + 2 * part + s) * 64 + lane] = pf[s];
+                    __syncthreads();
+                    if (again[p & 1] == 0) {
+                        l_run += l;
+                        return;
+                    }
+                } else if (__all(l < 32768.f)) {
                     l_run += l;
                     return;
                 }
             }
             ready(p, sc);
             l_run += weights(sc, pf);
+            if constexpr (PAIR) {
+#pragma unroll
+                for (int s = 0; s < 2; ++s) pbuf[(4 * group + 2 * part + s) * 64 + lane] = pf[s];
+                __syncthreads();
+            }
         };
 
         auto follow = [&]() {                    // outputs so far follow the reference exponent
@@ -752,6 +791,7 @@ __global__ __launch_bounds__(NW * 64, NW / 4) void attend_many_kernel(AttendArgs
             fetch(p0, p0);
             int e_page = settle(p0);
             stage(0, 0, e_page);
+            if (PAIR && tid < 2) again[tid] = 0;
             __syncthreads();
             for (int32_t p = p0; p < p1; ++p) {
                 const int b = (p - p0) & 1;
@@ -759,11 +799,20 @@ __global__ __launch_bounds__(NW * 64, NW / 4) void attend_many_kernel(AttendArgs
                 fetch(p + 1, p + 1);
                 follow();
                 if (seen(p)) {
-                    f32x16 sc[2];
+                    f32x16 sc[ST];
                     scores(b, sc);
-                    f16x8 pf[4];
-                    weigh(p, sc, pf);
-                    values(b, pf);
+                    if constexpr (PAIR) {
+                        f16x8 mine[2], pf[4];
+                        weigh(p, sc, mine);
+#pragma unroll
+                        for (int s = 0; s < 4; ++s) pf[s] = pbuf[(4 * group + s) * 64 + lane];
+                        values(b, pf);
+                        if (tid == 0) again[(p + 1) & 1] = 0;
+                    } else {
+                        f16x8 pf[4];
+                        weigh(p, sc, pf);
+                        values(b, pf);
+                    }
                 }
                 e_page = settle(p + 1);
                 stage(b ^ 1, b ^ 1, e_page);
@@ -772,7 +821,13 @@ __global__ __launch_bounds__(NW * 64, NW / 4) void attend_many_kernel(AttendArgs
         }
 
         // Outputs: a lane has, for its column, four dims at a time.
-        const float l = l_run + xor_lane(l_run, 32);
+        float l = l_run + xor_lane(l_run, 32);
+        if constexpr (PAIR) {
+            __syncthreads();                     // (also: the buffers may be filled for the next tile)
+            if (half == 0) mbuf[(2 * group + part) * 32 + col] = l;
+            __syncthreads();
+            l = mbuf[2 * group * 32 + col] + mbuf[(2 * group + 1) * 32 + col];
+        }
         if (w.row >= 0) {
             const uint64_t row_at = static_cast<uint64_t>(w.row) * a.heads + w.head;
             const float v_scale = e_ref == kNone ? 0.f : ldexpf(1.f, e_ref);
@@ -786,7 +841,7 @@ __global__ __launch_bounds__(NW * 64, NW / 4) void attend_many_kernel(AttendArgs
                         bf16x4 x;
 #pragma unroll
                         for (int k = 0; k < 4; ++k) x[k] = static_cast<__bf16>((o[e][i + k] * inv) * v_scale);
-                        *reinterpret_cast<bf16x4*>(static_cast<__bf16*>(a.out) + row_at * D + 32 * e + 2 * i + 4 * half) = x;
+                        *reinterpret_cast<bf16x4*>(static_cast<__bf16*>(a.out) + row_at * D + 32 * (ET * part + e) + 2 * i + 4 * half) = x;
                     }
             } else {
                 const uint64_t slot = static_cast<uint64_t>(piece) * a.s.rows * a.heads + row_at;
@@ -795,10 +850,10 @@ __global__ __launch_bounds__(NW * 64, NW / 4) void attend_many_kernel(AttendArgs
                     for (int e = 0; e < ET; ++e)
 #pragma unroll
                         for (int i = 0; i < 16; i += 4)
-                            *reinterpret_cast<float4*>(a.part + slot * D + 32 * e + 2 * i + 4 * half) =
+                            *reinterpret_cast<float4*>(a.part + slot * D + 32 * (ET * part + e) + 2 * i + 4 * half) =
                                 make_float4(o[e][i] * v_scale, o[e][i + 1] * v_scale, o[e][i + 2] * v_scale, o[e][i + 3] * v_scale);
                 }
-                if (half == 0) a.stat[slot] = make_float2(m_run, l);
+                if (half == 0 && part == 0) a.stat[slot] = make_float2(m_run, l);
             }
         }
     }
@@ -910,19 +965,20 @@ Plan plan_many(const qmv_kv_cache& c, const qmv_kv_seqs& s, uint32_t heads, uint
                 static_cast<uint32_t>((pages + pieces - 1) / pieces)};
 }
 
-template <int D, int NW>
+template <int D>
 hipError_t go_many(const AttendArgs& a, const Plan& p, hipStream_t s) {
-    const dim3 grid(a.s.seqs * a.c.kv_heads, p.tiles, p.pieces), block(NW * 64);
-    constexpr uint32_t bytes = 2 * 2 * kPage * D * 2;    // keys and values, f16, twice
+    const dim3 grid(a.s.seqs * a.c.kv_heads, p.tiles, p.pieces), block(512);
+    // keys and values, f16, twice; of pairs also probabilities, maxima, flags
+    constexpr uint32_t bytes = 2 * 2 * kPage * D * 2 + (D == 256 ? 4 * 4 * 64 * 16 + 4 * 2 * 32 * 4 + 16 : 0);
     if (bytes > 65536) {
-        const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(attend_many_kernel<D, NW>),
+        const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(attend_many_kernel<D>),
                                                  hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (e != hipSuccess) return e;
     }
-    hipLaunchKernelGGL((attend_many_kernel<D, NW>), grid, block, bytes, s, a);
+    hipLaunchKernelGGL((attend_many_kernel<D>), grid, block, bytes, s, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.pieces == 1) return e;
-    const uint32_t joins = p.tiles * (32 * NW / 4) < 65535 ? p.tiles * (32 * NW / 4) : 65535;
+    const uint32_t joins = p.tiles * (many_cols(D) / 4) < 65535 ? p.tiles * (many_cols(D) / 4) : 65535;
     hipLaunchKernelGGL((attend_join_kernel<QMV_BF16, D>), dim3(grid.x, joins), dim3(256), 0, s, a);
     return hipGetLastError();
 }
@@ -938,7 +994,7 @@ hipError_t go_few(const AttendArgs& a, const Plan& p, hipStream_t s) {
 }
 
 Plan plan_of(const qmv_kv_cache& c, const qmv_kv_seqs& s, uint32_t dtype, uint32_t heads, uint32_t window) {
-    return is_many(c, s, dtype, heads) ? plan_many(c, s, heads, window, c.head_dim <= 128 ? 256 : 128) : plan_few(c, s, heads, window);
+    return is_many(c, s, dtype, heads) ? plan_many(c, s, heads, window, many_cols(static_cast<int>(c.head_dim))) : plan_few(c, s, heads, window);
 }
 
 }  // namespace
@@ -959,9 +1015,9 @@ hipError_t launch_kv_attend(const qmv_kv_cache& c, const qmv_kv_seqs& s, uint32_
     const AttendArgs a{c, s, q, out, part, reinterpret_cast<float2*>(part + outputs), scale * kLog2e, heads,
                        heads / c.kv_heads, window, p.pieces, p.per};
     if (is_many(c, s, dtype, heads)) {
-        if (c.head_dim == 64) return go_many<64, 8>(a, p, stream);
-        if (c.head_dim == 128) return go_many<128, 8>(a, p, stream);
-        return go_many<256, 4>(a, p, stream);
+        if (c.head_dim == 64) return go_many<64>(a, p, stream);
+        if (c.head_dim == 128) return go_many<128>(a, p, stream);
+        return go_many<256>(a, p, stream);
     }
     if (dtype == QMV_F32) {
         if (c.head_dim == 64) return go_few<QMV_F32, 64>(a, p, stream);
