@@ -24,8 +24,14 @@
 // very k-indexes that V^T p^T takes from it.  So probabilities go from one
 // product to the next in the lane that computed them.
 //
+// Up to four columns (a decode step of four query heads to a key/value head,
+// say) leave room for their digits beside each other: column 4 d + c is digit
+// d of column c, one product takes the place of three, a score is joined by
+// two rotated additions, and the output sums stay apart by digit to the end,
+// one conversion and one multiply-add an output instead of five operations.
+//
 // Work: a workgroup of four waves has 16 columns (query row x head of one
-// key/value head) and a piece of the sequence's pages; each wave takes every
+// key/value head), or 4, and a piece of the sequence's pages; each wave takes every
 // fourth page and keeps its own running maximum, sum and output, joined in
 // shared memory at the end.  The pieces of a sequence are joined by a second
 // kernel, in their order.
@@ -40,7 +46,7 @@ typedef int i32x4 __attribute__((ext_vector_type(4)));
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kPScale = 127.0f * 65536.0f;   // p = 1 as a whole number
-constexpr int kCols = 16;                      // columns of a workgroup
+constexpr int few_cols(bool pack) { return pack ? 4 : 16; }   // columns of a workgroup
 constexpr uint32_t kTarget = 256;              // workgroups that a launch aims at
 
 struct AttendArgs {
@@ -78,6 +84,13 @@ __device__ __forceinline__ float join3(int c0, int c1, int c2) {
 }
 
 __device__ __forceinline__ float xor_lane(float v, int m) { return __shfl_xor(v, m); }
+
+// Sum of the lanes 4, 8 and 12 apart in a row of 16, the same bits in each.
+__device__ __forceinline__ float add_slots(float v) {
+    v += dpp_mov<0x128>(v);  // row_ror:8
+    v += dpp_mov<0x124>(v);  // row_ror:4
+    return v;
+}
 
 // Largest over the lanes 32 apart, and over those 16, 32 and 48 apart.  With
 // both operands alike, a swap leaves one half of the wave (one row of each
@@ -128,14 +141,23 @@ __device__ __forceinline__ Columns columns(const AttendArgs& a, const SeqRows& r
     return o;
 }
 
-template <uint32_t DT, int D>
+template <uint32_t DT, int D, bool PACK>
 __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attend_few_kernel(AttendArgs a) {
     typedef typename Elem<DT>::type T;
+    constexpr int kCols = few_cols(PACK);
+    constexpr int ND = PACK ? 1 : 3;   // digits in a lane
     constexpr int KS = D / 64;     // k-steps of a score tile
     constexpr int ET = D / 16;     // tiles of output dims
     __shared__ float acc[4][kCols][D + 1];
     __shared__ float stat[4][kCols][2];
-    const int lane = threadIdx.x & 63, col = lane & 15, quad = lane >> 4;
+    const int lane = threadIdx.x & 63, quad = lane >> 4;
+    const int lane16 = lane & 15, col = PACK ? lane & 3 : lane16, slot = lane16 >> 2;
+    // packed: this lane's digit, its weight (slot 3: none), the bytes it takes
+    // of pairs of words, and which of them are kept 128 up
+    const float weight = !PACK ? 1.f : (slot == 0 ? 0x1p-16f : (slot == 1 ? 0x1p-8f : (slot == 2 ? 1.f : 0.f)));
+    const uint32_t pick = slot == 3 ? 0x0C0Cu : static_cast<uint32_t>(slot * 0x101 + 0x400);
+    const uint32_t pick_lo = 0x0C0C0000u | pick, pick_hi = (pick << 16) | 0x0C0Cu;
+    const uint32_t lift = slot < 2 ? 0x80808080u : 0u;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const uint32_t seq = blockIdx.x / a.c.kv_heads, kvh = blockIdx.x % a.c.kv_heads;
     const uint32_t piece = blockIdx.z;
@@ -163,7 +185,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attend_few_kernel(Atten
         i32x4 kf[4][KS];
         int32_t ids = -1, id = -1;
         float kss = 0.f, vss = 0.f;
-        const int krow = 16 * (col >> 2) + (col & 3);
+        const int krow = 16 * (lane16 >> 2) + (lane16 & 3);
         auto look = [&](int32_t p) {
             const int32_t mine = p + 4 * lane;
             ids = mine < p1 ? page_id(a.c, a.s, seq, mine) : -1;
@@ -189,7 +211,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attend_few_kernel(Atten
         look(p0 + wave);
 
         // the query's digits
-        uint32_t qd[KS][3][4];
+        uint32_t qd[KS][ND][4];
         float qs;
         {
             float v[KS][16];
@@ -228,8 +250,12 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attend_few_kernel(Atten
                         x[i] = (zero ? 0 : static_cast<int>(rintf(ldexpf(v[s][4 * j + i], -e) * mul))) + 0x8080;
                     uint32_t d[3];
                     digits4(x, d);
+                    if constexpr (PACK) {
+                        qd[s][0][j] = slot == 0 ? d[0] : (slot == 1 ? d[1] : (slot == 2 ? d[2] : 0u));
+                    } else {
 #pragma unroll
-                    for (int k = 0; k < 3; ++k) qd[s][k][j] = d[k];
+                        for (int k = 0; k < 3; ++k) qd[s][k][j] = d[k];
+                    }
                 }
         }
 
@@ -252,25 +278,28 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attend_few_kernel(Atten
             i32x4 vf[ET];
 #pragma unroll
             for (int e = 0; e < ET; ++e)
-                vf[e] = *reinterpret_cast<const i32x4*>(vp + (16 * e + col) * kPage + 16 * quad);
+                vf[e] = *reinterpret_cast<const i32x4*>(vp + (16 * e + lane16) * kPage + 16 * quad);
             // scores
             float sc[4][4];
-            const float qk = qs * kscale;
+            const float qk = qs * kscale * weight;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                i32x4 c[3];
+                i32x4 c[ND];
 #pragma unroll
-                for (int k = 0; k < 3; ++k) c[k] = i32x4{0, 0, 0, 0};
+                for (int k = 0; k < ND; ++k) c[k] = i32x4{0, 0, 0, 0};
 #pragma unroll
                 for (int s = 0; s < KS; ++s)
 #pragma unroll
-                    for (int k = 0; k < 3; ++k) {
+                    for (int k = 0; k < ND; ++k) {
                         const i32x4 b = {static_cast<int>(qd[s][k][0]), static_cast<int>(qd[s][k][1]),
                                          static_cast<int>(qd[s][k][2]), static_cast<int>(qd[s][k][3])};
                         c[k] = __builtin_amdgcn_mfma_i32_16x16x64_i8(kf[j][s], b, c[k], 0, 0, 0);
                     }
 #pragma unroll
-                for (int i = 0; i < 4; ++i) sc[j][i] = join3(c[0][i], c[1][i], c[2][i]) * qk;
+                for (int i = 0; i < 4; ++i) {
+                    if constexpr (PACK) sc[j][i] = add_slots(static_cast<float>(c[0][i]) * qk);
+                    else sc[j][i] = join3(c[0][i], c[1][i], c[2][i]) * qk;
+                }
             }
             __builtin_amdgcn_sched_barrier(0);
             fetch((n + 1) & 63);
@@ -300,7 +329,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attend_few_kernel(Atten
             // still make the sum NaN, and so does a score of +infinity)
             const float ref = mt > -__builtin_inff() ? mt : 0.f;
             float lt[4] = {0.f, 0.f, 0.f, 0.f};
-            uint32_t pd[3][4];
+            uint32_t pd[ND][4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 uint32_t x[4];
@@ -308,14 +337,18 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attend_few_kernel(Atten
                 for (int i = 0; i < 4; ++i) {
                     const float pr = __builtin_amdgcn_exp2f(sc[j][i] - ref);
                     lt[i] += pr;
-                    // the whole number nearest to p 127 2^16 < 2^23 lies in
-                    // the low bits of its sum with 2^23
-                    x[i] = __builtin_bit_cast(uint32_t, fmaf(pr, kPScale, 0x1p23f)) - (0x4B000000u - 0x8080u);
+                    // the whole number nearest to p 127 2^16 + 0x8080 < 2^23
+                    // is in the low three bytes of its sum with 2^23
+                    x[i] = __builtin_bit_cast(uint32_t, fmaf(pr, kPScale, 0x1p23f + 0x8080));
                 }
-                uint32_t d[3];
-                digits4(x, d);
+                if constexpr (PACK) {
+                    pd[0][j] = (__builtin_amdgcn_perm(x[1], x[0], pick_lo) | __builtin_amdgcn_perm(x[3], x[2], pick_hi)) ^ lift;
+                } else {
+                    uint32_t d[3];
+                    digits4(x, d);
 #pragma unroll
-                for (int k = 0; k < 3; ++k) pd[k][j] = d[k];
+                    for (int k = 0; k < 3; ++k) pd[k][j] = d[k];
+                }
             }
             // Sums (of this lane's tokens; the lanes' are added at the end) are kept relative to the maximum of the first page seen
             // and moved to a larger one only where that is 2^40 away; a page
@@ -333,19 +366,22 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attend_few_kernel(Atten
                     for (int i = 0; i < 4; ++i) o[e][i] *= keep;
             }
             const float add = any ? __builtin_amdgcn_exp2f(ref - m_run) : 0.f;
-            const float put = any ? add * (vscale * (65536.f / kPScale)) : 0.f;
+            const float put = any ? add * (vscale * (65536.f / kPScale)) * weight : 0.f;
             l_run += any ? add * ((lt[0] + lt[1]) + (lt[2] + lt[3])) : 0.f;
 #pragma unroll
             for (int e = 0; e < ET; ++e) {
-                i32x4 c[3];
+                i32x4 c[ND];
 #pragma unroll
-                for (int k = 0; k < 3; ++k) {
+                for (int k = 0; k < ND; ++k) {
                     const i32x4 b = {static_cast<int>(pd[k][0]), static_cast<int>(pd[k][1]),
                                      static_cast<int>(pd[k][2]), static_cast<int>(pd[k][3])};
                     c[k] = __builtin_amdgcn_mfma_i32_16x16x64_i8(vf[e], b, i32x4{0, 0, 0, 0}, 0, 0, 0);
                 }
 #pragma unroll
-                for (int i = 0; i < 4; ++i) o[e][i] = fmaf(join3(c[0][i], c[1][i], c[2][i]), put, o[e][i]);
+                for (int i = 0; i < 4; ++i) {
+                    if constexpr (PACK) o[e][i] = fmaf(static_cast<float>(c[0][i]), put, o[e][i]);
+                    else o[e][i] = fmaf(join3(c[0][i], c[1][i], c[2][i]), put, o[e][i]);
+                }
                 if (e % 4 == 3) __builtin_amdgcn_sched_barrier(0);
             }
         }
@@ -356,8 +392,11 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attend_few_kernel(Atten
 #pragma unroll
         for (int e = 0; e < ET; ++e)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) acc[wave][col][16 * e + 4 * quad + i] = o[e][i];
-        if (quad == 0) {
+            for (int i = 0; i < 4; ++i) {
+                const float v = PACK ? add_slots(o[e][i]) : o[e][i];
+                if (!PACK || slot == 0) acc[wave][col][16 * e + 4 * quad + i] = v;
+            }
+        if (quad == 0 && (!PACK || slot == 0)) {
             stat[wave][col][0] = m_run;
             stat[wave][col][1] = l_run;
         }
@@ -918,10 +957,13 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a) {
 // 2 x 131072 tokens 63 us, two 69, four 75; 32 x 4000 38, 40 and 43.)
 struct Plan {
     uint32_t tiles, pieces, per;
+    bool pack;
 };
 Plan plan_few(const qmv_kv_cache& c, const qmv_kv_seqs& s, uint32_t heads, uint32_t window) {
     const uint64_t group = heads / c.kv_heads;
     const uint64_t most = s.max_new < s.rows ? (s.max_new == 0 ? 1 : s.max_new) : s.rows;
+    const bool pack = most * group <= 4;
+    const uint32_t kCols = few_cols(pack);
     uint64_t tiles = (most * group + kCols - 1) / kCols;
     if (tiles > 8192) tiles = 8192;
     uint64_t span = s.max_len;
@@ -933,7 +975,7 @@ Plan plan_few(const qmv_kv_cache& c, const qmv_kv_seqs& s, uint32_t heads, uint3
     if (pieces > 64) pieces = 64;
     if (pieces < 1) pieces = 1;
     return Plan{static_cast<uint32_t>(tiles), static_cast<uint32_t>(pieces),
-                static_cast<uint32_t>((pages + pieces - 1) / pieces)};
+                static_cast<uint32_t>((pages + pieces - 1) / pieces), pack};
 }
 
 // bfloat16 queries with at least this many columns a sequence go to the
@@ -962,7 +1004,7 @@ Plan plan_many(const qmv_kv_cache& c, const qmv_kv_seqs& s, uint32_t heads, uint
     if (pieces > 64) pieces = 64;
     if (pieces < 1) pieces = 1;
     return Plan{static_cast<uint32_t>(tiles), static_cast<uint32_t>(pieces),
-                static_cast<uint32_t>((pages + pieces - 1) / pieces)};
+                static_cast<uint32_t>((pages + pieces - 1) / pieces), false};
 }
 
 template <int D>
@@ -986,10 +1028,11 @@ hipError_t go_many(const AttendArgs& a, const Plan& p, hipStream_t s) {
 template <uint32_t DT, int D>
 hipError_t go_few(const AttendArgs& a, const Plan& p, hipStream_t s) {
     const dim3 grid(a.s.seqs * a.c.kv_heads, p.tiles, p.pieces), block(256);
-    hipLaunchKernelGGL((attend_few_kernel<DT, D>), grid, block, 0, s, a);
+    if (p.pack) hipLaunchKernelGGL((attend_few_kernel<DT, D, true>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((attend_few_kernel<DT, D, false>), grid, block, 0, s, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.pieces == 1) return e;
-    hipLaunchKernelGGL((attend_join_kernel<DT, D>), dim3(grid.x, p.tiles * (kCols / 4)), block, 0, s, a);
+    hipLaunchKernelGGL((attend_join_kernel<DT, D>), dim3(grid.x, p.tiles * (few_cols(p.pack) / 4)), block, 0, s, a);
     return hipGetLastError();
 }
 
