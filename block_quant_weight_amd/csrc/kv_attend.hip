@@ -136,7 +136,9 @@ __device__ __forceinline__ Columns columns(const AttendArgs& a, const SeqRows& r
     o.head = kvh * a.group + (c - t * a.group);
     o.first_pos = r.base + static_cast<int32_t>(t0);
     o.last_pos = r.base + static_cast<int32_t>(t1);
-    o.hi = max(o.last_pos + 1, 0);
+    // (what a sequence claims past its table is in no page)
+    const uint32_t room = min(a.s.table_stride, 0x7FFF0000u / kPage) * kPage;
+    o.hi = min(max(o.last_pos + 1, 0), static_cast<int32_t>(room));
     o.lo = sees_from(a.window, max(o.first_pos, 0));
     return o;
 }
@@ -350,10 +352,11 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attend_few_kernel(Atten
                     for (int k = 0; k < 3; ++k) pd[k][j] = d[k];
                 }
             }
-            // Sums (of this lane's tokens; the lanes' are added at the end) are kept relative to the maximum of the first page seen
-            // and moved to a larger one only where that is 2^40 away; a page
-            // that this column does not see leaves everything as it is,
-            // whatever its scales are.
+            // Sums (of this lane's tokens; the lanes' are added at the end)
+            // are kept relative to the maximum of the first page seen and
+            // moved to a larger one only where that is 2^40 away; a page that
+            // this column does not see leaves everything as it is, whatever
+            // its scales are.
             const float off = ref - m_run;
             if (__any(any && !(off <= 40.f))) {
                 const float m_new = any && !(off <= 40.f) ? ref : m_run;

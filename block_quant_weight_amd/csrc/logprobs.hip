@@ -7,9 +7,9 @@
 //
 // One pass over the logits, bound by their reading: a workgroup holds a
 // piece of the row in registers and leaves its maximum, S0 and S1 relative
-// to it, and for every group of 128 elements (of 8 or 16 lanes) its best element as
-// one 64-bit key (the value's order, then the lower index).  A second kernel, one
-// workgroup a row, joins the pieces and finds the top n: the n groups with
+// to it, and for every group of 128 elements (of 8 or 16 lanes) its best
+// element as one 64-bit key (the value's order, then the lower index).  A
+// second kernel, one workgroup a row, joins the pieces and finds the top n: the n groups with
 // the best keys hold the n best elements (an element outside them has n
 // better ones, the groups' own bests), so only their elements are read again.
 // Both searches list what reaches a bound that few pass, and place each listed
@@ -94,7 +94,8 @@ __global__ __launch_bounds__(256) void logits_kernel(const float* __restrict__ x
             int at = 0;
 #pragma unroll
             for (int e = E - 1; e >= 0; --e) at = v[e] == m ? e : at;
-            const uint32_t i = first + ((at >> 2) * 256 + tid) * 4 + (at & 3);
+            uint32_t i = first + ((at >> 2) * 256 + tid) * 4 + (at & 3);
+            if (i >= vocab) i = first + tid * 4;   // (NaN before the row's end)
             uint64_t k = i < vocab ? key_of(m, i) : 0;
             k = max64(k, dpp_u64<0xB1>(k));
             k = max64(k, dpp_u64<0x4E>(k));
@@ -345,7 +346,8 @@ hipError_t launch_logprobs(const LogprobArgs& a, void* workspace, hipStream_t s)
     const uint64_t total = uint64_t{pieces} * a.rows;
     Piece* stat = static_cast<Piece*>(workspace);
     uint64_t* keys = a.top != 0 ? reinterpret_cast<uint64_t*>(stat + total) : nullptr;
-    const dim3 grid(static_cast<uint32_t>(total < 0x7FFFFFFFull ? total : 0x7FFFFFFFull)), block(256);
+    // (a launch holds fewer than 2^32 threads)
+    const dim3 grid(static_cast<uint32_t>(total < (1u << 18) ? total : 1u << 18)), block(256);
     if (e == 16)
         hipLaunchKernelGGL(logits_kernel<16>, grid, block, 0, s, a.logits, a.rows, a.vocab, pieces, stat, keys);
     else

@@ -11,6 +11,9 @@
 namespace {
 
 constexpr uint32_t kDimLimit = 1u << 24;
+// Workgroups (of up to 512 threads) along a grid's first axis: a launch holds
+// fewer than 2^32 threads there.
+constexpr uint32_t kGridLimit = 1u << 22;
 
 bool aligned(const void* p, uintptr_t a) {
     return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0;
@@ -34,7 +37,8 @@ int check_kv(const qmv_kv_cache* c, const qmv_kv_seqs* s, uint32_t dtype) {
         return QMV_E_ARG;
     if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) return QMV_E_SHAPE;
     if (c->kv_heads > 65535 || c->pages > 0x7FFFFFFFu || s->rows > 0x7FFF0000u ||
-        uint64_t{s->seqs} * c->kv_heads > 0x7FFFFFFFu || uint64_t{c->pages} * c->kv_heads > 0x7FFFFFFFu)
+        uint64_t{s->seqs} * c->kv_heads > kGridLimit || uint64_t{c->pages} * c->kv_heads > 0x7FFFFFFFu ||
+        uint64_t{s->seqs} * s->table_stride > 0x7FFFFFFFu)
         return QMV_E_SHAPE;
     return QMV_OK;
 }

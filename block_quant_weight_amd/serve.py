@@ -99,6 +99,14 @@ def _dtype(t, what):
     raise TypeError(f"{what} must be float32 or bfloat16, not {t.dtype}")
 
 
+def _scratch(nbytes, stream):
+    """A workspace that a call allocates itself, in the order of its stream."""
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+    with torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream))):
+        return torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+
+
 def workspace(nbytes, device="cuda"):
     """A scratch tensor of nbytes for the calls that take one (never empty)."""
     return torch.empty(max(int(nbytes), 16), dtype=torch.uint8, device=device)
@@ -118,6 +126,7 @@ class KvCache:
         if tuple(k_scale.shape) != tuple(k.shape[:2]) or tuple(v_scale.shape) != tuple(k.shape[:2]):
             raise ValueError("the scales must be [pages, kv_heads]")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.device = k.get_device()
         n = k.numel()
         self.c = _Cache(_dev(k, torch.int8, n, "k"), _dev(v, torch.int8, n, "v"),
                         _dev(k_scale, torch.float32, 0, "k_scale"),
@@ -145,14 +154,18 @@ class KvSeqs:
             raise ValueError("table must be [seqs, table_stride]")
         self.seqs = table.shape[0]
         self.table, self.len, self.start = table, len, start
+        self.device = table.get_device()
         self.c = _Seqs(_dev(table, torch.int32, table.numel(), "table"),
                        _dev(len, torch.int32, self.seqs, "len"),
                        _dev(start, torch.int32, self.seqs + 1, "start"),
                        self.seqs, table.shape[1], 0, int(max_new), int(max_len))
 
 
-def _rows(seqs, t, heads, dim, what):
-    """A call's own copy of seqs with the rows of t [rows, heads, dim], and t's elements."""
+def _rows(cache, seqs, t, heads, what):
+    """A call's own copy of seqs with the rows of t [rows, heads, head_dim], and t's elements."""
+    dim = cache.head_dim
+    if cache.device != _device() or seqs.device != cache.device:
+        raise ValueError("the cache or the sequences are not on the current device")
     if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
         raise ValueError(f"{what} must be [rows, {heads}, {dim}]")
     c = _Seqs.from_buffer_copy(seqs.c)
@@ -185,7 +198,7 @@ def qmv_rms_norm(x, w, eps, res=None, sum=None, y=None, q=None, d=None, stream=N
 def qmv_kv_write(cache: KvCache, seqs: KvSeqs, k, v, stream=None):
     """k, v: float32 or bfloat16 [rows, kv_heads, head_dim]: the rows of seqs into the cache."""
     dt = _dtype(k, "k")
-    ref, n = _rows(seqs, k, cache.kv_heads, cache.head_dim, "k")
+    ref, n = _rows(cache, seqs, k, cache.kv_heads, "k")
     _check(lib().qmv_kv_write(cache.ref, ref, dt, _dev(k, k.dtype, n, "k"),
                               _dev(v, k.dtype, n, "v"), _stream(stream)), "qmv_kv_write")
 
@@ -197,7 +210,7 @@ def qmv_kv_read(cache: KvCache, seqs: KvSeqs, k=None, v=None, stream=None):
     if t is None:
         raise QmvError(QMV_E_ARG, "qmv_kv_read")
     dt = _dtype(t, "k or v")
-    ref, n = _rows(seqs, t, cache.kv_heads, cache.head_dim, "k or v")
+    ref, n = _rows(cache, seqs, t, cache.kv_heads, "k or v")
     _check(lib().qmv_kv_read(cache.ref, ref, dt, None if k is None else _dev(k, t.dtype, n, "k"),
                              None if v is None else _dev(v, t.dtype, n, "v"), _stream(stream)),
            "qmv_kv_read")
@@ -209,7 +222,7 @@ def qmv_kv_attend_workspace(cache: KvCache, seqs: KvSeqs, q, window=0) -> int:
     dt = _dtype(q, "q")
     if q.dim() != 3:
         raise ValueError("q must be [rows, heads, head_dim]")
-    ref, _ = _rows(seqs, q, q.shape[1], cache.head_dim, "q")
+    ref, _ = _rows(cache, seqs, q, q.shape[1], "q")
     _check(lib().qmv_kv_attend_workspace(cache.ref, ref, dt, q.shape[1], window,
                                          ctypes.byref(out)), "qmv_kv_attend_workspace")
     return out.value
@@ -219,19 +232,17 @@ def qmv_kv_attend(cache: KvCache, seqs: KvSeqs, q, out, scale=None, window=0, wo
                   stream=None):
     """q, out: float32 or bfloat16 [rows, heads, head_dim]; scale defaults to
     head_dim ** -0.5.  workspace: a uint8 GPU tensor of at least
-    qmv_kv_attend_workspace bytes; None allocates one, for use on the current
+    qmv_kv_attend_workspace bytes; None allocates one in the order of the
     stream."""
     dt = _dtype(q, "q")
     if q.dim() != 3:
         raise ValueError("q must be [rows, heads, head_dim]")
     heads = q.shape[1]
-    ref, n = _rows(seqs, q, heads, cache.head_dim, "q")
+    ref, n = _rows(cache, seqs, q, heads, "q")
     if workspace is None:
         nbytes = qmv_kv_attend_workspace(cache, seqs, q, window)
         if nbytes:
-            workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
-            if stream is not None and hasattr(stream, "cuda_stream"):
-                workspace.record_stream(stream)
+            workspace = _scratch(nbytes, stream)
     pw, nw = (None, 0) if workspace is None else (_dev(workspace, torch.uint8, 0, "workspace"),
                                                   workspace.numel())
     _check(lib().qmv_kv_attend(cache.ref, ref, dt, heads,
@@ -265,10 +276,7 @@ def qmv_logprobs(logits, ids=None, lp=None, entropy=None, top_ids=None, top_lp=N
             raise ValueError("top_ids must be [rows, top]")
         top = top_ids.shape[1]
     if workspace is None:
-        workspace = torch.empty(max(qmv_logprobs_workspace(rows, vocab, top), 16), dtype=torch.uint8,
-                                device=logits.device)
-        if stream is not None and hasattr(stream, "cuda_stream"):
-            workspace.record_stream(stream)
+        workspace = _scratch(max(qmv_logprobs_workspace(rows, vocab, top), 16), stream)
     f32, i32 = torch.float32, torch.int32
     _check(lib().qmv_logprobs(
         _dev(logits, f32, rows * vocab, "logits"), rows, vocab,

@@ -50,7 +50,7 @@ enum { QMV_F32 = 0, QMV_BF16 = 1 };
  * x, res, sum, y: [rows][cols], w: float32 [cols]; device memory, 16-byte
  * aligned; cols a multiple of 32, at most 2^24; eps >= 0.
  * Errors: QMV_E_ARG (x or w NULL, no output at all, only one of q and d,
- * misaligned pointer, rows 0, eps negative or NaN), QMV_E_SHAPE (cols),
+ * misaligned pointer, rows 0, eps negative, infinite or NaN), QMV_E_SHAPE (cols),
  * QMV_E_DEVICE.
  */
 int qmv_rms_norm(const float *x, const float *res, const float *w, float eps, uint32_t rows,
@@ -92,7 +92,8 @@ typedef struct qmv_kv_cache {
  * of the call's arrays; start is held to 0 .. rows, and rows of no sequence
  * are neither read nor written.  max_new, max_len: the largest count of rows
  * and the largest len among the sequences as far as the host knows; they
- * shape the launch, and results do not depend on them.
+ * shape the launch: results are right whatever they are, and the same bits
+ * for the same ones.
  * A position below 0 (more rows than len), past the table or in a page whose
  * id is outside [0, pages) has no place: nothing is written for it, it reads
  * as zero, and attention leaves it out.
@@ -109,19 +110,21 @@ typedef struct qmv_kv_seqs {
  * cache.  For each page, head and array that new tokens fall into, with amax
  * the largest magnitude of the new values there: need = the least power of
  * two d from 2^-126 with amax <= 127 d (0 if amax is 0; at most 2^121, where
- * codes end at 127); the scale becomes need if the page's first token is among the new ones, else the larger of
- * the old scale and need; earlier tokens' codes become code * old / scale,
+ * codes end at 127); the scale becomes need if the page's first token is among
+ * the new ones, else the larger of the old scale and need; earlier tokens' codes become code * old / scale,
  * and the new codes x / scale, both rounded to the nearest whole number,
  * halves to even.  A growing scale at least doubles, so whatever the order
  * of the writes every stored value stays within one scale of what was
  * written (half a scale if its page's scale did not grow after it).  An
  * infinite or NaN value makes the scale of its page, head and array NaN:
  * everything read from there is NaN until the page is begun anew.
- * Two sequences must not write into one page in the same call.
+ * A call must not write into one page twice, for two sequences or two places
+ * of one table.
  * Errors: QMV_E_ARG (a NULL or misaligned pointer, pages, kv_heads, seqs,
  * table_stride or rows 0, dtype unknown), QMV_E_SHAPE (head_dim, or a size that
- * a launch cannot hold: kv_heads above 65535, seqs * kv_heads or
- * pages * kv_heads of 2^31 or more, rows above 2^31 - 2^16), QMV_E_DEVICE.
+ * a launch cannot hold: kv_heads above 65535, seqs * kv_heads above 2^22,
+ * pages * kv_heads or seqs * table_stride of 2^31 or more, rows above
+ * 2^31 - 2^16), QMV_E_DEVICE.
  */
 int qmv_kv_write(const qmv_kv_cache *cache, const qmv_kv_seqs *seqs, uint32_t dtype, const void *k,
                  const void *v, void *stream);
@@ -144,9 +147,16 @@ int qmv_kv_read(const qmv_kv_cache *cache, const qmv_kv_seqs *seqs, uint32_t dty
  * A row that sees no token gets zeros.  The rows' own tokens have to be in
  * the cache (qmv_kv_write before this call on the stream).  Scores, the
  * softmax's maximum and sums and the output sums are float32 or exact
- * integers; with float32 q the products carry 22 bits of each operand or
- * more.  A query, or a page and head that is seen, with a NaN or infinity
- * gives NaN for the rows that see it and touches no other.
+ * integers.  Queries and probabilities enter the products as whole numbers
+ * of up to 127 2^16 (a row's largest magnitude, a page's largest
+ * probability); with bfloat16 q and 128 query rows and heads or more to a
+ * sequence and key/value head (by max_new) as float16, queries exactly,
+ * probabilities rounded to 11 bits (below 2^-28 of the largest: to 0), and values of a page whose scale is
+ * 2^-20 of the largest before it or less lose low bits.  A query, or a page
+ * and head that is seen, with a NaN or infinity gives NaN for the rows that
+ * see it and touches no other.  Scores past float32's range may give NaN;
+ * values below 2^63 in magnitude never leave it.  Scales of the cache are
+ * taken to be powers of two, 0 or NaN, as qmv_kv_write makes them.
  * workspace: device memory of at least qmv_kv_attend_workspace bytes (may be
  * NULL where that is 0), 16-byte aligned.
  * Errors: QMV_E_ARG (as qmv_kv_write; scale not finite; workspace too small),
@@ -171,8 +181,9 @@ int qmv_kv_attend(const qmv_kv_cache *cache, const qmv_kv_seqs *seqs, uint32_t d
  * top_ids and top_lp are given together, or NULL with top 0.  A logit of
  * -infinity is a token of probability 0.  A row that holds a NaN or
  * +infinity, or nothing but -infinity, gets NaN for lp, entropy and top_lp;
- * its top_ids are then some indexes of the row.  Sums in float32 pieces of
- * at most 32 terms each thread, relative to the largest logit.
+ * its top_ids are then some indexes of the row.  Sums are float32, of at
+ * most 16 terms in each thread and then pairwise, relative to the largest
+ * logit.
  * logits 4-byte aligned, the others 4-byte aligned; workspace: 16-byte
  * aligned, at least qmv_logprobs_workspace bytes.
  * Errors: QMV_E_ARG (logits NULL, no output, ids without lp or n_ids 0,

@@ -141,9 +141,10 @@ def attend(cache, table, lens, start, q, scale, window):
 def attend_bound(b, q, scale, longest, dtype):
     """How far an output may be off.
 
-    A score: the query's digits are off by half of 2^(E-22) with 2^(E-1) <=
-    |q|max, so by 2^-22 |q|max a value; the score's products and its exponent
-    round at most eight times relative to the largest score.  That error d
+    A score: the query's digits are off by half of |q|max / (127 2^16), below
+    2^-22 |q|max a value (bfloat16 queries of many columns are exact); the
+    score's products and its exponent round at most eight times relative to
+    the largest score.  That error d
     changes every p by at most a factor e^d, the quotient by e^2d.  Sums of
     pages: two roundings a page and about twenty others, each 2^-24 of the
     sum.  Probabilities in digits: half of 1 / (127 2^16) < 2^-23.9 each, 64

@@ -325,3 +325,97 @@ def test_refuses_what_it_cannot_take():
         S.qmv_kv_attend(cg, s, torch.zeros(1, 4, 128, device="cuda"), q)
     with pytest.raises(ValueError):
         S.qmv_kv_attend(cg, s, q[0], q)
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("group", [1, 2, 3, 4])
+def test_single_tokens_of_up_to_four_heads(group, dim):
+    """Decode: the columns of one product, over lengths of a page and beside it."""
+    for dtype in ("f32", "bf16"):
+        check([1, 64, 200, 0, 131], [1, 1, 1, 0, 1], 2 * group, 2, dim, dtype, seed=group + dim)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_many_short_sequences(dtype):
+    """More sequences than compute units, some without tokens or rows."""
+    g = np.random.default_rng(11)
+    lens = [int(n) for n in g.integers(0, 140, size=400)]
+    check(lens, [int(n > 0 and n % 7 != 3) for n in lens], 3, 1, 64, dtype, seed=12)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("hints", [(1, 1), (200, 100000), (0, 0), (33, 64)])
+def test_any_hints(hints, dtype):
+    """Hints far from the truth choose another launch, of other tiles and pieces."""
+    check([300, 9, 1500], [9, 9, 1], 4, 1, 64, dtype, seed=13, hints=hints)
+    check([150, 140], [150, 130], 2, 1, 256, dtype, seed=14, hints=hints)
+
+
+@pytest.mark.parametrize("window", [0, 40, 130])
+@pytest.mark.parametrize("lens,news,heads,kv_heads", [
+    ([300, 190], [150, 128], 2, 2), ([130, 70, 600], [129, 70, 45], 12, 4), ([257], [257], 5, 5)])
+def test_wide_heads_of_many_rows(lens, news, heads, kv_heads, window):
+    check(lens, news, heads, kv_heads, 256, "bf16", seed=sum(lens) + window, window=window)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("news", [1, 140])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_maxima_that_grow_and_values_far_apart(dim, news, dtype):
+    """Keys that double from page to page, so that each page's largest score
+    is far above the last one's; values' scales between 2^-40 and 2^40."""
+    g, c, table = make([700], 1, dim, seed=dim + news)
+    for n, page in enumerate(table[0]):
+        c.k_scale[page] = 2.0 ** (n - 11)
+        c.v_scale[page] = 2.0 ** int(g.integers(-40, 41))
+    q = queries(g, news, 2, dim)
+    ref, b = R.attend(c, table, [700], [0, news], q, np.float32(dim ** -0.5), 0)
+    got = attend(to_gpu(c), seqs(table, [700], [0, news]), q, dtype)
+    tol = R.attend_bound(b, q, dim ** -0.5, 700, dtype)
+    if dtype == "bf16":
+        tol = tol + 2.0 ** -8 * (np.abs(ref) + tol)
+    assert np.all(np.abs(got - ref) <= tol)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("scale", [-0.3, 0.0, 2.0])
+def test_any_scale(scale, dtype):
+    check([200, 90], [3, 1], 4, 2, 64, dtype, seed=15, scale=scale)
+    check([260], [140], 2, 2, 128, dtype, seed=16, scale=scale)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("news", [1, 150])
+def test_length_past_the_table(news, dtype):
+    """A sequence that claims 2^31 - 1 tokens of a table of four pages: its
+    rows see what is there."""
+    g, c, table = make([256], 2, 64, seed=17)
+    q = queries(g, news, 2, 64)
+    got = attend(to_gpu(c), seqs(table, [2 ** 31 - 1], [0, news], max_len=256), q, dtype)
+    ref, b = R.attend(c, np.repeat(table, news, 0), [256] * news, list(range(news + 1)), q, np.float32(0.125), 0)
+    tol = R.attend_bound(b, q, 0.125, 256, dtype)
+    if dtype == "bf16":
+        tol = tol + 2.0 ** -8 * (np.abs(ref) + tol)
+    assert np.all(np.abs(got - ref) <= tol)
+
+
+def test_device_and_streams(monkeypatch):
+    """A cache of another device is refused; a call on a stream without a
+    workspace allocates one in that stream's order."""
+    import torch
+    g, c, table = make([3000], 1, 64, seed=18)
+    cg, s = to_gpu(c), seqs(table, [3000], [0, 1])
+    qd = torch.from_numpy(queries(g, 1, 4, 64)).cuda()
+    want, got = torch.empty_like(qd), torch.empty_like(qd)
+    assert S.qmv_kv_attend_workspace(cg, s, qd) > 0
+    S.qmv_kv_attend(cg, s, qd, want)
+    st = torch.cuda.Stream()
+    for stream in (st, st.cuda_stream):
+        got.zero_()
+        torch.cuda.synchronize()
+        S.qmv_kv_attend(cg, s, qd, got, stream=stream)
+        st.synchronize()
+        assert torch.equal(got, want)
+    monkeypatch.setattr(cg, "device", 1)
+    with pytest.raises(ValueError, match="device"):
+        S.qmv_kv_attend(cg, s, qd, got)

@@ -202,3 +202,23 @@ def test_refuses_what_it_cannot_take():
         S.qmv_logprobs(x, top_ids=torch.zeros(2, 40, dtype=torch.int32, device="cuda"),
                        top_lp=torch.zeros(2, 40, device="cuda"))
     assert e.value.status == Q.QMV_E_SHAPE
+
+
+@pytest.mark.parametrize("vocab", [1, 3, 5, 100, 2049, 2050])
+def test_nan_at_the_end_of_a_row(vocab):
+    """The top of a row of NaN, or with one last, is still of the row."""
+    g = np.random.default_rng(14)
+    x = g.standard_normal((3, vocab)).astype(np.float32)
+    x[0] = np.nan
+    x[1, -1] = np.nan
+    top = min(vocab, 32)
+    got = run(x, ids_of(g, 3, vocab, 1), top)
+    assert np.all((got["top_ids"] >= 0) & (got["top_ids"] < vocab))
+    assert all(len(set(r)) == top for r in got["top_ids"].tolist())
+    assert np.all(np.isnan(got["top_lp"][:2])) and np.all(np.isfinite(got["top_lp"][2]))
+
+
+def test_more_rows_than_workgroups():
+    g = np.random.default_rng(15)
+    x = g.standard_normal((300001, 40)).astype(np.float32)
+    check(x, ids_of(g, 300001, 40, 1), 3)

@@ -175,3 +175,20 @@ def test_refuses_what_it_cannot_take():
         S.qmv_rms_norm(x, w, EPS, y=x.half())
     with pytest.raises(ValueError):
         S.qmv_rms_norm(x.cpu(), w, EPS, y=x)
+
+
+def test_arrays_past_the_caches():
+    """Arrays of 64 MB and more, and one float4 a thread of rows that do not fill it."""
+    for rows, cols in ((4100, 4096), (2100, 8224)):
+        x, res, w = data(rows, cols, cols)
+        o = run(x, res, w)
+        sel = np.r_[0:9, rows // 2 - 3:rows // 2, rows - 9:rows]
+        check(x[sel], res[sel], w, {k: v[sel] for k, v in o.items()})
+
+
+def test_more_rows_than_workgroups():
+    rows = (1 << 20) + 300
+    x, res, w = data(rows, 32, 5)
+    o = run(x, res, w)
+    sel = np.r_[0:300, (1 << 20) - 2:rows]
+    check(x[sel], res[sel], w, {k: v[sel] for k, v in o.items()})

@@ -128,3 +128,15 @@ def test_logprobs_refusals():
 def test_structs_match_the_header():
     assert ctypes.sizeof(S._Cache) == 48 and ctypes.sizeof(S._Seqs) == 48
     assert S.QMV_KV_PAGE == 64 and (S.QMV_F32, S.QMV_BF16) == (0, 1)
+
+
+def test_launch_limits():
+    """Sizes that a launch, or 32-bit places, cannot hold."""
+    L = S.lib()
+    for c, s in ((dict(kv_heads=4), dict(seqs=(1 << 20) + 1, table_stride=1)),
+                 (dict(pages=1 << 30), {}), ({}, dict(seqs=1 << 20, table_stride=1 << 11)),
+                 ({}, dict(rows=0x7FFF0001))):
+        assert L.qmv_kv_write(cache(**c), seqs(**s), 0, P, P, None) == SHAPE
+        assert L.qmv_kv_read(cache(**c), seqs(**s), 0, P, P, None) == SHAPE
+        assert L.qmv_kv_attend(cache(**c), seqs(**s), 0, 4, 1.0, 0, P, P, P, 1 << 62, None) == SHAPE
+    assert L.qmv_kv_attend(cache(), seqs(rows=1 << 28), 0, 8, 1.0, 0, P, P, P, 1 << 62, None) == SHAPE
