@@ -962,6 +962,12 @@ struct Plan {
     uint32_t tiles, pieces, per;
     bool pack;
 };
+// Pages that a tile of columns may see, as far as the host knows.
+uint64_t span_pages(const qmv_kv_seqs& s, uint32_t window, uint32_t cols) {
+    uint64_t span = s.max_len;
+    if (window != 0 && span > uint64_t{window} + cols) span = uint64_t{window} + cols;
+    return (span + kPage - 1) / kPage + 1;
+}
 Plan plan_few(const qmv_kv_cache& c, const qmv_kv_seqs& s, uint32_t heads, uint32_t window) {
     const uint64_t group = heads / c.kv_heads;
     const uint64_t most = s.max_new < s.rows ? (s.max_new == 0 ? 1 : s.max_new) : s.rows;
@@ -969,9 +975,7 @@ Plan plan_few(const qmv_kv_cache& c, const qmv_kv_seqs& s, uint32_t heads, uint3
     const uint32_t kCols = few_cols(pack);
     uint64_t tiles = (most * group + kCols - 1) / kCols;
     if (tiles > 8192) tiles = 8192;
-    uint64_t span = s.max_len;
-    if (window != 0 && span > uint64_t{window} + kCols) span = uint64_t{window} + kCols;
-    const uint64_t pages = (span + kPage - 1) / kPage + 1;
+    const uint64_t pages = span_pages(s, window, kCols);
     const uint64_t wgs = uint64_t{s.seqs} * c.kv_heads * tiles;
     uint64_t pieces = (kTarget + wgs - 1) / wgs;
     if (pieces > (pages + 7) / 8) pieces = (pages + 7) / 8;
@@ -981,15 +985,26 @@ Plan plan_few(const qmv_kv_cache& c, const qmv_kv_seqs& s, uint32_t heads, uint3
                 static_cast<uint32_t>((pages + pieces - 1) / pieces), pack};
 }
 
-// bfloat16 queries with at least this many columns a sequence go to the
-// kernel for many.  Measured with 32 heads on 8 (four columns a row), us for
-// many / few: 64 columns, 8 sequences of 3000: 40 / 32, one of 16000: 33 / 28;
-// 128 columns: 44 / 44 and 36 / 39; 256 columns: 54 / 77 and 45 / 62.
-constexpr uint32_t kManyCols = 128;
+// bfloat16 queries go to the kernel for many where a sequence has columns
+// enough to be worth tiles of 256 (kManyCols / D; at less the matrix cores
+// multiply zeros) and the launch has work enough that its waves do not wait
+// for each page by themselves: kManyWork, in products of 16 columns with a
+// page, times D.  Measured (us, many / few), sequences x tokens, columns:
+//   D 128, 8 heads: 1 x 2000, 256: 32 / 18; 1 x 16000, 128 and 256: 32 / 36 and
+//     42 / 59; 8 x 3000, 64 and 128: 30 / 25 and 34 / 44; 64 x 1000, 32, 64 and
+//     128: 55 / 37, 59 / 59 and 61 / 105
+//   D 256, 4 heads: 1 x 16000, 128 and 256: 51 / 43 and 53 / 66; 8 x 3000, 128:
+//     47 / 49; 64 x 1000, 32 and 64: 53 / 50 and 54 / 89
+//   D 64, 8 heads: 8 x 3000, 128 and 256: 28 / 25 and 35 / 40; 64 x 1000, 64, 128
+//     and 256: 49 / 31, 49 / 53 and 67 / 107
+constexpr uint64_t kManyCols = 8192;
+constexpr double kManyWork = 2e6;
 
-bool is_many(const qmv_kv_cache& c, const qmv_kv_seqs& s, uint32_t dtype, uint32_t heads) {
-    const uint64_t most = s.max_new < s.rows ? s.max_new : s.rows;
-    return dtype == QMV_BF16 && most * (heads / c.kv_heads) >= kManyCols;
+bool is_many(const qmv_kv_cache& c, const qmv_kv_seqs& s, uint32_t dtype, uint32_t heads, uint32_t window) {
+    const uint64_t most = s.max_new < s.rows ? s.max_new : s.rows, cols = most * (heads / c.kv_heads);
+    if (dtype != QMV_BF16 || cols * c.head_dim < kManyCols) return false;
+    const double products = static_cast<double>(uint64_t{s.seqs} * c.kv_heads) * static_cast<double>((cols + 15) / 16);
+    return products * static_cast<double>(span_pages(s, window, 16)) * c.head_dim >= kManyWork;
 }
 
 Plan plan_many(const qmv_kv_cache& c, const qmv_kv_seqs& s, uint32_t heads, uint32_t window, uint32_t cols) {
@@ -998,9 +1013,7 @@ Plan plan_many(const qmv_kv_cache& c, const qmv_kv_seqs& s, uint32_t heads, uint
     uint64_t tiles = (most * group + cols - 1) / cols;
     if (tiles > 65535) tiles = 65535;
     if (tiles < 1) tiles = 1;
-    uint64_t span = s.max_len;
-    if (window != 0 && span > uint64_t{window} + cols) span = uint64_t{window} + cols;
-    const uint64_t pages = (span + kPage - 1) / kPage + 1;
+    const uint64_t pages = span_pages(s, window, cols);
     const uint64_t wgs = uint64_t{s.seqs} * c.kv_heads * tiles;
     uint64_t pieces = 256 / wgs;
     if (pieces > pages / 8) pieces = pages / 8;
@@ -1040,7 +1053,7 @@ hipError_t go_few(const AttendArgs& a, const Plan& p, hipStream_t s) {
 }
 
 Plan plan_of(const qmv_kv_cache& c, const qmv_kv_seqs& s, uint32_t dtype, uint32_t heads, uint32_t window) {
-    return is_many(c, s, dtype, heads) ? plan_many(c, s, heads, window, many_cols(static_cast<int>(c.head_dim))) : plan_few(c, s, heads, window);
+    return is_many(c, s, dtype, heads, window) ? plan_many(c, s, heads, window, many_cols(static_cast<int>(c.head_dim))) : plan_few(c, s, heads, window);
 }
 
 }  // namespace
@@ -1060,7 +1073,7 @@ hipError_t launch_kv_attend(const qmv_kv_cache& c, const qmv_kv_seqs& s, uint32_
     const uint64_t outputs = uint64_t{p.pieces} * s.rows * heads * c.head_dim;
     const AttendArgs a{c, s, q, out, part, reinterpret_cast<float2*>(part + outputs), scale * kLog2e, heads,
                        heads / c.kv_heads, window, p.pieces, p.per};
-    if (is_many(c, s, dtype, heads)) {
+    if (is_many(c, s, dtype, heads, window)) {
         if (c.head_dim == 64) return go_many<64>(a, p, stream);
         if (c.head_dim == 128) return go_many<128>(a, p, stream);
         return go_many<256>(a, p, stream);
