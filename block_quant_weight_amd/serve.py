@@ -62,22 +62,25 @@ def lib():
     return _lib
 
 
-_device = torch.cuda.current_device
-# The current stream's handle without a Stream object around it (0.1 us, not
-# 3); a torch without it takes the long way.
+# The current device, and its current stream's handle without a Stream object
+# around it (0.1 us, not 3); a torch without them takes the long way.
+_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _stream(stream):
+def _stream(stream, here):
+    """Handle of a call's stream; `here` is the device of its tensors."""
+    now = _device()
+    if here != now:
+        raise ValueError("the tensors are not on the current device")
     if stream is None and _raw_stream is not None:
-        return _raw_stream(_device())
+        return _raw_stream(now)
     return _stream_of(stream)
 
 
-def _dev(t, dtype, numel, what):
-    """Address of a contiguous tensor of the current GPU with at least numel elements."""
-    if (t.dtype is dtype and t.is_cuda and t.is_contiguous() and t.numel() >= numel
-            and t.get_device() == _device()):
+def _dev(t, dtype, numel, what, here):
+    """Address of a contiguous GPU tensor of device `here` with at least numel elements."""
+    if t.dtype is dtype and t.get_device() == here >= 0 and t.is_contiguous() and t.numel() >= numel:
         return t.data_ptr()
     if not t.is_cuda:
         raise ValueError(f"{what} must be a GPU tensor")
@@ -87,7 +90,7 @@ def _dev(t, dtype, numel, what):
         raise ValueError(f"{what} must be contiguous")
     if t.numel() < numel:
         raise ValueError(f"{what} holds {t.numel()} elements, needs {numel}")
-    raise ValueError(f"{what} is not on the current device")
+    raise ValueError(f"{what} is not on the call's device")
 
 
 def _dtype(t, what):
@@ -127,10 +130,10 @@ class KvCache:
             raise ValueError("the scales must be [pages, kv_heads]")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.device = k.get_device()
-        n = k.numel()
-        self.c = _Cache(_dev(k, torch.int8, n, "k"), _dev(v, torch.int8, n, "v"),
-                        _dev(k_scale, torch.float32, 0, "k_scale"),
-                        _dev(v_scale, torch.float32, 0, "v_scale"),
+        n, here = k.numel(), self.device
+        self.c = _Cache(_dev(k, torch.int8, n, "k", here), _dev(v, torch.int8, n, "v", here),
+                        _dev(k_scale, torch.float32, 0, "k_scale", here),
+                        _dev(v_scale, torch.float32, 0, "v_scale", here),
                         self.pages, self.kv_heads, self.head_dim)
         self.ref = ctypes.pointer(self.c)
 
@@ -155,22 +158,24 @@ class KvSeqs:
         self.seqs = table.shape[0]
         self.table, self.len, self.start = table, len, start
         self.device = table.get_device()
-        self.c = _Seqs(_dev(table, torch.int32, table.numel(), "table"),
-                       _dev(len, torch.int32, self.seqs, "len"),
-                       _dev(start, torch.int32, self.seqs + 1, "start"),
+        here = self.device
+        self.c = _Seqs(_dev(table, torch.int32, table.numel(), "table", here),
+                       _dev(len, torch.int32, self.seqs, "len", here),
+                       _dev(start, torch.int32, self.seqs + 1, "start", here),
                        self.seqs, table.shape[1], 0, int(max_new), int(max_len))
 
 
 def _rows(cache, seqs, t, heads, what):
-    """A call's own copy of seqs with the rows of t [rows, heads, head_dim], and t's elements."""
-    dim = cache.head_dim
-    if cache.device != _device() or seqs.device != cache.device:
-        raise ValueError("the cache or the sequences are not on the current device")
+    """A call's own copy of seqs with the rows of t [rows, heads, head_dim],
+    t's elements, and the device."""
+    dim, here = cache.head_dim, cache.device
+    if seqs.device != here:
+        raise ValueError("the sequences are not on the cache's device")
     if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
         raise ValueError(f"{what} must be [rows, {heads}, {dim}]")
     c = _Seqs.from_buffer_copy(seqs.c)
     c.rows = t.shape[0]
-    return ctypes.byref(c), t.numel()
+    return ctypes.byref(c), t.numel(), here
 
 
 def qmv_rms_norm(x, w, eps, res=None, sum=None, y=None, q=None, d=None, stream=None):
@@ -180,27 +185,27 @@ def qmv_rms_norm(x, w, eps, res=None, sum=None, y=None, q=None, d=None, stream=N
     if x.dim() != 2:
         raise ValueError("x must be [rows, cols]")
     rows, cols = x.shape
-    n = rows * cols
+    n, here = rows * cols, x.get_device()
     f32 = torch.float32
     y32 = yb = None
     if y is not None:
         if _dtype(y, "y") == QMV_F32:
-            y32 = _dev(y, f32, n, "y")
+            y32 = _dev(y, f32, n, "y", here)
         else:
-            yb = _dev(y, torch.bfloat16, n, "y")
+            yb = _dev(y, torch.bfloat16, n, "y", here)
     _check(lib().qmv_rms_norm(
-        _dev(x, f32, n, "x"), None if res is None else _dev(res, f32, n, "res"),
-        _dev(w, f32, cols, "w"), eps, rows, cols, None if sum is None else _dev(sum, f32, n, "sum"),
-        y32, yb, None if q is None else _dev(q, torch.int8, n, "q"),
-        None if d is None else _dev(d, f32, n // 32, "d"), _stream(stream)), "qmv_rms_norm")
+        _dev(x, f32, n, "x", here), None if res is None else _dev(res, f32, n, "res", here),
+        _dev(w, f32, cols, "w", here), eps, rows, cols, None if sum is None else _dev(sum, f32, n, "sum", here),
+        y32, yb, None if q is None else _dev(q, torch.int8, n, "q", here),
+        None if d is None else _dev(d, f32, n // 32, "d", here), _stream(stream, here)), "qmv_rms_norm")
 
 
 def qmv_kv_write(cache: KvCache, seqs: KvSeqs, k, v, stream=None):
     """k, v: float32 or bfloat16 [rows, kv_heads, head_dim]: the rows of seqs into the cache."""
     dt = _dtype(k, "k")
-    ref, n = _rows(cache, seqs, k, cache.kv_heads, "k")
-    _check(lib().qmv_kv_write(cache.ref, ref, dt, _dev(k, k.dtype, n, "k"),
-                              _dev(v, k.dtype, n, "v"), _stream(stream)), "qmv_kv_write")
+    ref, n, here = _rows(cache, seqs, k, cache.kv_heads, "k")
+    _check(lib().qmv_kv_write(cache.ref, ref, dt, _dev(k, k.dtype, n, "k", here),
+                              _dev(v, k.dtype, n, "v", here), _stream(stream, here)), "qmv_kv_write")
 
 
 def qmv_kv_read(cache: KvCache, seqs: KvSeqs, k=None, v=None, stream=None):
@@ -210,9 +215,9 @@ def qmv_kv_read(cache: KvCache, seqs: KvSeqs, k=None, v=None, stream=None):
     if t is None:
         raise QmvError(QMV_E_ARG, "qmv_kv_read")
     dt = _dtype(t, "k or v")
-    ref, n = _rows(cache, seqs, t, cache.kv_heads, "k or v")
-    _check(lib().qmv_kv_read(cache.ref, ref, dt, None if k is None else _dev(k, t.dtype, n, "k"),
-                             None if v is None else _dev(v, t.dtype, n, "v"), _stream(stream)),
+    ref, n, here = _rows(cache, seqs, t, cache.kv_heads, "k or v")
+    _check(lib().qmv_kv_read(cache.ref, ref, dt, None if k is None else _dev(k, t.dtype, n, "k", here),
+                             None if v is None else _dev(v, t.dtype, n, "v", here), _stream(stream, here)),
            "qmv_kv_read")
 
 
@@ -222,7 +227,7 @@ def qmv_kv_attend_workspace(cache: KvCache, seqs: KvSeqs, q, window=0) -> int:
     dt = _dtype(q, "q")
     if q.dim() != 3:
         raise ValueError("q must be [rows, heads, head_dim]")
-    ref, _ = _rows(cache, seqs, q, q.shape[1], "q")
+    ref, _, _ = _rows(cache, seqs, q, q.shape[1], "q")
     _check(lib().qmv_kv_attend_workspace(cache.ref, ref, dt, q.shape[1], window,
                                          ctypes.byref(out)), "qmv_kv_attend_workspace")
     return out.value
@@ -238,17 +243,17 @@ def qmv_kv_attend(cache: KvCache, seqs: KvSeqs, q, out, scale=None, window=0, wo
     if q.dim() != 3:
         raise ValueError("q must be [rows, heads, head_dim]")
     heads = q.shape[1]
-    ref, n = _rows(cache, seqs, q, heads, "q")
+    ref, n, here = _rows(cache, seqs, q, heads, "q")
     if workspace is None:
         nbytes = qmv_kv_attend_workspace(cache, seqs, q, window)
         if nbytes:
             workspace = _scratch(nbytes, stream)
-    pw, nw = (None, 0) if workspace is None else (_dev(workspace, torch.uint8, 0, "workspace"),
+    pw, nw = (None, 0) if workspace is None else (_dev(workspace, torch.uint8, 0, "workspace", here),
                                                   workspace.numel())
     _check(lib().qmv_kv_attend(cache.ref, ref, dt, heads,
                                cache.head_dim ** -0.5 if scale is None else scale, window,
-                               _dev(q, q.dtype, n, "q"), _dev(out, q.dtype, n, "out"), pw, nw,
-                               _stream(stream)), "qmv_kv_attend")
+                               _dev(q, q.dtype, n, "q", here), _dev(out, q.dtype, n, "out", here), pw, nw,
+                               _stream(stream, here)), "qmv_kv_attend")
 
 
 def qmv_logprobs_workspace(rows, vocab, top=0) -> int:
@@ -277,13 +282,13 @@ def qmv_logprobs(logits, ids=None, lp=None, entropy=None, top_ids=None, top_lp=N
         top = top_ids.shape[1]
     if workspace is None:
         workspace = _scratch(max(qmv_logprobs_workspace(rows, vocab, top), 16), stream)
-    f32, i32 = torch.float32, torch.int32
+    f32, i32, here = torch.float32, torch.int32, logits.get_device()
     _check(lib().qmv_logprobs(
-        _dev(logits, f32, rows * vocab, "logits"), rows, vocab,
-        None if ids is None else _dev(ids, i32, rows * n, "ids"), n, top,
-        None if lp is None else _dev(lp, f32, rows * n, "lp"),
-        None if entropy is None else _dev(entropy, f32, rows, "entropy"),
-        None if top_ids is None else _dev(top_ids, i32, rows * top, "top_ids"),
-        None if top_lp is None else _dev(top_lp, f32, rows * top, "top_lp"),
-        _dev(workspace, torch.uint8, 0, "workspace"), workspace.numel(), _stream(stream)),
+        _dev(logits, f32, rows * vocab, "logits", here), rows, vocab,
+        None if ids is None else _dev(ids, i32, rows * n, "ids", here), n, top,
+        None if lp is None else _dev(lp, f32, rows * n, "lp", here),
+        None if entropy is None else _dev(entropy, f32, rows, "entropy", here),
+        None if top_ids is None else _dev(top_ids, i32, rows * top, "top_ids", here),
+        None if top_lp is None else _dev(top_lp, f32, rows * top, "top_lp", here),
+        _dev(workspace, torch.uint8, 0, "workspace", here), workspace.numel(), _stream(stream, here)),
         "qmv_logprobs")
