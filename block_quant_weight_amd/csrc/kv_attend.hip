@@ -31,10 +31,11 @@
 // one conversion and one multiply-add an output instead of five operations.
 //
 // Work: a workgroup of four waves has 16 columns (query row x head of one
-// key/value head), or 4, and a piece of the sequence's pages; each wave takes every
-// fourth page and keeps its own running maximum, sum and output, joined in
-// shared memory at the end.  The pieces of a sequence are joined by a second
-// kernel, in their order.
+// key/value head), or 4, and a piece of the sequence's pages; each wave takes
+// every fourth page and keeps its own running maximum, sum and output, joined
+// in shared memory at the end.  The pieces of a sequence are joined by a second
+// kernel, in their order.  Where there are columns enough, each wave has 16 of
+// its own and all of their pages, and nothing is joined.
 #include <type_traits>
 
 #include "kv_common.h"
@@ -46,7 +47,11 @@ typedef int i32x4 __attribute__((ext_vector_type(4)));
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kPScale = 127.0f * 65536.0f;   // p = 1 as a whole number
-constexpr int few_cols(bool pack) { return pack ? 4 : 16; }   // columns of a workgroup
+// How the kernel for few queries deals out its work: a workgroup has 16
+// columns, or 4 whose digits lie beside each other, and its waves share the
+// pages; or each wave has 16 columns and all of their pages.
+enum Few { kWide, kPack, kSolo };
+constexpr int few_cols(Few mode) { return mode == kPack ? 4 : (mode == kWide ? 16 : 64); }   // columns of a workgroup
 constexpr uint32_t kTarget = 256;              // workgroups that a launch aims at
 
 struct AttendArgs {
@@ -143,15 +148,17 @@ __device__ __forceinline__ Columns columns(const AttendArgs& a, const SeqRows& r
     return o;
 }
 
-template <uint32_t DT, int D, bool PACK>
+template <uint32_t DT, int D, Few MODE>
 __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attend_few_kernel(AttendArgs a) {
     typedef typename Elem<DT>::type T;
-    constexpr int kCols = few_cols(PACK);
+    constexpr bool PACK = MODE == kPack, SOLO = MODE == kSolo;
+    constexpr int kCols = PACK ? 4 : 16;
+    constexpr int STEP = SOLO ? 1 : 4;   // waves that share the pages
     constexpr int ND = PACK ? 1 : 3;   // digits in a lane
     constexpr int KS = D / 64;     // k-steps of a score tile
     constexpr int ET = D / 16;     // tiles of output dims
-    __shared__ float acc[4][kCols][D + 1];
-    __shared__ float stat[4][kCols][2];
+    __shared__ float acc[STEP][kCols][SOLO ? 1 : D + 1];
+    __shared__ float stat[STEP][kCols][2];
     const int lane = threadIdx.x & 63, quad = lane >> 4;
     const int lane16 = lane & 15, col = PACK ? lane & 3 : lane16, slot = lane16 >> 2;
     // packed: this lane's digit, its weight (slot 3: none), the bytes it takes
@@ -166,7 +173,10 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attend_few_kernel(Atten
     const SeqRows r = seq_rows(a.s, seq);
     const uint32_t all = static_cast<uint32_t>(r.count) * a.group;
     const uint32_t tiles = (all + kCols - 1) / kCols;
-    for (uint32_t tile = blockIdx.y; tile < tiles; tile += gridDim.y) {
+    // the last tiles see the most: they begin first
+    constexpr uint32_t kOwn = SOLO ? 4 : 1;   // tiles of a workgroup
+    for (uint32_t turn = kOwn * blockIdx.y + (SOLO ? wave : 0); turn < tiles; turn += kOwn * gridDim.y) {
+        const uint32_t tile = tiles - 1 - turn;
         const Columns w = columns<kCols>(a, r, kvh, tile, col);
         // pages of this piece
         const int32_t p_lo = w.lo / kPage, p_hi = (w.hi + kPage - 1) / kPage;
@@ -189,7 +199,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attend_few_kernel(Atten
         float kss = 0.f, vss = 0.f;
         const int krow = 16 * (lane16 >> 2) + (lane16 & 3);
         auto look = [&](int32_t p) {
-            const int32_t mine = p + 4 * lane;
+            const int32_t mine = p + STEP * lane;
             ids = mine < p1 ? page_id(a.c, a.s, seq, mine) : -1;
             if (ids >= 0) {
                 const uint64_t at = static_cast<uint64_t>(ids) * a.c.kv_heads + kvh;
@@ -210,7 +220,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attend_few_kernel(Atten
                     kf[j][s] = *reinterpret_cast<const i32x4*>(kp + 4 * j * D + 64 * s);
         };
         int n = 0;                               // the page's lane
-        look(p0 + wave);
+        look(p0 + (SOLO ? 0 : wave));
 
         // the query's digits
         uint32_t qd[KS][ND][4];
@@ -268,10 +278,10 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attend_few_kernel(Atten
             for (int i = 0; i < 4; ++i) o[e][i] = 0.f;
         float m_run = -__builtin_inff(), l_run = 0.f;
 
-        for (int32_t p = p0 + wave; p < p1; p += 4, n = (n + 1) & 63) {
+        for (int32_t p = p0 + (SOLO ? 0 : wave); p < p1; p += STEP, n = (n + 1) & 63) {
             const int32_t at_id = id;
             const float kscale = read_lane(kss, n) * a.scale_log2, vscale = read_lane(vss, n);
-            if (n == 63) look(p + 4);
+            if (n == 63) look(p + STEP);
             if (at_id < 0) {
                 fetch((n + 1) & 63);
                 continue;
@@ -391,6 +401,24 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attend_few_kernel(Atten
 
         l_run += xor_lane(l_run, 16);
         l_run += xor_lane(l_run, 32);
+        if constexpr (SOLO) {
+            if (w.row >= 0) {
+                const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
+                const uint64_t at = (static_cast<uint64_t>(w.row) * a.heads + w.head) * D + 4 * quad;
+#pragma unroll
+                for (int e = 0; e < ET; ++e) {
+                    const float v[4] = {o[e][0] * inv, o[e][1] * inv, o[e][2] * inv, o[e][3] * inv};
+                    if constexpr (DT == QMV_F32) {
+                        *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at + 16 * e) = make_float4(v[0], v[1], v[2], v[3]);
+                    } else {
+                        typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+                        const bf16x4 x = {static_cast<__bf16>(v[0]), static_cast<__bf16>(v[1]), static_cast<__bf16>(v[2]), static_cast<__bf16>(v[3])};
+                        *reinterpret_cast<bf16x4*>(static_cast<__bf16*>(a.out) + at + 16 * e) = x;
+                    }
+                }
+            }
+            continue;
+        }
         // the four waves' results
 #pragma unroll
         for (int e = 0; e < ET; ++e)
@@ -960,7 +988,7 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a) {
 // 2 x 131072 tokens 63 us, two 69, four 75; 32 x 4000 38, 40 and 43.)
 struct Plan {
     uint32_t tiles, pieces, per;
-    bool pack;
+    Few few;
 };
 // Pages that a tile of columns may see, as far as the host knows.
 uint64_t span_pages(const qmv_kv_seqs& s, uint32_t window, uint32_t cols) {
@@ -968,11 +996,26 @@ uint64_t span_pages(const qmv_kv_seqs& s, uint32_t window, uint32_t cols) {
     if (window != 0 && span > uint64_t{window} + cols) span = uint64_t{window} + cols;
     return (span + kPage - 1) / kPage + 1;
 }
+// Each wave has its own columns where there are waves enough that way: tiles of
+// 16 columns for every SIMD (two for head dims of 64), or for few pages a tile
+// fewer, kSoloPage / D a page.  A wave then makes its queries' digits once, not
+// four waves the same ones, and nothing is joined.  Measured with float32 (us,
+// waves share the pages / each its own), sequences x new of tokens:
+//   D 128, 8 heads: 1 x 8192 of 8192 1517 / 1392, 8 x 300 of 300 72 / 29, 64 x 8
+//     of 1000 38 / 35; 1 head a query head: 1 x 1000 of 1000 (504 tiles) 18 / 26
+//   D 256, 4 heads: 8 x 300 of 300 148 / 42, 1 x 300 of 300 (300 tiles) 33 / 22,
+//     64 x 8 of 8000 (512 tiles) 258 / 348
+//   D 64, 8 heads: 8 x 300 of 300 37 / 16, 64 x 8 of 1000 (1024 tiles) 22 / 26
+constexpr uint64_t kSoloPage = 8192;
 Plan plan_few(const qmv_kv_cache& c, const qmv_kv_seqs& s, uint32_t heads, uint32_t window) {
     const uint64_t group = heads / c.kv_heads;
     const uint64_t most = s.max_new < s.rows ? (s.max_new == 0 ? 1 : s.max_new) : s.rows;
-    const bool pack = most * group <= 4;
-    const uint32_t kCols = few_cols(pack);
+    Few mode = most * group <= 4 ? kPack : kWide;
+    const uint64_t tiles16 = uint64_t{s.seqs} * c.kv_heads * ((most * group + 15) / 16);
+    if (mode == kWide && (tiles16 >= (c.head_dim == 64 ? 2048u : 1024u) ||
+                          tiles16 * c.head_dim >= kSoloPage * span_pages(s, window, 16)))
+        mode = kSolo;
+    const uint32_t kCols = few_cols(mode);
     uint64_t tiles = (most * group + kCols - 1) / kCols;
     if (tiles > 8192) tiles = 8192;
     const uint64_t pages = span_pages(s, window, kCols);
@@ -980,9 +1023,9 @@ Plan plan_few(const qmv_kv_cache& c, const qmv_kv_seqs& s, uint32_t heads, uint3
     uint64_t pieces = (kTarget + wgs - 1) / wgs;
     if (pieces > (pages + 7) / 8) pieces = (pages + 7) / 8;
     if (pieces > 64) pieces = 64;
-    if (pieces < 1) pieces = 1;
+    if (pieces < 1 || mode == kSolo) pieces = 1;
     return Plan{static_cast<uint32_t>(tiles), static_cast<uint32_t>(pieces),
-                static_cast<uint32_t>((pages + pieces - 1) / pieces), pack};
+                static_cast<uint32_t>((pages + pieces - 1) / pieces), mode};
 }
 
 // bfloat16 queries go to the kernel for many where a sequence has columns
@@ -991,20 +1034,22 @@ Plan plan_few(const qmv_kv_cache& c, const qmv_kv_seqs& s, uint32_t heads, uint3
 // for each page by themselves: kManyWork, in products of 16 columns with a
 // page, times D.  Measured (us, many / few), sequences x tokens, columns:
 //   D 128, 8 heads: 1 x 2000, 256: 32 / 18; 1 x 16000, 128 and 256: 32 / 36 and
-//     42 / 59; 8 x 3000, 64 and 128: 30 / 25 and 34 / 44; 64 x 1000, 32, 64 and
-//     128: 55 / 37, 59 / 59 and 61 / 105
-//   D 256, 4 heads: 1 x 16000, 128 and 256: 51 / 43 and 53 / 66; 8 x 3000, 128:
-//     47 / 49; 64 x 1000, 32 and 64: 53 / 50 and 54 / 89
-//   D 64, 8 heads: 8 x 3000, 128 and 256: 28 / 25 and 35 / 40; 64 x 1000, 64, 128
-//     and 256: 49 / 31, 49 / 53 and 67 / 107
-constexpr uint64_t kManyCols = 8192;
+//     42 / 58; 8 x 3000, 64 and 128: 30 / 25 and 34 / 44; 64 x 1000, 64 and 128:
+//     59 / 49 and 61 / 79; whole prompts 2 x 500 27 / 24, 1 x 2000 79 / 119
+//   D 256, 4 heads: 1 x 16000, 128 and 256: 51 / 42 and 53 / 64; 8 x 3000, 128:
+//     46 / 48; 64 x 1000, 64 and 128: 55 / 52 and 60 / 93
+//   D 64, 8 heads: 8 x 3000, 128 and 256: 27 / 25 and 36 / 41; 64 x 1000, 128
+//     and 256: 50 / 42 and 67 / 71; whole prompts 1 x 1000 36 / 27, 1 x 4000 133 / 190
+constexpr uint64_t kManyCols = 16384;
 constexpr double kManyWork = 2e6;
 
 bool is_many(const qmv_kv_cache& c, const qmv_kv_seqs& s, uint32_t dtype, uint32_t heads, uint32_t window) {
     const uint64_t most = s.max_new < s.rows ? s.max_new : s.rows, cols = most * (heads / c.kv_heads);
     if (dtype != QMV_BF16 || cols * c.head_dim < kManyCols) return false;
     const double products = static_cast<double>(uint64_t{s.seqs} * c.kv_heads) * static_cast<double>((cols + 15) / 16);
-    return products * static_cast<double>(span_pages(s, window, 16)) * c.head_dim >= kManyWork;
+    qmv_kv_seqs mean = s;   // the middle row's tokens
+    mean.max_len -= static_cast<uint32_t>(most / 2 < s.max_len ? most / 2 : s.max_len);
+    return products * static_cast<double>(span_pages(mean, window, 16)) * c.head_dim >= kManyWork;
 }
 
 Plan plan_many(const qmv_kv_cache& c, const qmv_kv_seqs& s, uint32_t heads, uint32_t window, uint32_t cols) {
@@ -1020,7 +1065,7 @@ Plan plan_many(const qmv_kv_cache& c, const qmv_kv_seqs& s, uint32_t heads, uint
     if (pieces > 64) pieces = 64;
     if (pieces < 1) pieces = 1;
     return Plan{static_cast<uint32_t>(tiles), static_cast<uint32_t>(pieces),
-                static_cast<uint32_t>((pages + pieces - 1) / pieces), false};
+                static_cast<uint32_t>((pages + pieces - 1) / pieces), kWide};
 }
 
 template <int D>
@@ -1044,11 +1089,12 @@ hipError_t go_many(const AttendArgs& a, const Plan& p, hipStream_t s) {
 template <uint32_t DT, int D>
 hipError_t go_few(const AttendArgs& a, const Plan& p, hipStream_t s) {
     const dim3 grid(a.s.seqs * a.c.kv_heads, p.tiles, p.pieces), block(256);
-    if (p.pack) hipLaunchKernelGGL((attend_few_kernel<DT, D, true>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((attend_few_kernel<DT, D, false>), grid, block, 0, s, a);
+    if (p.few == kPack) hipLaunchKernelGGL((attend_few_kernel<DT, D, kPack>), grid, block, 0, s, a);
+    else if (p.few == kSolo) hipLaunchKernelGGL((attend_few_kernel<DT, D, kSolo>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((attend_few_kernel<DT, D, kWide>), grid, block, 0, s, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.pieces == 1) return e;
-    hipLaunchKernelGGL((attend_join_kernel<DT, D>), dim3(grid.x, p.tiles * (few_cols(p.pack) / 4)), block, 0, s, a);
+    hipLaunchKernelGGL((attend_join_kernel<DT, D>), dim3(grid.x, p.tiles * (few_cols(p.few) / 4)), block, 0, s, a);
     return hipGetLastError();
 }
 

@@ -149,7 +149,7 @@ int qmv_kv_read(const qmv_kv_cache *cache, const qmv_kv_seqs *seqs, uint32_t dty
  * softmax's maximum and sums and the output sums are float32 or exact
  * integers.  Queries and probabilities enter the products as whole numbers
  * of up to 127 2^16 (a row's largest magnitude, a page's largest
- * probability), or, where bfloat16 queries are many (at least 8192 / head_dim
+ * probability), or, where bfloat16 queries are many (at least 16384 / head_dim
  * rows and heads to a sequence and key/value head, in a call of enough work,
  * by max_new and max_len), as float16: queries exactly, probabilities rounded
  * to 11 bits (below 2^-28 of the largest: to 0), and values of a page whose

@@ -419,3 +419,21 @@ def test_device_and_streams(monkeypatch):
     monkeypatch.setattr(cg, "device", 1)
     with pytest.raises(ValueError, match="device"):
         S.qmv_kv_attend(cg, s, qd, got)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_a_wave_for_each_tile(dim, dtype):
+    """Many short pieces: 40 sequences, some without rows, ends inside a tile
+    of 16 columns and inside a workgroup's four."""
+    g = np.random.default_rng(19)
+    lens = [int(n) for n in g.integers(1, 120, size=40)]
+    news = [min(n, int(m)) for n, m in zip(lens, g.integers(0, 40, size=40))]
+    check(lens, news, 5 if dim == 64 else 3, 1, dim, dtype, seed=20)
+    check([130, 20], [130, 20], 4, 4, dim, dtype, seed=21, window=40, hints=(130, 64))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_more_pages_than_a_wave_looks_up_at_once(dtype):
+    """More than 64 pages in one wave."""
+    check([4500], [70], 64, 1, 64, dtype, seed=22, hints=(70, 64))

@@ -32,12 +32,12 @@ def many(request, monkeypatch):
         n, heads, dim = q.shape
         group = heads // c.kv_heads
         # 8192 / dim columns or, whole, at least 256 workgroups' of 256
-        cols = (1 << 18 if window else 1 << 16) if request.param == "whole" else 8192 // dim
+        cols = (1 << 18 if window else 1 << 16) if request.param == "whole" else 16384 // dim
         all_rows = max(n, -(-cols // group))
         # (what chooses the kernel: columns, and products of 16 with a page)
         pages = -(-(min(window + 16, 1 << 24) if window else 1 << 24) // 64) + 1
         cols = all_rows * group
-        assert cols * dim >= 8192 and s.seqs * c.kv_heads * -(-cols // 16) * pages * dim >= 2.4e6
+        assert cols * dim >= 16384 and s.seqs * c.kv_heads * -(-cols // 16) * pages * dim >= 2.4e6
         qd = torch.full((all_rows, heads, dim), float("nan"), dtype=torch.bfloat16, device="cuda")
         qd[:n] = torch.from_numpy(q)
         out = torch.full_like(qd, 5.0)
