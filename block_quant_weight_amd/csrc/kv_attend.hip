@@ -90,8 +90,13 @@ __device__ __forceinline__ float join3(int c0, int c1, int c2) {
 
 __device__ __forceinline__ float xor_lane(float v, int m) { return __shfl_xor(v, m); }
 
-// Sum of the lanes 4, 8 and 12 apart in a row of 16, the same bits in each.
-__device__ __forceinline__ float add_slots(float v) {
+// Sum of c times w of the lanes 4, 8 and 12 apart in a row of 16, the same
+// bits in each: the products are rounded before they are added (fused, each
+// lane would round the others' alone, and digits that are then made of a sum
+// in different lanes would not be of one number).
+__device__ __forceinline__ float add_slots(float c, float w) {
+#pragma clang fp contract(off)
+    float v = c * w;
     v += dpp_mov<0x128>(v);  // row_ror:8
     v += dpp_mov<0x124>(v);  // row_ror:4
     return v;
@@ -309,7 +314,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attend_few_kernel(Atten
                     }
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    if constexpr (PACK) sc[j][i] = add_slots(static_cast<float>(c[0][i]) * qk);
+                    if constexpr (PACK) sc[j][i] = add_slots(static_cast<float>(c[0][i]), qk);
                     else sc[j][i] = join3(c[0][i], c[1][i], c[2][i]) * qk;
                 }
             }
@@ -424,7 +429,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attend_few_kernel(Atten
         for (int e = 0; e < ET; ++e)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float v = PACK ? add_slots(o[e][i]) : o[e][i];
+                const float v = PACK ? add_slots(o[e][i], 1.f) : o[e][i];
                 if (!PACK || slot == 0) acc[wave][col][16 * e + 4 * quad + i] = v;
             }
         if (quad == 0 && (!PACK || slot == 0)) {

@@ -437,3 +437,11 @@ def test_a_wave_for_each_tile(dim, dtype):
 def test_more_pages_than_a_wave_looks_up_at_once(dtype):
     """More than 64 pages in one wave."""
     check([4500], [70], 64, 1, 64, dtype, seed=22, hints=(70, 64))
+
+
+@pytest.mark.parametrize("dim,scale", [(64, 0.125), (64, 0.5), (128, 0.25), (256, 0.0625)])
+def test_digits_of_a_probability_agree(dim, scale):
+    """Some 800000 probabilities that matter, whose digits are made in
+    different lanes: one whose lanes differ by a last bit next to a border of
+    a digit is off by a hundredth of itself."""
+    check([64] * 400, [1] * 400, 32, 8, dim, "f32", seed=23, scale=scale)
