@@ -129,24 +129,22 @@ __global__ __launch_bounds__(256) void logits_kernel(const float* __restrict__ x
     }
 }
 
-// The largest u with at least n of the set lanes' values >= u (0 if fewer
-// than n lanes are set), from the highest bit down.
-__device__ __forceinline__ uint32_t nth_u32(uint32_t v, bool set, uint32_t n) {
-    uint32_t u = 0;
-#pragma unroll 4
-    for (uint32_t bit = 0x80000000u; bit != 0; bit >>= 1)
-        u |= __builtin_popcountll(__ballot(set && v >= (u | bit))) >= static_cast<int>(n) ? bit : 0u;
-    return u;
-}
-// The n-th largest of the wave's 64 keys, 0 if fewer than n are not 0.
+// The n-th largest of the wave's 64 keys (distinct where not 0), 0 if fewer
+// than n are not 0: each lane counts the keys above its own.
 __device__ __forceinline__ uint64_t wave_nth(uint64_t k, uint32_t n) {
-    const uint32_t hi = static_cast<uint32_t>(k >> 32);
-    const uint32_t h = nth_u32(hi, k != 0, n);
-    if (h == 0) return 0;   // (an element's order is never 0)
-    const uint32_t above = __builtin_popcountll(__ballot(hi > h)), with = __builtin_popcountll(__ballot(hi >= h));
-    // equal values: by their indexes
-    const uint32_t l = with == n ? 0 : nth_u32(static_cast<uint32_t>(k), hi == h, n - above);
-    return (static_cast<uint64_t>(h) << 32) | l;
+    const int lo = static_cast<int>(k), hi = static_cast<int>(k >> 32);
+    uint32_t above = 0;
+#pragma unroll
+    for (int i = 0; i < 64; ++i) {
+        const uint64_t o = static_cast<uint64_t>(static_cast<uint32_t>(__builtin_amdgcn_readlane(hi, i))) << 32 |
+                           static_cast<uint32_t>(__builtin_amdgcn_readlane(lo, i));
+        above += o > k ? 1u : 0u;
+    }
+    const uint64_t at = __ballot(above == n - 1 && k != 0);
+    if (at == 0) return 0;
+    const int lane = __builtin_ctzll(at);
+    return static_cast<uint64_t>(static_cast<uint32_t>(__builtin_amdgcn_readlane(hi, lane))) << 32 |
+           static_cast<uint32_t>(__builtin_amdgcn_readlane(lo, lane));
 }
 
 constexpr uint32_t kList = 4096;   // candidates that a workgroup holds
@@ -156,9 +154,10 @@ template <int R>
 __device__ __forceinline__ void collect(const uint64_t (&k)[R], uint64_t from, uint64_t* list, uint32_t* count) {
     uint64_t take[R];
     uint32_t all = 0;
+    if (from == 0) from = 1;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-        take[r] = __ballot(k[r] >= from && k[r] != 0);
+        take[r] = __ballot(k[r] >= from);
         all += __builtin_popcountll(take[r]);
     }
     if (all == 0) return;
@@ -176,42 +175,71 @@ __device__ __forceinline__ void collect(const uint64_t (&k)[R], uint64_t from, u
 }
 
 // The n largest of the list's keys (all distinct), in order, to best: every
-// key's place is the number of larger ones, whatever the list's order.  The
-// list is read eight keys at a time, zeros after its end.
+// key's place is the number of larger ones, whatever the list's order.  Four
+// threads count for two keys, each a quarter of the list eight keys at a time,
+// with zeros after its end.
 __device__ __forceinline__ void place(uint64_t* list, uint32_t count, uint32_t n, uint64_t* best) {
-    const uint32_t end = (count + 7) & ~7u;
-    if (threadIdx.x < end - count) list[count + threadIdx.x] = 0;
+    const uint32_t end = (count + 31) & ~31u, tid = threadIdx.x;
+    if (tid < end - count) list[count + tid] = 0;
     __syncthreads();
-    for (uint32_t i = threadIdx.x; i < count; i += 256) {
-        const uint64_t k = list[i];
-        uint32_t rank = 0;
-        for (uint32_t j = 0; j < end; j += 8) {
+    for (uint32_t base = 0; base < count; base += 128) {
+        const uint32_t i = base + (tid >> 2);
+        const uint64_t k0 = i < count ? list[i] : 0, k1 = i + 64 < count ? list[i + 64] : 0;
+        uint32_t r0 = 0, r1 = 0;
+        for (uint32_t j = 8 * (tid & 3); j < end; j += 32) {
             uint64_t o[8];
 #pragma unroll
             for (int u = 0; u < 8; ++u) o[u] = list[j + u];
 #pragma unroll
-            for (int u = 0; u < 8; ++u) rank += o[u] > k ? 1 : 0;
+            for (int u = 0; u < 8; ++u) {
+                r0 += o[u] > k0 ? 1 : 0;
+                r1 += o[u] > k1 ? 1 : 0;
+            }
         }
-        if (rank < n) best[rank] = k;
+        r0 += dpp_u32<0xB1>(r0);
+        r1 += dpp_u32<0xB1>(r1);
+        r0 += dpp_u32<0x4E>(r0);
+        r1 += dpp_u32<0x4E>(r1);
+        if ((tid & 3) == 0) {
+            if (k0 != 0 && r0 < n) best[r0] = k0;
+            if (k1 != 0 && r1 < n) best[r1] = k1;
+        }
     }
     __syncthreads();
+}
+
+// A group's elements, from one of them: the first, and how far element o is from it.
+template <int E>
+__device__ __forceinline__ uint32_t group_first(uint32_t e) {
+    constexpr uint32_t kStrip = 4 * (kGroup / E);   // elements side by side
+    return e / (256 * E) * (256 * E) + e % 1024 / kStrip * kStrip;
+}
+template <int E>
+__device__ __forceinline__ uint32_t in_group(uint32_t o) {
+    constexpr uint32_t kStrip = 4 * (kGroup / E);
+    return o / kStrip * 1024 + o % kStrip;
 }
 
 template <int E>
 __global__ __launch_bounds__(256) void logprobs_kernel(LogprobArgs a, uint32_t pieces,
                                                        const Piece* __restrict__ stat,
                                                        const uint64_t* __restrict__ keys) {
-    constexpr int R = 8, RE = 10;                 // keys, elements a thread takes at once (20 groups: 10)
+    constexpr int R = 8, RE = 10;                 // keys, elements a thread takes at once (20 groups' in one turn)
     constexpr uint32_t kLanes = kGroup / E;       // lanes of a group
     static_assert(4 * kMaxTop * R + kMaxTop <= kList && kMaxTop * kGroup <= kList, "candidates fit the list");
     __shared__ float red[3][4];
-    __shared__ __attribute__((aligned(16))) uint64_t list[kList + 8];
+    __shared__ __attribute__((aligned(16))) uint64_t list[kList + 32];
     __shared__ uint64_t groups[kMaxTop], best[kMaxTop], bound[4];
     __shared__ uint32_t count;
     const uint64_t row = blockIdx.x;
-    const uint32_t tid = threadIdx.x, wave = tid >> 6;
+    const uint32_t tid = threadIdx.x;
+    const uint32_t wave = static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<int>(tid >> 6)));
     const float* x = a.logits + row * a.vocab;
-    // the groups' keys are on the way while the sums are joined
+    // the first pieces and the groups' keys are on the way together
+    const Piece* st = stat + row * pieces;
+    const Piece none = {-kInf, 0.f, 0.f, 0.f}, own = tid < pieces ? st[tid] : none;
+    int32_t id = -1;
+    if (tid < a.n_ids) id = a.ids[row * a.n_ids + tid];
     const uint64_t* gk = keys + row * pieces * (256 / kLanes);
     const uint32_t n_groups = pieces * (256 / kLanes);
     uint64_t k[R];
@@ -220,23 +248,18 @@ __global__ __launch_bounds__(256) void logprobs_kernel(LogprobArgs a, uint32_t p
         const uint32_t i = r * 256 + tid;
         k[r] = a.top != 0 && i < n_groups ? gk[i] : 0;
     }
-    int32_t id = -1;
-    float xid = 0.f;
-    if (tid < a.n_ids) {
-        id = a.ids[row * a.n_ids + tid];
-        if (id >= 0 && static_cast<uint32_t>(id) < a.vocab) xid = x[id];
-    }
     // the row's maximum and sums
-    const Piece* st = stat + row * pieces;
-    float m = -kInf;
-    for (uint32_t i = tid; i < pieces; i += 256) m = fmaxf(m, st[i].m);
+    float m = own.m;
+    for (uint32_t i = tid + 256; i < pieces; i += 256) m = fmaxf(m, st[i].m);
     m = wave_max_f32(m);
     if ((tid & 63) == 0) red[0][wave] = m;
+    float xid = 0.f;
+    if (id >= 0 && static_cast<uint32_t>(id) < a.vocab) xid = x[id];
     __syncthreads();
     m = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
     float s0 = 0.f, s1 = 0.f;
     for (uint32_t i = tid; i < pieces; i += 256) {
-        const Piece p = st[i];
+        const Piece p = i == tid ? own : st[i];
         // a piece of nothing but -infinity (and NaN) has its sums relative to 0
         const float d = p.m > -kInf ? p.m - m : (p.s0 == 0.f ? -kInf : 0.f);
         const float f = expf(d);
@@ -292,27 +315,46 @@ __global__ __launch_bounds__(256) void logprobs_kernel(LogprobArgs a, uint32_t p
         // the best of the batches before
         if (base != 0 && tid < a.top && groups[tid] != 0) list[atomicAdd(&count, 1)] = groups[tid];
         __syncthreads();
+        // The elements of the first listed groups (there are about four to
+        // each of the n) are fetched while these are placed: a line of 128
+        // bytes a thread.
+        float ahead[2];
+#pragma unroll
+        for (uint32_t u = 0; u < 2; ++u) {
+            const uint32_t i = u * 64 + tid / 4;
+            const uint64_t g = i < count ? list[i] : 0;
+            const uint32_t at = group_first<E>(0xFFFFFFFFu - static_cast<uint32_t>(g)) + in_group<E>(tid % 4 * 32);
+            ahead[u] = x[g != 0 && at < a.vocab ? at : 0];
+        }
         place(list, count, a.top, groups);
+        asm volatile("" ::"v"(ahead[0]), "v"(ahead[1]));
     }
-    // Their elements that reach the last of them.
+    // Their elements that reach the last of them (its value is looked at
+    // first: most are below it).
     const uint64_t last = groups[a.top - 1];
+    const float least = last != 0 ? of_order(static_cast<uint32_t>(last >> 32)) : -kInf;
     if (tid == 0) count = 0;
     __syncthreads();
-    const uint32_t all = a.top * kGroup;
-    for (uint32_t base = 0; base < all; base += 256 * RE) {
+    // (half of the workgroup has a group at a time; lane i knows group i)
+    const uint32_t mine = static_cast<uint32_t>(groups[tid % kMaxTop]), off = in_group<E>(tid % kGroup);
+    for (uint32_t base = 0; base < a.top; base += 2 * RE) {
         uint64_t k[RE];
+        float v[RE];
+        uint32_t index[RE];
 #pragma unroll
         for (int r = 0; r < RE; ++r) {
-            const uint32_t j = base + r * 256 + tid;
-            // the group of a best element: its piece and lanes
-            const uint64_t g = j < all ? groups[j / kGroup] : 0;
-            const uint32_t e = 0xFFFFFFFFu - static_cast<uint32_t>(g);
-            const uint32_t piece = e / (256 * E), lanes = (e % 1024) / (4 * kLanes);
-            const uint32_t o = j % kGroup;
-            const uint32_t index = piece * (256 * E) + (o / (4 * kLanes)) * 1024 + lanes * (4 * kLanes) + o % (4 * kLanes);
-            const bool there = g != 0 && index < a.vocab;
-            const float v = x[there ? index : 0];
-            k[r] = there ? key_of(v, index) : 0;
+            const uint32_t i = base + 2 * r + wave / 2;
+            const uint32_t g = static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(mine), static_cast<int>(i % kMaxTop)));
+            const uint32_t at = group_first<E>(0xFFFFFFFFu - g) + off;
+            // (the rest of a key is never 0)
+            index[r] = i < a.top && g != 0 && at < a.vocab ? at : a.vocab;
+            v[r] = x[index[r] < a.vocab ? index[r] : 0];
+        }
+#pragma unroll
+        for (int r = 0; r < RE; ++r) {
+            const bool may = index[r] < a.vocab && !(v[r] < least);
+            k[r] = 0;
+            if (__any(may) && may) k[r] = key_of(v[r], index[r]);
         }
         collect<RE>(k, last, list, &count);
     }
