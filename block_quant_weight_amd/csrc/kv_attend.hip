@@ -74,16 +74,14 @@ struct AttendArgs {
 };
 
 // Three signed digits of each of four whole numbers |x| <= 127 * 2^16, as
-// dwords of four bytes: x = d0 + 256 d1 + 65536 d2.  Given are x + 0x8080.
-__device__ __forceinline__ void digits4(const uint32_t x[4], uint32_t d[3]) {
-    uint32_t u[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) u[i] = x[i] ^ 0x8080u;
+// dwords of four bytes: x = d0 + 256 d1 + 65536 d2.  Given are u = x + 0x8080,
+// whose lower two bytes are the digits 128 up.
+__device__ __forceinline__ void digits4(const uint32_t u[4], uint32_t d[3]) {
     // bytes 0 of (u0, u1) and (u2, u3), bytes 1, bytes 2
     const uint32_t a = __builtin_amdgcn_perm(u[1], u[0], 0x05010400u);  // b0 b0' b1 b1'
     const uint32_t b = __builtin_amdgcn_perm(u[3], u[2], 0x05010400u);
-    d[0] = __builtin_amdgcn_perm(b, a, 0x05040100u);
-    d[1] = __builtin_amdgcn_perm(b, a, 0x07060302u);
+    d[0] = __builtin_amdgcn_perm(b, a, 0x05040100u) ^ 0x80808080u;
+    d[1] = __builtin_amdgcn_perm(b, a, 0x07060302u) ^ 0x80808080u;
     const uint32_t e = __builtin_amdgcn_perm(u[1], u[0], 0x00000602u);
     const uint32_t f = __builtin_amdgcn_perm(u[3], u[2], 0x06020000u);
     d[2] = __builtin_amdgcn_perm(f, e, 0x07060100u);
@@ -171,6 +169,8 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attend_few_kernel(Atten
     constexpr int ET = D / 16;     // tiles of output dims
     __shared__ float acc[STEP][kCols][SOLO ? 1 : D + 1];
     __shared__ float stat[STEP][kCols][2];
+    __shared__ float4 part[kCols];       // what each wave's output counts for
+    __shared__ uint64_t place[kCols];    // where the column goes (row * heads + head)
     const int lane = threadIdx.x & 63, quad = lane >> 4;
     const int lane16 = lane & 15, col = PACK ? lane & 3 : lane16, slot = lane16 >> 2;
     // packed: this lane's digit, its weight (slot 3: none), the bytes it takes
@@ -210,9 +210,16 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attend_few_kernel(Atten
         int32_t ids = -1, id = -1;
         float kss = 0.f, vss = 0.f;
         const int krow = 16 * (lane16 >> 2) + (lane16 & 3);
-        auto look = [&](int32_t p) {
+        // What the table says (where there is no page its first entry is read
+        // and not used, so that the load waits for no branch).
+        auto entry = [&](int32_t p) {
             const int32_t mine = p + STEP * lane;
-            ids = mine < p1 ? page_id(a.c, a.s, seq, mine) : -1;
+            const bool there = mine < p1;        // (p1 is at most the table's length)
+            const int32_t id = a.s.table[static_cast<uint64_t>(seq) * a.s.table_stride + (there ? mine : 0)];
+            return there ? id : -1;
+        };
+        auto look = [&](int32_t id) {
+            ids = id >= 0 && static_cast<uint32_t>(id) < a.c.pages ? id : -1;
             if (ids >= 0) {
                 const uint64_t at = static_cast<uint64_t>(ids) * a.c.kv_heads + kvh;
                 kss = a.c.k_scale[at];
@@ -231,16 +238,11 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attend_few_kernel(Atten
                 for (int s = 0; s < KS; ++s)
                     kf[j][s] = *reinterpret_cast<const i32x4*>(kp + 4 * j * D + 64 * s);
         };
-        int n = 0;                               // the page's lane
-        look(p0 + (SOLO ? 0 : wave));
-
-        // the query's digits
-        uint32_t qd[KS][ND][4];
-        float qs;
+        // (the query is on the way while the pages are looked up)
+        const int32_t first_entry = entry(p0 + (SOLO ? 0 : wave));
+        float v[KS][16];
         {
-            float v[KS][16];
             const T* qp = static_cast<const T*>(a.q) + (static_cast<uint64_t>(w.row < 0 ? 0 : w.row) * a.heads + w.head) * D;
-            uint32_t m = 0;
 #pragma unroll
             for (int s = 0; s < KS; ++s) {
                 if (w.row >= 0) {
@@ -251,32 +253,47 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attend_few_kernel(Atten
                     for (int i = 0; i < 16; ++i) v[s][i] = 0.f;
                 }
             }
-            fetch(0);
+        }
+        int n = 0;                               // the page's lane
+        look(first_entry);
+        fetch(0);
+
+        // the query's digits
+        uint32_t qd[KS][ND][4];
+        float qs;
+        {
+            uint32_t m = 0;
 #pragma unroll
             for (int s = 0; s < KS; ++s)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) m = max(m, __builtin_bit_cast(uint32_t, v[s][i]) & 0x7FFFFFFFu);
             m = max(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), 16)));
             m = max(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), 32)));
-            const float amax = __builtin_bit_cast(float, m);
-            int e = 0;
-            const bool zero = m == 0 || m >= 0x7F800000u;
-            const float top = zero ? 1.f : frexpf(amax, &e);  // amax = top 2^e
-            const float mul = kPScale / top;
-            qs = m >= 0x7F800000u ? __builtin_nanf("") : (zero ? 0.f : ldexpf(top / 127.f, e));  // 2^16 / (mul 2^-e)
+            const bool none = m >= 0x7F800000u;
+            const float amax = none ? 0.f : __builtin_bit_cast(float, m);
+            qs = none ? __builtin_nanf("") : amax / 127.f;        // 2^16 times the digits' unit
+            // rows that hold no numbers count as 0, and small ones are moved
+            // up first, where 1 / amax is finite
+            const bool low = amax < 0x1p-96f;
+            if (__any(none || low)) {
+#pragma unroll
+                for (int s = 0; s < KS; ++s)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) v[s][i] = none ? 0.f : v[s][i] * (low ? 0x1p64f : 1.f);
+            }
+            const float mul = amax == 0.f ? 0.f : kPScale / (low ? amax * 0x1p64f : amax);
 #pragma unroll
             for (int s = 0; s < KS; ++s)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     uint32_t x[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        x[i] = (zero ? 0 : static_cast<int>(rintf(ldexpf(v[s][4 * j + i], -e) * mul))) + 0x8080;
-                    uint32_t d[3];
-                    digits4(x, d);
+                    for (int i = 0; i < 4; ++i) x[i] = static_cast<int>(rintf(v[s][4 * j + i] * mul)) + 0x8080;
                     if constexpr (PACK) {
-                        qd[s][0][j] = slot == 0 ? d[0] : (slot == 1 ? d[1] : (slot == 2 ? d[2] : 0u));
+                        qd[s][0][j] = (__builtin_amdgcn_perm(x[1], x[0], pick_lo) | __builtin_amdgcn_perm(x[3], x[2], pick_hi)) ^ lift;
                     } else {
+                        uint32_t d[3];
+                        digits4(x, d);
 #pragma unroll
                         for (int k = 0; k < 3; ++k) qd[s][k][j] = d[k];
                     }
@@ -293,7 +310,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attend_few_kernel(Atten
         for (int32_t p = p0 + (SOLO ? 0 : wave); p < p1; p += STEP, n = (n + 1) & 63) {
             const int32_t at_id = id;
             const float kscale = read_lane(kss, n) * a.scale_log2, vscale = read_lane(vss, n);
-            if (n == 63) look(p + STEP);
+            if (n == 63) look(entry(p + STEP));
             if (at_id < 0) {
                 fetch((n + 1) & 63);
                 continue;
@@ -444,29 +461,35 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attend_few_kernel(Atten
             stat[wave][col][1] = l_run;
         }
         __syncthreads();
-        for (int i = threadIdx.x; i < kCols * D; i += 256) {
-            const int cc = i / D, dim = i % D;
+        if (threadIdx.x < kCols) {
+            const int cc = threadIdx.x;
             const uint32_t gc = tile * kCols + cc;
-            if (gc >= all) break;
-            float m = stat[0][cc][0], l = 0.f, v = 0.f;
+            float m = stat[0][cc][0], l = 0.f, f[4];
 #pragma unroll
             for (int u = 1; u < 4; ++u) m = fmaxf(m, stat[u][cc][0]);
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-                const float f = stat[u][cc][0] == m ? 1.f : exp2f(stat[u][cc][0] - m);
-                l += f * stat[u][cc][1];
-                v += f * acc[u][cc][dim];
+                f[u] = stat[u][cc][0] == m ? 1.f : exp2f(stat[u][cc][0] - m);
+                l += f[u] * stat[u][cc][1];
             }
             const uint64_t at = static_cast<uint64_t>(r.first + static_cast<int32_t>(gc / a.group)) * a.heads + kvh * a.group + gc % a.group;
+            const float inv = a.pieces == 1 ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
+            part[cc] = make_float4(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv);
+            place[cc] = at;
+            if (a.pieces != 1 && gc < all) a.stat[static_cast<uint64_t>(piece) * a.s.rows * a.heads + at] = make_float2(m, l);
+        }
+        __syncthreads();
+        const int here = static_cast<int>(min(all - tile * kCols, static_cast<uint32_t>(kCols)));
+        for (int i = threadIdx.x; i < here * D; i += 256) {
+            const int cc = i / D, dim = i % D;
+            const float4 f = part[cc];
+            const float res = (f.x * acc[0][cc][dim] + f.y * acc[1][cc][dim]) + (f.z * acc[2][cc][dim] + f.w * acc[3][cc][dim]);
             if (a.pieces == 1) {
-                const float res = l == 0.f ? 0.f : v / l;
-                if constexpr (DT == QMV_F32) static_cast<float*>(a.out)[at * D + dim] = res;
-                else static_cast<__bf16*>(a.out)[at * D + dim] = static_cast<__bf16>(res);
-            } else {
+                if constexpr (DT == QMV_F32) static_cast<float*>(a.out)[place[cc] * D + dim] = res;
+                else static_cast<__bf16*>(a.out)[place[cc] * D + dim] = static_cast<__bf16>(res);
+            } else if (p0 < p1) {
                 // (of a piece without pages only the statistics are read)
-                const uint64_t slot = static_cast<uint64_t>(piece) * a.s.rows * a.heads + at;
-                if (p0 < p1) a.part[slot * D + dim] = v;
-                if (dim == 0) a.stat[slot] = make_float2(m, l);
+                a.part[(static_cast<uint64_t>(piece) * a.s.rows * a.heads + place[cc]) * D + dim] = res;
             }
         }
         __syncthreads();
@@ -1004,7 +1027,11 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a) {
 // The launch: tiles of 16 columns of a sequence and head, and pieces of its
 // pages, so that every compute unit has a workgroup, with at least two pages
 // for each wave of a piece.  (One workgroup of four waves a compute unit:
-// 2 x 131072 tokens 63 us, two 69, four 75; 32 x 4000 38, 40 and 43.)
+// 2 x 131072 tokens 63 us, two 69, four 75; 32 x 4000 38, 40 and 43.)  Short
+// sequences stay whole, as a second kernel costs more than their pages one
+// after another (one sequence of 8 heads of 128, whole / in pieces: 500 tokens
+// 8.4 / 10.5 us, 1000 11.0 / 10.6; of 2 heads of 64, 1000 7.2 / 8.2, 2000 10.1 /
+// 8.3; of 4 heads of 256, 500 14.0 / 15.2, 1000 19.2 / 15.7).
 struct Plan {
     uint32_t tiles, pieces, per;
     Few few;
@@ -1041,6 +1068,7 @@ Plan plan_few(const qmv_kv_cache& c, const qmv_kv_seqs& s, uint32_t heads, uint3
     const uint64_t wgs = uint64_t{s.seqs} * c.kv_heads * tiles;
     uint64_t pieces = (kTarget + wgs - 1) / wgs;
     if (pieces > (pages + 7) / 8) pieces = (pages + 7) / 8;
+    if (pages <= (c.head_dim == 64 ? 24u : (c.head_dim == 128 ? 17u : 10u))) pieces = 1;
     if (pieces > 64) pieces = 64;
     if (pieces < 1 || mode == kSolo) pieces = 1;
     return Plan{static_cast<uint32_t>(tiles), static_cast<uint32_t>(pieces),
