@@ -971,18 +971,28 @@ __global__ __launch_bounds__(512, 2) void attend_many_kernel(AttendArgs a) {
     }
 }
 
-// Joins the pieces of each column, one wave a column: lane z has piece z's
-// maximum and sum (at most 64 pieces), and the pieces' outputs are added in
-// their order, D / 64 values a lane.
-template <uint32_t DT, int D>
+// Joins the pieces of each column: lane z has piece z's maximum and sum (at
+// most 64 pieces), and the pieces' outputs are added in their order, D / 64
+// values a lane, eight pieces to a trip to memory.  A wave has a column, or,
+// SPLIT, a workgroup has one and its waves a quarter of the pieces each.
+// Pieces from which on a workgroup has one column (one sequence of 32000
+// tokens, 4 heads of 256, both kernels: 36 us with a wave a column, 25 so; 8000
+// of 8 heads of 128 12.9 and 11.8; with fewer pieces no difference).
+constexpr uint32_t kSplitJoin = 9;
+
+template <uint32_t DT, int D, bool SPLIT>
 __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a) {
     constexpr int V = D / 64;
+    __shared__ float quarter[4][D];
     const uint32_t seq = blockIdx.x / a.c.kv_heads, kvh = blockIdx.x % a.c.kv_heads;
     const int lane = threadIdx.x & 63;
+    const uint32_t wave = static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6)));
     const SeqRows r = seq_rows(a.s, seq);
     const uint32_t n = static_cast<uint32_t>(r.count) * a.group;
     const uint64_t step = static_cast<uint64_t>(a.s.rows) * a.heads;
-    for (uint32_t gc = blockIdx.y * 4 + (threadIdx.x >> 6); gc < n; gc += gridDim.y * 4) {
+    const uint32_t each = SPLIT ? (a.pieces + 3) / 4 : a.pieces;
+    const uint32_t from = SPLIT ? wave * each : 0, to = min(from + each, a.pieces);
+    for (uint32_t gc = SPLIT ? blockIdx.y : blockIdx.y * 4 + wave; gc < n; gc += SPLIT ? gridDim.y : gridDim.y * 4) {
         const uint64_t at = static_cast<uint64_t>(r.first + static_cast<int32_t>(gc / a.group)) * a.heads + kvh * a.group + gc % a.group;
         float2 st = make_float2(-__builtin_inff(), 0.f);
         if (static_cast<uint32_t>(lane) < a.pieces) st = a.stat[lane * step + at];
@@ -999,39 +1009,63 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a) {
 #pragma unroll
         for (int i = 0; i < V; ++i) v[i] = 0.f;
         const float* pp = a.part + at * D + lane * V;
-        for (uint32_t z = 0; z < a.pieces; z += 8) {
+        for (uint32_t z = from; z < to; z += 8) {
             float x[8][V];
+            const uint64_t take = used >> z & ((1ull << min(to - z, 8u)) - 1);
 #pragma unroll
             for (int u = 0; u < 8; ++u)
 #pragma unroll
                 for (int i = 0; i < V; ++i)
-                    x[u][i] = (used >> (z + u) & 1) != 0 ? pp[(z + u) * step * D + i] : 0.f;
+                    x[u][i] = (take >> u & 1) != 0 ? pp[(z + u) * step * D + i] : 0.f;
 #pragma unroll
             for (int u = 0; u < 8; ++u) {
                 const float g = read_lane(f, (z + u) & 63);
-                if ((used >> (z + u) & 1) != 0) {
+                if ((take >> u & 1) != 0) {
 #pragma unroll
                     for (int i = 0; i < V; ++i) v[i] = fmaf(g, x[u][i], v[i]);
                 }
             }
         }
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        auto store = [&](int dim, float res) {
+            if constexpr (DT == QMV_F32) static_cast<float*>(a.out)[at * D + dim] = res;
+            else static_cast<__bf16*>(a.out)[at * D + dim] = static_cast<__bf16>(res);
+        };
+        if constexpr (SPLIT) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const float res = l == 0.f ? 0.f : v[i] / l;
-            if constexpr (DT == QMV_F32) static_cast<float*>(a.out)[at * D + lane * V + i] = res;
-            else static_cast<__bf16*>(a.out)[at * D + lane * V + i] = static_cast<__bf16>(res);
+            for (int i = 0; i < V; ++i) quarter[wave][lane * V + i] = v[i];
+            __syncthreads();
+            const int dim = threadIdx.x;
+            if (dim < D) store(dim, ((quarter[0][dim] + quarter[1][dim]) + (quarter[2][dim] + quarter[3][dim])) * inv);
+            __syncthreads();
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i) store(lane * V + i, v[i] * inv);
         }
     }
 }
 
+// Enqueues the join of up to `columns` columns a sequence and head, where there are pieces to join.
+template <uint32_t DT, int D>
+hipError_t join(const AttendArgs& a, uint32_t columns, hipStream_t s) {
+    const uint32_t x = a.s.seqs * a.c.kv_heads;
+    if (a.pieces >= kSplitJoin)
+        hipLaunchKernelGGL((attend_join_kernel<DT, D, true>), dim3(x, columns < 65535 ? columns : 65535), dim3(256), 0, s, a);
+    else if (a.pieces > 1)
+        hipLaunchKernelGGL((attend_join_kernel<DT, D, false>), dim3(x, columns / 4 < 65535 ? (columns + 3) / 4 : 65535), dim3(256), 0, s, a);
+    return hipGetLastError();
+}
+
 // The launch: tiles of 16 columns of a sequence and head, and pieces of its
-// pages, so that every compute unit has a workgroup, with at least two pages
-// for each wave of a piece.  (One workgroup of four waves a compute unit:
-// 2 x 131072 tokens 63 us, two 69, four 75; 32 x 4000 38, 40 and 43.)  Short
-// sequences stay whole, as a second kernel costs more than their pages one
-// after another (one sequence of 8 heads of 128, whole / in pieces: 500 tokens
-// 8.4 / 10.5 us, 1000 11.0 / 10.6; of 2 heads of 64, 1000 7.2 / 8.2, 2000 10.1 /
-// 8.3; of 4 heads of 256, 500 14.0 / 15.2, 1000 19.2 / 15.7).
+// pages, so that every compute unit has a workgroup, with at least one page
+// for each wave of a piece.  (One workgroup of four waves a compute unit: 2 x
+// 131072 tokens 63 us, two 69, four 75; 32 x 4000 38, 40 and 43.  Two pages a
+// wave at least: one sequence of 4000 tokens with 8 heads of 128 11.2 us, with 4
+// of 256 17.6; one: 9.9 and 14.4.)  Short sequences stay whole, as a second
+// kernel costs as much as their pages one after another, and its launch a call
+// more on the host (one sequence, whole / in pieces: 500 tokens of 8 heads of
+// 128 8.0 / 9.9 us, 1000 10.5 / 9.9; 1000 of 2 heads of 64 6.9 / 7.9; 500 of 4
+// heads of 256 13.0 / 14.0).
 struct Plan {
     uint32_t tiles, pieces, per;
     Few few;
@@ -1067,7 +1101,7 @@ Plan plan_few(const qmv_kv_cache& c, const qmv_kv_seqs& s, uint32_t heads, uint3
     const uint64_t pages = span_pages(s, window, kCols);
     const uint64_t wgs = uint64_t{s.seqs} * c.kv_heads * tiles;
     uint64_t pieces = (kTarget + wgs - 1) / wgs;
-    if (pieces > (pages + 7) / 8) pieces = (pages + 7) / 8;
+    if (pieces > (pages + 3) / 4) pieces = (pages + 3) / 4;
     if (pages <= (c.head_dim == 64 ? 24u : (c.head_dim == 128 ? 17u : 10u))) pieces = 1;
     if (pieces > 64) pieces = 64;
     if (pieces < 1 || mode == kSolo) pieces = 1;
@@ -1127,10 +1161,7 @@ hipError_t go_many(const AttendArgs& a, const Plan& p, hipStream_t s) {
     }
     hipLaunchKernelGGL((attend_many_kernel<D>), grid, block, bytes, s, a);
     const hipError_t e = hipGetLastError();
-    if (e != hipSuccess || p.pieces == 1) return e;
-    const uint32_t joins = p.tiles * (many_cols(D) / 4) < 65535 ? p.tiles * (many_cols(D) / 4) : 65535;
-    hipLaunchKernelGGL((attend_join_kernel<QMV_BF16, D>), dim3(grid.x, joins), dim3(256), 0, s, a);
-    return hipGetLastError();
+    return e != hipSuccess ? e : join<QMV_BF16, D>(a, p.tiles * many_cols(D), s);
 }
 
 template <uint32_t DT, int D>
@@ -1139,10 +1170,8 @@ hipError_t go_few(const AttendArgs& a, const Plan& p, hipStream_t s) {
     if (p.few == kPack) hipLaunchKernelGGL((attend_few_kernel<DT, D, kPack>), grid, block, 0, s, a);
     else if (p.few == kSolo) hipLaunchKernelGGL((attend_few_kernel<DT, D, kSolo>), grid, block, 0, s, a);
     else hipLaunchKernelGGL((attend_few_kernel<DT, D, kWide>), grid, block, 0, s, a);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess || p.pieces == 1) return e;
-    hipLaunchKernelGGL((attend_join_kernel<DT, D>), dim3(grid.x, p.tiles * (few_cols(p.few) / 4)), block, 0, s, a);
-    return hipGetLastError();
+    const hipError_t e = hipGetLastError();
+    return e != hipSuccess ? e : join<DT, D>(a, p.tiles * few_cols(p.few), s);
 }
 
 Plan plan_of(const qmv_kv_cache& c, const qmv_kv_seqs& s, uint32_t dtype, uint32_t heads, uint32_t window) {
