@@ -13,7 +13,7 @@
 // the best keys hold the n best elements (an element outside them has n
 // better ones, the groups' own bests), so only their elements are read again.
 // Both searches list what reaches a bound that few pass, and place each listed
-// key by counting the larger ones.
+// key by counting the larger ones.  Rows of up to 8192 are done by one kernel.
 //
 // 64 rows of 248320: 12.3 us for the first kernel, 5.2 TB/s, and 7.0 for the
 // second, a chain of six trips to memory or barriers; one row: 3.1 and 6.8.
@@ -64,7 +64,34 @@ struct Piece {
     float m, s0, s1, pad;
 };
 
-// E values a thread: element (u * 256 + tid) * 4 + c of the piece.
+// E values a thread: element first + (u * 256 + thread) * 4 + c of the row,
+// -infinity past its end.
+template <int E>
+__device__ __forceinline__ void load_piece(const float* p, uint32_t first, uint32_t vocab, float (&v)[E]) {
+#pragma unroll
+    for (int u = 0; u < E / 4; ++u) {
+        const uint32_t i = first + (u * 256 + threadIdx.x) * 4;
+        if (i + 4 <= vocab) {
+            const Float4u t = *reinterpret_cast<const Float4u*>(p + i);
+            v[4 * u] = t.x; v[4 * u + 1] = t.y; v[4 * u + 2] = t.z; v[4 * u + 3] = t.w;
+        } else {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) v[4 * u + c] = i + c < vocab ? p[i + c] : -kInf;
+        }
+    }
+}
+// Key of the first of a thread's elements that has their maximum m (of only
+// NaN and -infinity: of one of them), 0 of a thread without elements.
+template <int E>
+__device__ __forceinline__ uint64_t best_key(const float (&v)[E], float m, uint32_t first, uint32_t vocab) {
+    int at = 0;
+#pragma unroll
+    for (int e = E - 1; e >= 0; --e) at = v[e] == m ? e : at;
+    uint32_t i = first + ((at >> 2) * 256 + threadIdx.x) * 4 + (at & 3);
+    if (i >= vocab) i = first + threadIdx.x * 4;   // (NaN before the row's end)
+    return i < vocab ? key_of(m, i) : 0;
+}
+
 template <int E>
 __global__ __launch_bounds__(256) void logits_kernel(const float* __restrict__ x, uint32_t rows, uint32_t vocab,
                                                      uint32_t pieces, Piece* __restrict__ stat,
@@ -77,29 +104,12 @@ __global__ __launch_bounds__(256) void logits_kernel(const float* __restrict__ x
         const uint32_t first = static_cast<uint32_t>(g % pieces) * (256 * E);
         const float* p = x + row * vocab;
         float v[E];
-#pragma unroll
-        for (int u = 0; u < E / 4; ++u) {
-            const uint32_t i = first + (u * 256 + tid) * 4;
-            if (i + 4 <= vocab) {
-                const Float4u t = *reinterpret_cast<const Float4u*>(p + i);
-                v[4 * u] = t.x; v[4 * u + 1] = t.y; v[4 * u + 2] = t.z; v[4 * u + 3] = t.w;
-            } else {
-#pragma unroll
-                for (int c = 0; c < 4; ++c) v[4 * u + c] = i + c < vocab ? p[i + c] : -kInf;
-            }
-        }
+        load_piece<E>(p, first, vocab, v);
         float m = -kInf;
 #pragma unroll
         for (int e = 0; e < E; ++e) m = fmaxf(m, v[e]);
         if (keys != nullptr) {
-            // the first element that has the thread's maximum (one of only
-            // NaN and -infinity: its first)
-            int at = 0;
-#pragma unroll
-            for (int e = E - 1; e >= 0; --e) at = v[e] == m ? e : at;
-            uint32_t i = first + ((at >> 2) * 256 + tid) * 4 + (at & 3);
-            if (i >= vocab) i = first + tid * 4;   // (NaN before the row's end)
-            uint64_t k = i < vocab ? key_of(m, i) : 0;
+            uint64_t k = best_key<E>(v, m, first, vocab);
             k = max64(k, dpp_u64<0xB1>(k));
             k = max64(k, dpp_u64<0x4E>(k));
             if constexpr (E <= 16) k = max64(k, dpp_u64<0x141>(k));
@@ -370,6 +380,89 @@ __global__ __launch_bounds__(256) void logprobs_kernel(LogprobArgs a, uint32_t p
     }
 }
 
+// Rows of at most 256 E elements, in one kernel: a workgroup has its row in
+// registers, and the bound of the best elements is that of the threads' bests.
+// (One row, this / the two kernels, us: 500 elements 4.3 / 17, 1500 4.9 / 81, as
+// few groups mean many candidates; 4000 6.1 / 8.9, 8000 8.3 / 9.2; 2000 rows of
+// 8000 28 / 30.  Rows longer than 8192 would need more registers than a thread
+// may have for four workgroups a compute unit.)
+template <int E>
+__global__ __launch_bounds__(256) void logprobs_row_kernel(LogprobArgs a) {
+    // (at most n threads of a wave reach the bound)
+    __shared__ __attribute__((aligned(16))) uint64_t list[4 * kMaxTop * E + 32];
+    __shared__ float red[3][4];
+    __shared__ uint64_t best[kMaxTop], bound[4];
+    __shared__ uint32_t count;
+    const uint64_t row = blockIdx.x;
+    const uint32_t tid = threadIdx.x, wave = tid >> 6;
+    const float* x = a.logits + row * a.vocab;
+    int32_t id = -1;
+    if (tid < a.n_ids) id = a.ids[row * a.n_ids + tid];
+    float v[E];
+    load_piece<E>(x, 0, a.vocab, v);
+    float m = -kInf;
+#pragma unroll
+    for (int e = 0; e < E; ++e) m = fmaxf(m, v[e]);
+    if (a.top != 0) {
+        const uint64_t b = wave_nth(best_key<E>(v, m, 0, a.vocab), a.top);
+        if ((tid & 63) == 0) bound[wave] = b;
+        if (tid == 0) count = 0;
+        if (tid < kMaxTop) best[tid] = 0;
+    }
+    m = wave_max_f32(m);
+    if ((tid & 63) == 0) red[0][wave] = m;
+    float xid = 0.f;
+    if (id >= 0 && static_cast<uint32_t>(id) < a.vocab) xid = x[id];
+    __syncthreads();
+    m = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
+    const float ref = m > -kInf ? m : 0.f;
+    float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        const float d = v[e] - ref, t = __expf(d);
+        s0 += t;
+        s1 += d > -kInf ? t * d : 0.f;
+    }
+    s0 = wave_reduce(s0);
+    s1 = wave_reduce(s1);
+    if ((tid & 63) == 0) {
+        red[1][wave] = s0;
+        red[2][wave] = s1;
+    }
+    if (a.top != 0) {
+        const uint64_t from = max64(max64(bound[0], bound[1]), max64(bound[2], bound[3]));
+        const float least = from != 0 ? of_order(static_cast<uint32_t>(from >> 32)) : -kInf;
+        uint64_t k[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const uint32_t i = ((e >> 2) * 256 + tid) * 4 + (e & 3);
+            const bool may = i < a.vocab && !(v[e] < least);
+            k[e] = 0;
+            if (__any(may) && may) k[e] = key_of(v[e], i);
+        }
+        collect<E>(k, from, list, &count);
+    }
+    __syncthreads();
+    s0 = (red[1][0] + red[1][1]) + (red[1][2] + red[1][3]);
+    s1 = (red[2][0] + red[2][1]) + (red[2][2] + red[2][3]);
+    const float ln = s0 > 0.f ? logf(s0) : __builtin_nanf("");
+    if (a.entropy != nullptr && tid == 0) a.entropy[row] = ln - s1 / s0;
+    for (uint32_t i = tid; i < a.n_ids; i += 256) {
+        if (i >= 256) {
+            id = a.ids[row * a.n_ids + i];
+            if (id >= 0 && static_cast<uint32_t>(id) < a.vocab) xid = x[id];
+        }
+        a.lp[row * a.n_ids + i] = id >= 0 && static_cast<uint32_t>(id) < a.vocab ? (xid - m) - ln : 0.f;
+    }
+    if (a.top == 0) return;
+    place(list, count, a.top, best);
+    if (tid < a.top) {
+        const uint64_t k = best[tid];
+        a.top_ids[row * a.top + tid] = static_cast<int32_t>(0xFFFFFFFFu - static_cast<uint32_t>(k));
+        a.top_lp[row * a.top + tid] = (of_order(static_cast<uint32_t>(k >> 32)) - m) - ln;
+    }
+}
+
 // Values a thread of the first kernel holds: 16 (64 x 248320: 13.4 us, 32
 // 13.8, 8 14.9), or 8 where that would leave compute units idle.
 int values(uint64_t rows, uint32_t vocab) {
@@ -385,6 +478,13 @@ uint64_t logprobs_workspace_bytes(uint32_t rows, uint32_t vocab, uint32_t top) {
 }
 
 hipError_t launch_logprobs(const LogprobArgs& a, void* workspace, hipStream_t s) {
+    if (a.vocab <= 8192) {
+        if (a.vocab <= 1024) hipLaunchKernelGGL(logprobs_row_kernel<4>, dim3(a.rows), dim3(256), 0, s, a);
+        else if (a.vocab <= 2048) hipLaunchKernelGGL(logprobs_row_kernel<8>, dim3(a.rows), dim3(256), 0, s, a);
+        else if (a.vocab <= 4096) hipLaunchKernelGGL(logprobs_row_kernel<16>, dim3(a.rows), dim3(256), 0, s, a);
+        else hipLaunchKernelGGL(logprobs_row_kernel<32>, dim3(a.rows), dim3(256), 0, s, a);
+        return hipGetLastError();
+    }
     const int e = values(a.rows, a.vocab);
     const uint32_t per = 256u * e;
     const uint32_t pieces = (a.vocab + per - 1) / per;

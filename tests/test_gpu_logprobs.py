@@ -222,3 +222,17 @@ def test_more_rows_than_workgroups():
     g = np.random.default_rng(15)
     x = g.standard_normal((300001, 40)).astype(np.float32)
     check(x, ids_of(g, 300001, 40, 1), 3)
+
+
+@pytest.mark.parametrize("rows", [3, 700])
+@pytest.mark.parametrize("vocab", [1, 2, 31, 32, 33, 255, 1023, 1024, 1025, 2047, 2048, 2049, 4095, 4096, 4097,
+                                   8191, 8192, 8193])
+def test_rows_around_a_workgroups_size(rows, vocab):
+    """Both sides of the sizes at which a row changes kernels, with values
+    spread, equal, and in order (so that one wave has the best)."""
+    g = np.random.default_rng(vocab)
+    x = (3 * g.standard_normal((rows, vocab))).astype(np.float32)
+    x[0] = 1.5
+    x[1] = np.arange(vocab, dtype=np.float32) / 64
+    x[2, vocab // 2:] = -np.inf if vocab > 1 else 0.0
+    check(x, ids_of(g, rows, vocab, 300 if rows == 3 else 1), min(vocab // 2 if vocab in (2, 31) else vocab, 32))
