@@ -183,7 +183,7 @@ int qmv_kv_attend(const qmv_kv_cache *cache, const qmv_kv_seqs *seqs, uint32_t d
  * -infinity is a token of probability 0.  A row that holds a NaN or
  * +infinity, or nothing but -infinity, gets NaN for lp, entropy and top_lp;
  * its top_ids are then some indexes of the row.  Sums are float32, of at
- * most 16 terms in each thread and then pairwise, relative to the largest
+ * most 32 terms in each thread and then pairwise, relative to the largest
  * logit.
  * logits 4-byte aligned, the others 4-byte aligned; workspace: 16-byte
  * aligned, at least qmv_logprobs_workspace bytes.

@@ -236,3 +236,20 @@ def test_rows_around_a_workgroups_size(rows, vocab):
     x[1] = np.arange(vocab, dtype=np.float32) / 64
     x[2, vocab // 2:] = -np.inf if vocab > 1 else 0.0
     check(x, ids_of(g, rows, vocab, 300 if rows == 3 else 1), min(vocab // 2 if vocab in (2, 31) else vocab, 32))
+
+
+def test_more_pieces_than_workgroups():
+    """90000 rows of three pieces; sampled rows against the reference."""
+    import torch
+    rows, vocab, top = 90000, 8193, 4
+    x = torch.randn(rows, vocab, device="cuda")
+    ids = torch.randint(0, vocab, (rows, 1), device="cuda", dtype=torch.int32)
+    lp, h = torch.empty(rows, 1, device="cuda"), torch.empty(rows, device="cuda")
+    ti, tl = torch.empty(rows, top, dtype=torch.int32, device="cuda"), torch.empty(rows, top, device="cuda")
+    S.qmv_logprobs(x, ids, lp, h, ti, tl)
+    sel = [0, 1, 43690, 65535, 87381, 87382, rows - 2, rows - 1]
+    ref = R.logprobs(x[sel].cpu().numpy(), ids[sel].cpu().numpy(), top)
+    assert np.all(np.abs(lp[sel].cpu().numpy() - ref["lp"]) <= R.logprob_bound(ref, ref["lp"], 3))
+    assert np.all(np.abs(h[sel].cpu().numpy() - ref["entropy"]) <= R.entropy_bound(ref, 3))
+    assert np.array_equal(ti[sel].cpu().numpy(), ref["top_ids"])
+    assert np.all(np.abs(tl[sel].cpu().numpy() - ref["top_lp"]) <= R.logprob_bound(ref, ref["top_lp"], 3))
