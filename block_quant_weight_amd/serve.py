@@ -95,11 +95,12 @@ def _dev(t, dtype, numel, what, here):
 
 def _dtype(t, what):
     """QMV_F32 or QMV_BF16 of a tensor."""
-    if t.dtype == torch.float32:
+    dt = t.dtype
+    if dt is torch.float32:
         return QMV_F32
-    if t.dtype == torch.bfloat16:
+    if dt is torch.bfloat16:
         return QMV_BF16
-    raise TypeError(f"{what} must be float32 or bfloat16, not {t.dtype}")
+    raise TypeError(f"{what} must be float32 or bfloat16, not {dt}")
 
 
 def _scratch(nbytes, stream):
@@ -150,7 +151,8 @@ class KvSeqs:
     table_stride], len int32 [seqs], start int32 [seqs + 1], on the GPU; rows
     of the call's arrays are given by each call's tensors.  max_new and
     max_len, the largest number of rows and of tokens of one sequence, shape
-    the launch only.  One object serves all layers of a step."""
+    the launch only.  One object serves all layers of a step, and all steps of
+    a graph: its tensors are changed in place."""
 
     def __init__(self, table, len, start, max_new, max_len):
         if table.dim() != 2:
@@ -163,28 +165,40 @@ class KvSeqs:
                        _dev(len, torch.int32, self.seqs, "len", here),
                        _dev(start, torch.int32, self.seqs + 1, "start", here),
                        self.seqs, table.shape[1], 0, int(max_new), int(max_len))
+        self.last = (0, ctypes.byref(self.c))
+
+    def with_rows(self, rows):
+        """A reference to these sequences' struct for calls of so many rows
+        (kept for the next call of as many; the struct never changes)."""
+        last = self.last
+        if last[0] != rows:
+            c = _Seqs.from_buffer_copy(self.c)
+            c.rows = rows
+            self.last = last = (rows, ctypes.byref(c))
+        return last[1]
 
 
 def _rows(cache, seqs, t, heads, what):
-    """A call's own copy of seqs with the rows of t [rows, heads, head_dim],
-    t's elements, and the device."""
-    dim, here = cache.head_dim, cache.device
+    """seqs with the rows of t [rows, heads, head_dim] for a call, t's
+    elements, and the device."""
+    here = cache.device
     if seqs.device != here:
         raise ValueError("the sequences are not on the cache's device")
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
-        raise ValueError(f"{what} must be [rows, {heads}, {dim}]")
-    c = _Seqs.from_buffer_copy(seqs.c)
-    c.rows = t.shape[0]
-    return ctypes.byref(c), t.numel(), here
+    shape = t.shape
+    if len(shape) != 3 or shape[1] != heads or shape[2] != cache.head_dim:
+        raise ValueError(f"{what} must be [rows, {heads}, {cache.head_dim}]")
+    rows = shape[0]
+    return seqs.with_rows(rows), rows * heads * cache.head_dim, here
 
 
 def qmv_rms_norm(x, w, eps, res=None, sum=None, y=None, q=None, d=None, stream=None):
     """x, res, sum: float32 [rows, cols]; w: float32 [cols]; y: float32 or
     bfloat16 [rows, cols]; q int8 [rows, cols] with d float32 [rows, cols/32].
     Outputs that are None are not computed; sum may be res or x."""
-    if x.dim() != 2:
+    shape = x.shape
+    if len(shape) != 2:
         raise ValueError("x must be [rows, cols]")
-    rows, cols = x.shape
+    rows, cols = shape
     n, here = rows * cols, x.get_device()
     f32 = torch.float32
     y32 = yb = None
@@ -225,10 +239,10 @@ def qmv_kv_attend_workspace(cache: KvCache, seqs: KvSeqs, q, window=0) -> int:
     """Bytes of workspace that qmv_kv_attend needs for q [rows, heads, head_dim]."""
     out = ctypes.c_uint64(0)
     dt = _dtype(q, "q")
-    if q.dim() != 3:
-        raise ValueError("q must be [rows, heads, head_dim]")
-    ref, _, _ = _rows(cache, seqs, q, q.shape[1], "q")
-    _check(lib().qmv_kv_attend_workspace(cache.ref, ref, dt, q.shape[1], window,
+    shape = q.shape
+    heads = shape[1] if len(shape) == 3 else 0
+    ref, _, _ = _rows(cache, seqs, q, heads, "q")
+    _check(lib().qmv_kv_attend_workspace(cache.ref, ref, dt, heads, window,
                                          ctypes.byref(out)), "qmv_kv_attend_workspace")
     return out.value
 
@@ -240,9 +254,8 @@ def qmv_kv_attend(cache: KvCache, seqs: KvSeqs, q, out, scale=None, window=0, wo
     qmv_kv_attend_workspace bytes; None allocates one in the order of the
     stream."""
     dt = _dtype(q, "q")
-    if q.dim() != 3:
-        raise ValueError("q must be [rows, heads, head_dim]")
-    heads = q.shape[1]
+    shape = q.shape
+    heads = shape[1] if len(shape) == 3 else 0
     ref, n, here = _rows(cache, seqs, q, heads, "q")
     if workspace is None:
         nbytes = qmv_kv_attend_workspace(cache, seqs, q, window)
