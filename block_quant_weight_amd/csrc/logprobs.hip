@@ -112,7 +112,7 @@ __global__ __launch_bounds__(256) void logits_kernel(const float* __restrict__ x
             uint64_t k = best_key<E>(v, m, first, vocab);
             k = max64(k, dpp_u64<0xB1>(k));
             k = max64(k, dpp_u64<0x4E>(k));
-            if constexpr (E <= 16) k = max64(k, dpp_u64<0x141>(k));
+            k = max64(k, dpp_u64<0x141>(k));
             if constexpr (E == 8) k = max64(k, dpp_u64<0x140>(k));
             constexpr int kLanes = kGroup / E;
             if (tid % kLanes == 0) keys[g * (256 / kLanes) + tid / kLanes] = k;

@@ -157,6 +157,8 @@ class KvSeqs:
     def __init__(self, table, len, start, max_new, max_len):
         if table.dim() != 2:
             raise ValueError("table must be [seqs, table_stride]")
+        if max_new < 0 or max_len < 0:
+            raise ValueError("max_new and max_len must not be negative")
         self.seqs = table.shape[0]
         self.table, self.len, self.start = table, len, start
         self.device = table.get_device()
@@ -239,6 +241,8 @@ def qmv_kv_attend_workspace(cache: KvCache, seqs: KvSeqs, q, window=0) -> int:
     """Bytes of workspace that qmv_kv_attend needs for q [rows, heads, head_dim]."""
     out = ctypes.c_uint64(0)
     dt = _dtype(q, "q")
+    if window < 0:
+        raise ValueError("window must not be negative")
     shape = q.shape
     heads = shape[1] if len(shape) == 3 else 0
     ref, _, _ = _rows(cache, seqs, q, heads, "q")
@@ -254,6 +258,8 @@ def qmv_kv_attend(cache: KvCache, seqs: KvSeqs, q, out, scale=None, window=0, wo
     qmv_kv_attend_workspace bytes; None allocates one in the order of the
     stream."""
     dt = _dtype(q, "q")
+    if window < 0:
+        raise ValueError("window must not be negative")
     shape = q.shape
     heads = shape[1] if len(shape) == 3 else 0
     ref, n, here = _rows(cache, seqs, q, heads, "q")

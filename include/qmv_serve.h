@@ -119,7 +119,8 @@ typedef struct qmv_kv_seqs {
  * infinite or NaN value makes the scale of its page, head and array NaN:
  * everything read from there is NaN until the page is begun anew.
  * A call must not write into one page twice, for two sequences or two places
- * of one table.
+ * of one table.  A page's first token is written before or with its others
+ * (what is read of a page that was never begun is whatever its memory holds).
  * Errors: QMV_E_ARG (a NULL or misaligned pointer, pages, kv_heads, seqs,
  * table_stride or rows 0, dtype unknown), QMV_E_SHAPE (head_dim, or a size that
  * a launch cannot hold: kv_heads above 65535, seqs * kv_heads above 2^22,

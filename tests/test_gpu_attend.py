@@ -445,3 +445,34 @@ def test_digits_of_a_probability_agree(dim, scale):
     different lanes: one whose lanes differ by a last bit next to a border of
     a digit is off by a hundredth of itself."""
     check([64] * 400, [1] * 400, 32, 8, dim, "f32", seed=23, scale=scale)
+
+
+def test_refuses_negative_sizes():
+    import torch
+    g, c, table = make([100], 1, 64, seed=25)
+    for new, longest in ((-1, 100), (1, -100)):
+        with pytest.raises(ValueError):
+            seqs(table, [100], [0, 1], new, longest)
+    q = torch.zeros(1, 2, 64, device="cuda")
+    s = seqs(table, [100], [0, 1])
+    with pytest.raises(ValueError):
+        S.qmv_kv_attend(to_gpu(c), s, q, q, window=-1)
+    with pytest.raises(ValueError):
+        S.qmv_kv_attend_workspace(to_gpu(c), s, q, window=-5)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_pages_shared_by_sequences(dtype):
+    """Two sequences with the same first pages, and a page twice in a table."""
+    g, c, table = make([300, 250], 2, 128, seed=26)
+    table[1, :3] = table[0, :3]
+    table[0, 3] = table[0, 1]
+    start, lens = [0, 1, 41], [300, 250]
+    q = queries(g, 41, 6, 128)
+    got = attend(to_gpu(c), seqs(table, lens, start), q, dtype)
+    sc = np.float32(128 ** -0.5)
+    ref, b = R.attend(c, table, lens, start, q, sc, 0)
+    tol = R.attend_bound(b, q, sc, 300, dtype)
+    if dtype == "bf16":
+        tol = tol + 2.0 ** -8 * (np.abs(ref) + tol)
+    assert np.all(np.abs(got - ref) <= tol)
