@@ -526,7 +526,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attend_few_kernel(Atten
 // Measured: a prompt of 8192 with 32 heads on 8 of 128, 582 us, 945 TFLOP/s (a
 // large bfloat16 product: 1360), bound by the matrix cores, the exponentials
 // between their two products and the page's barrier; three pieces of up to 500
-// rows under a window of 1024, 16 heads on 4 of 256, 63 us, 326 TFLOP/s: there
+// rows under a window of 1024, 16 heads on 4 of 256, 60 us, 340 TFLOP/s: there
 // are 160 tiles for 256 compute units, and each operand of a product is read
 // from shared memory for 32 columns alone, as long as the product itself takes.
 
@@ -720,8 +720,10 @@ __global__ __launch_bounds__(512, 2) void attend_many_kernel(AttendArgs a) {
 #pragma unroll
             for (int u = 0; u < PER; ++u) {
                 const int i = tid + u * NT;
+                // (known at compile time but for head dims of 64)
+                const bool keys = UNITS / 2 % NT == 0 ? u * NT < UNITS / 2 : wave * 64 < UNITS / 2;
                 f16x8 x[2];
-                if (wave * 64 + u * NT < UNITS / 2) {
+                if (keys) {
                     codes_to_f16(st[u], __builtin_bit_cast(f16x2, f16_power(0)), __builtin_bit_cast(f16x2, f16_less(0)), x);
                     const int row = i / (D / 16), c = (2 * (i % (D / 16))) ^ swizzle<KC>(row);
                     f16x8* d = kbuf + (kb * kPage + row) * KC;
@@ -753,7 +755,7 @@ __global__ __launch_bounds__(512, 2) void attend_many_kernel(AttendArgs a) {
         // from the compiler, which would keep one for every read in a register.)
         const uint32_t k_row = static_cast<uint32_t>((32 * part + token_of_row(col)) * KC + (half ^ swizzle<KC>(token_of_row(col))));
         const uint32_t v_row = static_cast<uint32_t>((32 * ET * part + col) * 8 + (half ^ swizzle<8>(col)));
-        // Reads of shared memory run kAhead products ahead.
+        // N products whose operands are read from shared memory kAhead ahead.
         auto pipelined = [](auto n) {
             constexpr int kAhead = 6, N = decltype(n)::value;
             __builtin_amdgcn_sched_group_barrier(0x100, kAhead, 0);
@@ -780,7 +782,11 @@ __global__ __launch_bounds__(512, 2) void attend_many_kernel(AttendArgs a) {
                     sc[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kbuf[(from ^ (2 * s)) + 32 * t * KC], qf[s], sc[t], 0, 0, 0);
             pipelined(std::integral_constant<int, ST * QS>{});
         };
-        auto values = [&](int b, const f16x8 (&pf)[4]) {
+        // The values' products; of pairs beside them the next page goes into
+        // shared memory (three pieces of 500 under a window of 1024: 65 us with
+        // one after the other, 62 so; head dims of 128 and 64, whose waves
+        // drift apart by themselves, lose 2 %).
+        auto values = [&](int b, const f16x8 (&pf)[4], int e_page) {
             __builtin_amdgcn_sched_barrier(0);
             uint32_t from = v_row + b * D * 8;
             asm volatile("" : "+v"(from));
@@ -789,7 +795,21 @@ __global__ __launch_bounds__(512, 2) void attend_many_kernel(AttendArgs a) {
 #pragma unroll
                 for (int e = 0; e < ET; ++e)
                     o[e] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vbuf[(from ^ (2 * s)) + 32 * e * 8], pf[s], o[e], 0, 0, 0);
-            pipelined(std::integral_constant<int, 4 * ET>{});
+            if constexpr (PAIR) {
+                constexpr int kAhead = 6, N = 4 * ET, kEach = 24 * PER / N, kStore = N / (2 * PER);
+                stage(b ^ 1, b ^ 1, e_page);
+                __builtin_amdgcn_sched_group_barrier(0x100, kAhead, 0);
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                    if (i < N - kAhead) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x002, kEach, 0);
+                    if (i % kStore == kStore - 1) __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            } else {
+                pipelined(std::integral_constant<int, 4 * ET>{});
+            }
         };
         float fm = 0.f, base = 0.f;              // p = e^(sc fm - base)
         bool begun = false;                      // every column of the wave has a reference
@@ -913,21 +933,23 @@ __global__ __launch_bounds__(512, 2) void attend_many_kernel(AttendArgs a) {
                 if (seen(p)) {
                     f32x16 sc[ST];
                     scores(b, sc);
+                    f16x8 pf[4];
                     if constexpr (PAIR) {
-                        f16x8 mine[2], pf[4];
+                        f16x8 mine[2];
                         weigh(p, sc, mine);
 #pragma unroll
                         for (int s = 0; s < 4; ++s) pf[s] = pbuf[(4 * group + s) * 64 + lane];
-                        values(b, pf);
                         if (tid == 0) again[(p + 1) & 1] = 0;
+                        e_page = settle(p + 1);
                     } else {
-                        f16x8 pf[4];
                         weigh(p, sc, pf);
-                        values(b, pf);
                     }
+                    values(b, pf, e_page);
                 }
-                e_page = settle(p + 1);
-                stage(b ^ 1, b ^ 1, e_page);
+                if (!PAIR || !seen(p)) {
+                    e_page = settle(p + 1);
+                    stage(b ^ 1, b ^ 1, e_page);
+                }
                 __syncthreads();
             }
         }
