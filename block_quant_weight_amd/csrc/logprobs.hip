@@ -18,6 +18,7 @@
 // 64 rows of 248320: 12.3 us for the first kernel, 5.2 TB/s, and 7.0 for the
 // second, a chain of six trips to memory or barriers; one row: 3.1 and 6.8.
 #include "device_common.h"
+#include "logprob_keys.h"
 #include "serve_kernels.h"
 
 namespace qmv {
@@ -26,19 +27,6 @@ namespace {
 constexpr uint32_t kGroup = 128;   // elements of a group: 8 lanes' of 16, or 16 lanes' of 8
 constexpr int kMaxTop = 32;
 constexpr float kInf = __builtin_inff();
-
-// A float's place in the order of the floats (-0 and 0 alike, a NaN at the
-// place of -infinity), and back.
-__device__ __forceinline__ uint32_t order_of(float x) {
-    const uint32_t b = __builtin_bit_cast(uint32_t, x == x ? x + 0.f : -kInf);
-    return (b & 0x80000000u) != 0 ? ~b : b | 0x80000000u;
-}
-__device__ __forceinline__ float of_order(uint32_t u) {
-    return __builtin_bit_cast(float, (u & 0x80000000u) != 0 ? u & 0x7FFFFFFFu : ~u);
-}
-__device__ __forceinline__ uint64_t key_of(float x, uint32_t index) {
-    return (static_cast<uint64_t>(order_of(x)) << 32) | (0xFFFFFFFFu - index);
-}
 
 template <int CTRL>
 __device__ __forceinline__ uint64_t dpp_u64(uint64_t v) {
@@ -70,7 +58,7 @@ template <int E>
 __device__ __forceinline__ void load_piece(const float* p, uint32_t first, uint32_t vocab, float (&v)[E]) {
 #pragma unroll
     for (int u = 0; u < E / 4; ++u) {
-        const uint32_t i = first + (u * 256 + threadIdx.x) * 4;
+        const uint32_t i = index_of(4 * u, threadIdx.x, first);
         if (i + 4 <= vocab) {
             const Float4u t = *reinterpret_cast<const Float4u*>(p + i);
             v[4 * u] = t.x; v[4 * u + 1] = t.y; v[4 * u + 2] = t.z; v[4 * u + 3] = t.w;
@@ -79,17 +67,6 @@ __device__ __forceinline__ void load_piece(const float* p, uint32_t first, uint3
             for (int c = 0; c < 4; ++c) v[4 * u + c] = i + c < vocab ? p[i + c] : -kInf;
         }
     }
-}
-// Key of the first of a thread's elements that has their maximum m (of only
-// NaN and -infinity: of one of them), 0 of a thread without elements.
-template <int E>
-__device__ __forceinline__ uint64_t best_key(const float (&v)[E], float m, uint32_t first, uint32_t vocab) {
-    int at = 0;
-#pragma unroll
-    for (int e = E - 1; e >= 0; --e) at = v[e] == m ? e : at;
-    uint32_t i = first + ((at >> 2) * 256 + threadIdx.x) * 4 + (at & 3);
-    if (i >= vocab) i = first + threadIdx.x * 4;   // (NaN before the row's end)
-    return i < vocab ? key_of(m, i) : 0;
 }
 
 template <int E>
@@ -109,7 +86,7 @@ __global__ __launch_bounds__(256) void logits_kernel(const float* __restrict__ x
 #pragma unroll
         for (int e = 0; e < E; ++e) m = fmaxf(m, v[e]);
         if (keys != nullptr) {
-            uint64_t k = best_key<E>(v, m, first, vocab);
+            uint64_t k = best_key<E>(v, m, tid, first, vocab);
             k = max64(k, dpp_u64<0xB1>(k));
             k = max64(k, dpp_u64<0x4E>(k));
             k = max64(k, dpp_u64<0x141>(k));
@@ -162,8 +139,10 @@ __device__ __forceinline__ uint64_t wave_nth(uint64_t k, uint32_t n) {
 
 constexpr uint32_t kList = 4096;   // candidates that a workgroup holds
 
-// Appends the wave's keys that are at least `from` (and not 0) to the list.
-template <int R>
+// Appends the wave's keys that are at least `from` (and not 0) to the list, which
+// holds CAP.  The callers' bounds keep the count below that; it is held to CAP here
+// and where it is read all the same, so that no row can write past the list's end.
+template <int R, uint32_t CAP>
 __device__ __forceinline__ void collect(const uint64_t (&k)[R], uint64_t from, uint64_t* list, uint32_t* count) {
     uint64_t take[R];
     uint32_t all = 0;
@@ -182,7 +161,7 @@ __device__ __forceinline__ void collect(const uint64_t (&k)[R], uint64_t from, u
         if (take[r] == 0) continue;
         const uint32_t before = __builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(take[r] >> 32),
                                                           __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(take[r]), 0));
-        if ((take[r] >> (threadIdx.x & 63) & 1) != 0) list[at + before] = k[r];
+        if ((take[r] >> (threadIdx.x & 63) & 1) != 0 && at + before < CAP) list[at + before] = k[r];
         at += __builtin_popcountll(take[r]);
     }
 }
@@ -324,9 +303,12 @@ __global__ __launch_bounds__(256) void logprobs_kernel(LogprobArgs a, uint32_t p
         if (tid == 0) count = 0;
         __syncthreads();
         b = max64(max64(bound[0], bound[1]), max64(bound[2], bound[3]));
-        collect<R>(k, b, list, &count);
+        collect<R, kList>(k, b, list, &count);
         // the best of the batches before
-        if (base != 0 && tid < a.top && groups[tid] != 0) list[atomicAdd(&count, 1)] = groups[tid];
+        if (base != 0 && tid < a.top && groups[tid] != 0) {
+            const uint32_t at = atomicAdd(&count, 1);
+            if (at < kList) list[at] = groups[tid];
+        }
         __syncthreads();
         // The elements of the first listed groups (there are about four to
         // each of the n) are fetched while these are placed: a line of 128
@@ -335,11 +317,11 @@ __global__ __launch_bounds__(256) void logprobs_kernel(LogprobArgs a, uint32_t p
 #pragma unroll
         for (uint32_t u = 0; u < 2; ++u) {
             const uint32_t i = u * 64 + tid / 4;
-            const uint64_t g = i < count ? list[i] : 0;
+            const uint64_t g = i < min(count, kList) ? list[i] : 0;
             const uint32_t at = group_first<E>(0xFFFFFFFFu - static_cast<uint32_t>(g)) + in_group<E>(tid % 4 * 32);
             ahead[u] = x[g != 0 && at < a.vocab ? at : 0];
         }
-        place(list, count, a.top, groups);
+        place(list, min(count, kList), a.top, groups);
         asm volatile("" ::"v"(ahead[0]), "v"(ahead[1]));
     }
     // Their elements that reach the last of them (its value is looked at
@@ -369,10 +351,10 @@ __global__ __launch_bounds__(256) void logprobs_kernel(LogprobArgs a, uint32_t p
             k[r] = 0;
             if (__any(may) && may) k[r] = key_of(v[r], index[r]);
         }
-        collect<RE>(k, last, list, &count);
+        collect<RE, kList>(k, last, list, &count);
     }
     __syncthreads();
-    place(list, count, a.top, best);
+    place(list, min(count, kList), a.top, best);
     if (tid < a.top) {
         const uint64_t k = best[tid];
         a.top_ids[row * a.top + tid] = static_cast<int32_t>(0xFFFFFFFFu - static_cast<uint32_t>(k));
@@ -388,8 +370,9 @@ __global__ __launch_bounds__(256) void logprobs_kernel(LogprobArgs a, uint32_t p
 // may have for four workgroups a compute unit.)
 template <int E>
 __global__ __launch_bounds__(256) void logprobs_row_kernel(LogprobArgs a) {
-    // (at most n threads of a wave reach the bound)
-    __shared__ __attribute__((aligned(16))) uint64_t list[4 * kMaxTop * E + 32];
+    // at most n threads of a wave have a key that reaches the bound
+    constexpr uint32_t kRowList = 4 * kMaxTop * E;
+    __shared__ __attribute__((aligned(16))) uint64_t list[kRowList + 32];
     __shared__ float red[3][4];
     __shared__ uint64_t best[kMaxTop], bound[4];
     __shared__ uint32_t count;
@@ -404,7 +387,7 @@ __global__ __launch_bounds__(256) void logprobs_row_kernel(LogprobArgs a) {
 #pragma unroll
     for (int e = 0; e < E; ++e) m = fmaxf(m, v[e]);
     if (a.top != 0) {
-        const uint64_t b = wave_nth(best_key<E>(v, m, 0, a.vocab), a.top);
+        const uint64_t b = wave_nth(best_key<E>(v, m, tid, 0, a.vocab), a.top);
         if ((tid & 63) == 0) bound[wave] = b;
         if (tid == 0) count = 0;
         if (tid < kMaxTop) best[tid] = 0;
@@ -435,12 +418,12 @@ __global__ __launch_bounds__(256) void logprobs_row_kernel(LogprobArgs a) {
         uint64_t k[E];
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-            const uint32_t i = ((e >> 2) * 256 + tid) * 4 + (e & 3);
+            const uint32_t i = index_of(e, tid, 0);
             const bool may = i < a.vocab && !(v[e] < least);
             k[e] = 0;
             if (__any(may) && may) k[e] = key_of(v[e], i);
         }
-        collect<E>(k, from, list, &count);
+        collect<E, kRowList>(k, from, list, &count);
     }
     __syncthreads();
     s0 = (red[1][0] + red[1][1]) + (red[1][2] + red[1][3]);
@@ -455,7 +438,7 @@ __global__ __launch_bounds__(256) void logprobs_row_kernel(LogprobArgs a) {
         a.lp[row * a.n_ids + i] = id >= 0 && static_cast<uint32_t>(id) < a.vocab ? (xid - m) - ln : 0.f;
     }
     if (a.top == 0) return;
-    place(list, count, a.top, best);
+    place(list, min(count, kRowList), a.top, best);
     if (tid < a.top) {
         const uint64_t k = best[tid];
         a.top_ids[row * a.top + tid] = static_cast<int32_t>(0xFFFFFFFFu - static_cast<uint32_t>(k));

@@ -253,3 +253,30 @@ def test_more_pieces_than_workgroups():
     assert np.all(np.abs(h[sel].cpu().numpy() - ref["entropy"]) <= R.entropy_bound(ref, 3))
     assert np.array_equal(ti[sel].cpu().numpy(), ref["top_ids"])
     assert np.all(np.abs(tl[sel].cpu().numpy() - ref["top_lp"]) <= R.logprob_bound(ref, ref["top_lp"], 3))
+
+
+@pytest.mark.parametrize("vocab", [5, 64, 1000, 1024, 2048, 3001, 4096, 8191, 8192, 8193, 20000])
+@pytest.mark.parametrize("top", [1, 20, 32])
+def test_rows_of_nan_and_infinity(vocab, top):
+    """Rows that mix NaN with -infinity, in blocks and scattered: NaN, indexes
+    of the row, each once; the ordinary row between them as it is alone."""
+    g = np.random.default_rng(vocab + top)
+    top = min(top, vocab)
+    plain = g.standard_normal(vocab).astype(np.float32)
+    rows = []
+    for nans in sorted({1, vocab // 8, vocab // 2, vocab - vocab // 8, vocab - 1, vocab} - {0}):
+        for infs in sorted({0, (vocab - nans) // 2, vocab - nans}):
+            for order in range(4):
+                x = np.concatenate([np.full(nans, np.nan), np.full(infs, -np.inf), plain[:vocab - nans - infs]])
+                x = x[::-1] if order == 1 else (np.roll(x, infs) if order == 2 else (g.permutation(x) if order == 3 else x))
+                rows.append(x.astype(np.float32))
+    rows.append(plain)
+    x = np.stack(rows)
+    ids = ids_of(g, x.shape[0], vocab, 2)
+    got = run(x, ids, top)
+    for k in ("lp", "entropy", "top_lp"):
+        assert np.all(np.isnan(got[k][:-1])), k
+    assert np.all((got["top_ids"] >= 0) & (got["top_ids"] < vocab))
+    assert all(len(set(r)) == top for r in got["top_ids"].tolist())
+    check(plain[None], ids[-1:], top)
+    assert np.array_equal(got["top_ids"][-1], R.logprobs(plain[None], ids[-1:], top)["top_ids"][0])
