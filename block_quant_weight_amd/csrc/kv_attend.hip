@@ -507,13 +507,16 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attend_few_kernel(Atten
 //
 // All operands are exact: a query row is scaled by a power of two to a largest
 // magnitude in [2^14, 2^15) (bfloat16's 8 bits fit f16's 11), codes are whole
-// numbers.  The values' scales enter as powers of two relative to a reference
-// exponent that follows the pages' largest: code 2^(e - ref), exact from
-// 2^-19 up; probabilities are rounded to f16 and their sum is taken from the
-// rounded ones, so that numerator and denominator agree.  Sums are relative
-// to a running reference, times 2^3, that is moved (and the outputs scaled)
-// only when probabilities reach 2^10 or more, so that they stay f16; down to
-// 2^-17 of the reference they keep all of f16's bits, down to 2^-27 some.
+// numbers.  The values' scales enter as powers of two relative to the unit of
+// the outputs so far, whose exponent follows the pages' largest: code 2^(e -
+// unit), exact in f16 from 2^-24 to 2^5.  For a page further below, the outputs
+// are moved to a lower unit and back after it, which takes nothing from them
+// down to 2^-96 of the largest.  Probabilities are rounded to f16 and their sum
+// is taken from the rounded ones, so that numerator and denominator agree.  They
+// are relative to a running reference, times 2^3, that is moved (and the outputs
+// scaled) where a page's maximum is 2^6 above it, or, where no maximum is sought,
+// where a lane's sum reaches 2^15, so that they stay f16; down to 2^-17 of the
+// reference they keep all of f16's bits, down to 2^-27 some.
 //
 // Rows and columns are arranged as above: the 32 x 32 output gives lane l,
 // register 4 a + b the row 8 a + 4 (l / 32) + b and takes the k-indexes 8 (l /
@@ -576,6 +579,11 @@ __device__ __forceinline__ uint32_t f16_less(int up) {   // 1152 = 1.125 2^10
 
 // Exponent of a scale, a power of two; kNone for 0, kNan for what is no number.
 constexpr int kNone = -1000, kNan = 1000;
+// f16 holds codes times 2^-kBelow to 2^kAbove (the packed conversion stays
+// below 65504 up to there).  kFar: how far below the largest a unit goes.  A
+// page's probabilities sum to less than 2^17, its outputs to 2^29, those of 2^25
+// pages to 2^54: 2^72 times that is a float32.
+constexpr int kAbove = 5, kBelow = 24, kFar = 72;
 __device__ __forceinline__ int exponent_of(float s) {
     const uint32_t b = __builtin_bit_cast(uint32_t, s) & 0x7FFFFFFFu;
     return b < 0x00800000u ? kNone : (b >= 0x7F800000u ? kNan : static_cast<int>(b >> 23) - 127);
@@ -680,7 +688,7 @@ __global__ __launch_bounds__(512, 2) void attend_many_kernel(AttendArgs a) {
 #pragma unroll
             for (int i = 0; i < 16; ++i) o[e][i] = 0.f;
         float m_run = -__builtin_inff(), l_run = 0.f;   // this lane's part of the sum
-        int e_ref = kNone;
+        int e_ref = kNone, unit = kNone;                // largest exponent so far, that of the outputs' unit
 
         // Lane i has, of page at + i: its place (page id * kv_heads + head; -1:
         // none), its keys' scale and its values' scale's exponent.
@@ -711,12 +719,9 @@ __global__ __launch_bounds__(512, 2) void attend_many_kernel(AttendArgs a) {
             for (int u = 0; u < PER; ++u)
                 st[u] = *reinterpret_cast<const i32x4*>((wave * 64 + u * NT < UNITS / 2 ? k_from + k_at : v_from + v_at) + 16 * u * NT);
         };
-        // Into shared memory; the values by 2^(their exponent - the
-        // reference), which moves up where that would pass 2^5 (the packed
-        // conversion stays below f16's 65504 up to there).
-        auto stage = [&](int kb, int vb, int e_page) {
-            const int up = max(min(e_page - e_ref, 5), -24);
-            const uint32_t v_mul = e_page == kNone ? 0u : f16_power(up), v_less = e_page == kNone ? 0u : f16_less(up);
+        // Into shared memory; the values times 2^up (0 where that is below f16).
+        auto stage = [&](int kb, int vb, int up) {
+            const uint32_t v_mul = up < -kBelow ? 0u : f16_power(up), v_less = up < -kBelow ? 0u : f16_less(up);
 #pragma unroll
             for (int u = 0; u < PER; ++u) {
                 const int i = tid + u * NT;
@@ -738,15 +743,16 @@ __global__ __launch_bounds__(512, 2) void attend_many_kernel(AttendArgs a) {
                 }
             }
         };
-        int move = 0;                            // how far the reference exponent moves with the page staged
+        // Settles the unit for a page's values, and what they are staged with.
+        int want = kNone;                        // the unit's exponent for the page staged
         auto settle = [&](int32_t p) {
             if (place(p) < 0) return kNone;
             const int e = __builtin_amdgcn_readlane(exps, p - at);
-            if (e == kNone || e == kNan) return e;
-            if (e_ref == kNone) e_ref = e;
-            if (e - e_ref > 5) move = e - e_ref;
-            e_ref += move;
-            return e;
+            if (e == kNone) return kNone;
+            if (e == kNan) return 0;             // (sums that see them are NaN)
+            if (e - e_ref > kAbove) e_ref = e;   // (kNone: the first)
+            want = e - e_ref < -kBelow ? max(e, e_ref - kFar) : e_ref;
+            return e - want;
         };
         // whether this wave's columns (a pair's workgroup's) see anything of a page
         auto seen = [&](int32_t p) { return (PAIR || (p >= seen_lo && p < seen_hi)) && place(p) >= 0; };
@@ -786,7 +792,7 @@ __global__ __launch_bounds__(512, 2) void attend_many_kernel(AttendArgs a) {
         // shared memory (three pieces of 500 under a window of 1024: 65 us with
         // one after the other, 62 so; head dims of 128 and 64, whose waves
         // drift apart by themselves, lose 2 %).
-        auto values = [&](int b, const f16x8 (&pf)[4], int e_page) {
+        auto values = [&](int b, const f16x8 (&pf)[4], int up) {
             __builtin_amdgcn_sched_barrier(0);
             uint32_t from = v_row + b * D * 8;
             asm volatile("" : "+v"(from));
@@ -797,7 +803,7 @@ __global__ __launch_bounds__(512, 2) void attend_many_kernel(AttendArgs a) {
                     o[e] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vbuf[(from ^ (2 * s)) + 32 * e * 8], pf[s], o[e], 0, 0, 0);
             if constexpr (PAIR) {
                 constexpr int kAhead = 6, N = 4 * ET, kEach = 24 * PER / N, kStore = N / (2 * PER);
-                stage(b ^ 1, b ^ 1, e_page);
+                stage(b ^ 1, b ^ 1, up);
                 __builtin_amdgcn_sched_group_barrier(0x100, kAhead, 0);
 #pragma unroll
                 for (int i = 0; i < N; ++i) {
@@ -908,21 +914,21 @@ __global__ __launch_bounds__(512, 2) void attend_many_kernel(AttendArgs a) {
             }
         };
 
-        auto follow = [&]() {                    // outputs so far follow the reference exponent
-            if (move == 0) return;
-            const float f = ldexpf(1.f, -move);
+        auto follow = [&]() {                    // outputs so far in the unit of the page staged
+            if (unit == want) return;
+            const float f = ldexpf(1.f, unit - want);   // (kNone: they are 0)
+            unit = want;
 #pragma unroll
             for (int e = 0; e < ET; ++e)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) o[e][i] *= f;
-            move = 0;
         };
 
         if (p0 < p1) {
             look(p0);
             fetch(p0, p0);
-            int e_page = settle(p0);
-            stage(0, 0, e_page);
+            int up = settle(p0);
+            stage(0, 0, up);
             if (PAIR && tid < 2) again[tid] = 0;
             __syncthreads();
             for (int32_t p = p0; p < p1; ++p) {
@@ -940,15 +946,15 @@ __global__ __launch_bounds__(512, 2) void attend_many_kernel(AttendArgs a) {
 #pragma unroll
                         for (int s = 0; s < 4; ++s) pf[s] = pbuf[(4 * group + s) * 64 + lane];
                         if (tid == 0) again[(p + 1) & 1] = 0;
-                        e_page = settle(p + 1);
+                        up = settle(p + 1);
                     } else {
                         weigh(p, sc, pf);
                     }
-                    values(b, pf, e_page);
+                    values(b, pf, up);
                 }
                 if (!PAIR || !seen(p)) {
-                    e_page = settle(p + 1);
-                    stage(b ^ 1, b ^ 1, e_page);
+                    up = settle(p + 1);
+                    stage(b ^ 1, b ^ 1, up);
                 }
                 __syncthreads();
             }
@@ -964,7 +970,7 @@ __global__ __launch_bounds__(512, 2) void attend_many_kernel(AttendArgs a) {
         }
         if (w.row >= 0) {
             const uint64_t row_at = static_cast<uint64_t>(w.row) * a.heads + w.head;
-            const float v_scale = e_ref == kNone ? 0.f : ldexpf(1.f, e_ref);
+            const float v_scale = unit == kNone ? 0.f : ldexpf(1.f, unit);
             if (a.pieces == 1) {
                 const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll

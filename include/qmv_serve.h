@@ -153,12 +153,13 @@ int qmv_kv_read(const qmv_kv_cache *cache, const qmv_kv_seqs *seqs, uint32_t dty
  * probability), or, where bfloat16 queries are many (at least 16384 / head_dim
  * rows and heads to a sequence and key/value head, in a call of enough work,
  * by max_new and max_len), as float16: queries exactly, probabilities rounded
- * to 11 bits (below 2^-28 of the largest: to 0), and values of a page whose
- * scale is 2^-20 of the largest before it or less lose low bits.  A query, or
- * a page and head that is seen, with a NaN or infinity gives NaN for the rows
- * that see it and touches no other.  Scores past float32's range may give
- * NaN; values below 2^63 in magnitude never leave it.  Scales of the cache
- * are taken to be powers of two, 0 or NaN, as qmv_kv_write makes them.
+ * to 11 bits (below 2^-28 of the largest: to 0).  A query, or a page and head
+ * that is seen, with a NaN or infinity gives NaN for the rows that see it and
+ * touches no other.  Scores past float32's range may give NaN; values below
+ * 2^63 in magnitude never leave it.  Values below 2^-96, or below 2^-96 of the
+ * largest of their sequence and head, may lose low bits or count as 0.  Scales
+ * of the cache are taken to be powers of two, 0 or NaN, as qmv_kv_write makes
+ * them.
  * workspace: device memory of at least qmv_kv_attend_workspace bytes (may be
  * NULL where that is 0), 16-byte aligned.
  * Errors: QMV_E_ARG (as qmv_kv_write; scale not finite; workspace too small),

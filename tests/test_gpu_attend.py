@@ -476,3 +476,77 @@ def test_pages_shared_by_sequences(dtype):
     if dtype == "bf16":
         tol = tol + 2.0 ** -8 * (np.abs(ref) + tol)
     assert np.all(np.abs(got - ref) <= tol)
+
+
+def held(c, table, lens, start, q, dtype, window=0, b=None):
+    """A call against its reference; b: what replaces the bound's sizes."""
+    dim = q.shape[2]
+    got = attend(to_gpu(c), seqs(table, lens, start), q, dtype, window=window)
+    ref, sizes = R.attend(c, table, lens, start, q, np.float32(dim ** -0.5), window)
+    sizes.update(b or {})
+    tol = R.attend_bound(sizes, q, dim ** -0.5, max(lens), dtype)
+    if dtype == "bf16":
+        tol = tol + 2.0 ** -8 * (np.abs(ref) + tol)
+    err = np.abs(got[:start[-1]] - ref[:start[-1]])
+    assert np.all(err <= tol[:start[-1]]), f"worst {np.nanmax(err / np.maximum(tol[:start[-1]], 1e-300)):.3g} of the bound"
+
+
+# exponents of the values' scales, page by page: a large page that later rows of
+# the tile do not see, at the borders of what f16 holds of the smaller ones (24
+# below it) and far past them; a small page that earlier rows see alone; up to
+# 2^96 apart
+FAR = [[0, -20, -24, -5], [0, -25, -25, -26], [0, -30, 0, -30], [-40, 0, -41, 5], [6, -18, 5, 11],
+       [10, -70, -72, 24], [-60, 30, -60, 36], [-90, -90, 5, -90], [36, 36, -20, -60]]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("exps", FAR, ids=lambda e: "_".join(map(str, e)))
+def test_scales_of_pages_that_a_row_does_not_see(exps, dim, dtype):
+    """Rows under a window, each held against the values that it sees itself."""
+    narrow_windows(exps, dim, dtype, (1, 20, 64))
+
+
+def narrow_windows(exps, dim, dtype, windows):
+    g, c, table = make([64 * len(exps)], 1, dim, seed=27)
+    for page, e in zip(table[0], exps):
+        c.v_scale[page] = 2.0 ** e
+    q = queries(g, 200, 2, dim)
+    for window in windows:
+        held(c, table, [64 * len(exps)], [0, 200], q, dtype, window)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("exps", FAR, ids=lambda e: "_".join(map(str, e)))
+def test_scales_of_pages_without_weight(exps, dim, dtype):
+    """No window, but keys so that every row's weight lies on its own page: the
+    earlier pages' is below e^-200 of it, where neither float32 nor float16 has
+    anything left, so each row is held against its own page's values."""
+    g, c, table = make([64 * len(exps)], 1, dim, seed=28)
+    for n, page in enumerate(table[0]):
+        c.v_scale[page] = 2.0 ** exps[n]
+        c.k_scale[page] = 2.0 ** -6
+        c.k[page] = np.rint(c.k[page] / 40)
+        c.k[page, 0, :, 0] = 20 * n
+    q = queries(g, 200, 2, dim)
+    q[:, :, 0] = 64 * 12 * dim ** 0.5              # a score of 240 a page
+    q = R.bf16(q.astype(np.float32))
+    own = np.zeros((200, 2, 1))
+    for t in range(200):
+        pos = 64 * len(exps) - 200 + t
+        own[t] = np.abs(c.v[table[0, pos // 64], 0]).max() * 2.0 ** exps[pos // 64]
+    held(c, table, [64 * len(exps)], [0, 200], q, dtype, b={"vmax": own})
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("exps", [[0, -105, -112, 0], [50, -100, -120, -126], [-60, 50, -75, -126], [50, 0, -126, -60]],
+                         ids=lambda e: "_".join(map(str, e)))
+def test_scales_further_apart_than_float32(exps, dim, dtype):
+    """Rows that see all of the pages: what is far below the rest does not show,
+    and nothing leaves float32 on the way."""
+    g, c, table = make([64 * len(exps)], 1, dim, seed=29)
+    for page, e in zip(table[0], exps):
+        c.v_scale[page] = 2.0 ** e
+    held(c, table, [64 * len(exps)], [0, 64], queries(g, 64, 2, dim), dtype)

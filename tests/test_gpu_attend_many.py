@@ -110,3 +110,24 @@ def test_out_may_be_q_and_capture(many):
 @pytest.mark.parametrize("many", ["whole"], indirect=True)
 def test_many_short_sequences(many):
     A.test_many_short_sequences("bf16")
+
+
+@pytest.mark.parametrize("many", ["whole"], indirect=True)
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("exps", A.FAR, ids=lambda e: "_".join(map(str, e)))
+def test_scales_of_pages_that_a_row_does_not_see(many, exps, dim):
+    # (at head dims of 64 narrower ones are too little work to choose this kernel)
+    A.narrow_windows(exps, dim, "bf16", (50, 64) if dim == 64 else (1, 20, 64))
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("exps", A.FAR, ids=lambda e: "_".join(map(str, e)))
+def test_scales_of_pages_without_weight(many, exps, dim):
+    A.test_scales_of_pages_without_weight(exps, dim, "bf16")
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("exps", [[0, -105, -112, 0], [50, -100, -120, -126], [-60, 50, -75, -126], [50, 0, -126, -60]],
+                         ids=lambda e: "_".join(map(str, e)))
+def test_scales_further_apart_than_float32(many, exps, dim):
+    A.test_scales_further_apart_than_float32(exps, dim, "bf16")
