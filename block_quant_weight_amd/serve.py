@@ -78,19 +78,31 @@ def _stream(stream, here):
     return _stream_of(stream)
 
 
-def _dev(t, dtype, numel, what, here):
-    """Address of a contiguous GPU tensor of device `here` with at least numel elements."""
+def _dev(t, dtype, shape, what, here):
+    """Address of a contiguous GPU tensor of device `here` of that shape."""
+    if t.dtype is dtype and t.get_device() == here >= 0 and t.is_contiguous() and t.shape == shape:
+        return t.data_ptr()
+    return _refuse(t, dtype, what, None if t.shape == shape else
+                   f"{what} must be {list(shape)}, not {list(t.shape)}")
+
+
+def _first(t, dtype, numel, what, here):
+    """Address of a contiguous GPU tensor of device `here` with at least numel
+    elements, the first of which are used."""
     if t.dtype is dtype and t.get_device() == here >= 0 and t.is_contiguous() and t.numel() >= numel:
         return t.data_ptr()
+    return _refuse(t, dtype, what, None if t.numel() >= numel else
+                   f"{what} holds {t.numel()} elements, needs {numel}")
+
+
+def _refuse(t, dtype, what, size):
     if not t.is_cuda:
         raise ValueError(f"{what} must be a GPU tensor")
     if t.dtype != dtype:
         raise TypeError(f"{what} must be {dtype}, not {t.dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{what} must be contiguous")
-    if t.numel() < numel:
-        raise ValueError(f"{what} holds {t.numel()} elements, needs {numel}")
-    raise ValueError(f"{what} is not on the call's device")
+    raise ValueError(size or f"{what} is not on the call's device")
 
 
 def _dtype(t, what):
@@ -131,10 +143,10 @@ class KvCache:
             raise ValueError("the scales must be [pages, kv_heads]")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.device = k.get_device()
-        n, here = k.numel(), self.device
-        self.c = _Cache(_dev(k, torch.int8, n, "k", here), _dev(v, torch.int8, n, "v", here),
-                        _dev(k_scale, torch.float32, 0, "k_scale", here),
-                        _dev(v_scale, torch.float32, 0, "v_scale", here),
+        here = self.device
+        self.c = _Cache(_dev(k, torch.int8, k.shape, "k", here), _dev(v, torch.int8, v.shape, "v", here),
+                        _dev(k_scale, torch.float32, k_scale.shape, "k_scale", here),
+                        _dev(v_scale, torch.float32, v_scale.shape, "v_scale", here),
                         self.pages, self.kv_heads, self.head_dim)
         self.ref = ctypes.pointer(self.c)
 
@@ -148,8 +160,9 @@ class KvCache:
 
 class KvSeqs:
     """The tokens a call is about (qmv_kv_seqs): table int32 [seqs,
-    table_stride], len int32 [seqs], start int32 [seqs + 1], on the GPU; rows
-    of the call's arrays are given by each call's tensors.  max_new and
+    table_stride], len int32 [seqs], start int32 [seqs + 1] (of longer ones the
+    first elements), on the GPU; rows of the call's arrays are given by each
+    call's tensors.  max_new and
     max_len, the largest number of rows and of tokens of one sequence, shape
     the launch only.  One object serves all layers of a step, and all steps of
     a graph: its tensors are changed in place."""
@@ -163,9 +176,9 @@ class KvSeqs:
         self.table, self.len, self.start = table, len, start
         self.device = table.get_device()
         here = self.device
-        self.c = _Seqs(_dev(table, torch.int32, table.numel(), "table", here),
-                       _dev(len, torch.int32, self.seqs, "len", here),
-                       _dev(start, torch.int32, self.seqs + 1, "start", here),
+        self.c = _Seqs(_dev(table, torch.int32, table.shape, "table", here),
+                       _first(len, torch.int32, self.seqs, "len", here),
+                       _first(start, torch.int32, self.seqs + 1, "start", here),
                        self.seqs, table.shape[1], 0, int(max_new), int(max_len))
         self.last = (0, ctypes.byref(self.c))
 
@@ -182,15 +195,14 @@ class KvSeqs:
 
 def _rows(cache, seqs, t, heads, what):
     """seqs with the rows of t [rows, heads, head_dim] for a call, t's
-    elements, and the device."""
+    shape, and the device."""
     here = cache.device
     if seqs.device != here:
         raise ValueError("the sequences are not on the cache's device")
     shape = t.shape
     if len(shape) != 3 or shape[1] != heads or shape[2] != cache.head_dim:
         raise ValueError(f"{what} must be [rows, {heads}, {cache.head_dim}]")
-    rows = shape[0]
-    return seqs.with_rows(rows), rows * heads * cache.head_dim, here
+    return seqs.with_rows(shape[0]), shape, here
 
 
 def qmv_rms_norm(x, w, eps, res=None, sum=None, y=None, q=None, d=None, stream=None):
@@ -201,27 +213,26 @@ def qmv_rms_norm(x, w, eps, res=None, sum=None, y=None, q=None, d=None, stream=N
     if len(shape) != 2:
         raise ValueError("x must be [rows, cols]")
     rows, cols = shape
-    n, here = rows * cols, x.get_device()
-    f32 = torch.float32
+    here, f32 = x.get_device(), torch.float32
     y32 = yb = None
     if y is not None:
         if _dtype(y, "y") == QMV_F32:
-            y32 = _dev(y, f32, n, "y", here)
+            y32 = _dev(y, f32, shape, "y", here)
         else:
-            yb = _dev(y, torch.bfloat16, n, "y", here)
+            yb = _dev(y, torch.bfloat16, shape, "y", here)
     _check(lib().qmv_rms_norm(
-        _dev(x, f32, n, "x", here), None if res is None else _dev(res, f32, n, "res", here),
-        _dev(w, f32, cols, "w", here), eps, rows, cols, None if sum is None else _dev(sum, f32, n, "sum", here),
-        y32, yb, None if q is None else _dev(q, torch.int8, n, "q", here),
-        None if d is None else _dev(d, f32, n // 32, "d", here), _stream(stream, here)), "qmv_rms_norm")
+        _dev(x, f32, shape, "x", here), None if res is None else _dev(res, f32, shape, "res", here),
+        _dev(w, f32, (cols,), "w", here), eps, rows, cols, None if sum is None else _dev(sum, f32, shape, "sum", here),
+        y32, yb, None if q is None else _dev(q, torch.int8, shape, "q", here),
+        None if d is None else _dev(d, f32, (rows, cols // 32), "d", here), _stream(stream, here)), "qmv_rms_norm")
 
 
 def qmv_kv_write(cache: KvCache, seqs: KvSeqs, k, v, stream=None):
     """k, v: float32 or bfloat16 [rows, kv_heads, head_dim]: the rows of seqs into the cache."""
     dt = _dtype(k, "k")
-    ref, n, here = _rows(cache, seqs, k, cache.kv_heads, "k")
-    _check(lib().qmv_kv_write(cache.ref, ref, dt, _dev(k, k.dtype, n, "k", here),
-                              _dev(v, k.dtype, n, "v", here), _stream(stream, here)), "qmv_kv_write")
+    ref, shape, here = _rows(cache, seqs, k, cache.kv_heads, "k")
+    _check(lib().qmv_kv_write(cache.ref, ref, dt, _dev(k, k.dtype, shape, "k", here),
+                              _dev(v, k.dtype, shape, "v", here), _stream(stream, here)), "qmv_kv_write")
 
 
 def qmv_kv_read(cache: KvCache, seqs: KvSeqs, k=None, v=None, stream=None):
@@ -231,9 +242,9 @@ def qmv_kv_read(cache: KvCache, seqs: KvSeqs, k=None, v=None, stream=None):
     if t is None:
         raise QmvError(QMV_E_ARG, "qmv_kv_read")
     dt = _dtype(t, "k or v")
-    ref, n, here = _rows(cache, seqs, t, cache.kv_heads, "k or v")
-    _check(lib().qmv_kv_read(cache.ref, ref, dt, None if k is None else _dev(k, t.dtype, n, "k", here),
-                             None if v is None else _dev(v, t.dtype, n, "v", here), _stream(stream, here)),
+    ref, shape, here = _rows(cache, seqs, t, cache.kv_heads, "k or v")
+    _check(lib().qmv_kv_read(cache.ref, ref, dt, None if k is None else _dev(k, t.dtype, shape, "k", here),
+                             None if v is None else _dev(v, t.dtype, shape, "v", here), _stream(stream, here)),
            "qmv_kv_read")
 
 
@@ -262,16 +273,16 @@ def qmv_kv_attend(cache: KvCache, seqs: KvSeqs, q, out, scale=None, window=0, wo
         raise ValueError("window must not be negative")
     shape = q.shape
     heads = shape[1] if len(shape) == 3 else 0
-    ref, n, here = _rows(cache, seqs, q, heads, "q")
+    ref, shape, here = _rows(cache, seqs, q, heads, "q")
     if workspace is None:
         nbytes = qmv_kv_attend_workspace(cache, seqs, q, window)
         if nbytes:
             workspace = _scratch(nbytes, stream)
-    pw, nw = (None, 0) if workspace is None else (_dev(workspace, torch.uint8, 0, "workspace", here),
+    pw, nw = (None, 0) if workspace is None else (_first(workspace, torch.uint8, 0, "workspace", here),
                                                   workspace.numel())
     _check(lib().qmv_kv_attend(cache.ref, ref, dt, heads,
                                cache.head_dim ** -0.5 if scale is None else scale, window,
-                               _dev(q, q.dtype, n, "q", here), _dev(out, q.dtype, n, "out", here), pw, nw,
+                               _dev(q, q.dtype, shape, "q", here), _dev(out, q.dtype, shape, "out", here), pw, nw,
                                _stream(stream, here)), "qmv_kv_attend")
 
 
@@ -303,11 +314,11 @@ def qmv_logprobs(logits, ids=None, lp=None, entropy=None, top_ids=None, top_lp=N
         workspace = _scratch(max(qmv_logprobs_workspace(rows, vocab, top), 16), stream)
     f32, i32, here = torch.float32, torch.int32, logits.get_device()
     _check(lib().qmv_logprobs(
-        _dev(logits, f32, rows * vocab, "logits", here), rows, vocab,
-        None if ids is None else _dev(ids, i32, rows * n, "ids", here), n, top,
-        None if lp is None else _dev(lp, f32, rows * n, "lp", here),
-        None if entropy is None else _dev(entropy, f32, rows, "entropy", here),
-        None if top_ids is None else _dev(top_ids, i32, rows * top, "top_ids", here),
-        None if top_lp is None else _dev(top_lp, f32, rows * top, "top_lp", here),
-        _dev(workspace, torch.uint8, 0, "workspace", here), workspace.numel(), _stream(stream, here)),
+        _dev(logits, f32, (rows, vocab), "logits", here), rows, vocab,
+        None if ids is None else _dev(ids, i32, (rows, n), "ids", here), n, top,
+        None if lp is None else _dev(lp, f32, lp.shape if ids is None else (rows, n), "lp", here),
+        None if entropy is None else _dev(entropy, f32, (rows,), "entropy", here),
+        None if top_ids is None else _dev(top_ids, i32, (rows, top), "top_ids", here),
+        None if top_lp is None else _dev(top_lp, f32, top_lp.shape if top_ids is None else (rows, top), "top_lp", here),
+        _first(workspace, torch.uint8, 0, "workspace", here), workspace.numel(), _stream(stream, here)),
         "qmv_logprobs")
