@@ -115,6 +115,13 @@ def _dtype(t, what):
     raise TypeError(f"{what} must be float32 or bfloat16, not {dt}")
 
 
+def _u32(n, what):
+    """n, which the library takes in 32 bits."""
+    if not 0 <= n <= 0xFFFFFFFF:
+        raise ValueError(f"{what} must be between 0 and 2^32 - 1")
+    return n
+
+
 def _scratch(nbytes, stream):
     """A workspace that a call allocates itself, in the order of its stream."""
     if stream is None:
@@ -179,7 +186,7 @@ class KvSeqs:
         self.c = _Seqs(_dev(table, torch.int32, table.shape, "table", here),
                        _first(len, torch.int32, self.seqs, "len", here),
                        _first(start, torch.int32, self.seqs + 1, "start", here),
-                       self.seqs, table.shape[1], 0, int(max_new), int(max_len))
+                       self.seqs, table.shape[1], 0, min(int(max_new), 0xFFFFFFFF), min(int(max_len), 0xFFFFFFFF))
         self.last = (0, ctypes.byref(self.c))
 
     def with_rows(self, rows):
@@ -252,8 +259,7 @@ def qmv_kv_attend_workspace(cache: KvCache, seqs: KvSeqs, q, window=0) -> int:
     """Bytes of workspace that qmv_kv_attend needs for q [rows, heads, head_dim]."""
     out = ctypes.c_uint64(0)
     dt = _dtype(q, "q")
-    if window < 0:
-        raise ValueError("window must not be negative")
+    _u32(window, "window")
     shape = q.shape
     heads = shape[1] if len(shape) == 3 else 0
     ref, _, _ = _rows(cache, seqs, q, heads, "q")
@@ -269,8 +275,7 @@ def qmv_kv_attend(cache: KvCache, seqs: KvSeqs, q, out, scale=None, window=0, wo
     qmv_kv_attend_workspace bytes; None allocates one in the order of the
     stream."""
     dt = _dtype(q, "q")
-    if window < 0:
-        raise ValueError("window must not be negative")
+    _u32(window, "window")
     shape = q.shape
     heads = shape[1] if len(shape) == 3 else 0
     ref, shape, here = _rows(cache, seqs, q, heads, "q")
@@ -288,7 +293,8 @@ def qmv_kv_attend(cache: KvCache, seqs: KvSeqs, q, out, scale=None, window=0, wo
 
 def qmv_logprobs_workspace(rows, vocab, top=0) -> int:
     out = ctypes.c_uint64(0)
-    _check(lib().qmv_logprobs_workspace(rows, vocab, top, ctypes.byref(out)), "qmv_logprobs_workspace")
+    _check(lib().qmv_logprobs_workspace(_u32(rows, "rows"), _u32(vocab, "vocab"), _u32(top, "top"),
+                                        ctypes.byref(out)), "qmv_logprobs_workspace")
     return out.value
 
 

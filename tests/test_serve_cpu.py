@@ -140,3 +140,31 @@ def test_launch_limits():
         assert L.qmv_kv_read(cache(**c), seqs(**s), 0, P, P, None) == SHAPE
         assert L.qmv_kv_attend(cache(**c), seqs(**s), 0, 4, 1.0, 0, P, P, P, 1 << 62, None) == SHAPE
     assert L.qmv_kv_attend(cache(), seqs(rows=1 << 28), 0, 8, 1.0, 0, P, P, P, 1 << 62, None) == SHAPE
+
+
+@pytest.mark.parametrize("window", [-1, 1 << 32, (1 << 32) + 5, 1 << 64])
+def test_windows_that_32_bits_do_not_hold(window):
+    """(2^32 + 5 would be a window of 5.)"""
+    import torch
+    q = torch.zeros(1, 2, 64)
+    with pytest.raises(ValueError, match="window"):
+        S.qmv_kv_attend(None, None, q, q, window=window)
+    with pytest.raises(ValueError, match="window"):
+        S.qmv_kv_attend_workspace(None, None, q, window=window)
+
+
+def test_sizes_that_32_bits_do_not_hold():
+    assert S.qmv_logprobs_workspace(1, 10000, 3) > 0
+    for sizes in (((1 << 32) + 1, 10000, 3), (1, (1 << 32) + 10000, 3), (1, 10000, (1 << 32) + 3), (-1, 10000, 0)):
+        with pytest.raises(ValueError):
+            S.qmv_logprobs_workspace(*sizes)
+
+
+def test_hints_past_32_bits_count_as_the_largest(monkeypatch):
+    """A hint is only a hint: 2^32 is not 0."""
+    import torch
+    monkeypatch.setattr(S, "_dev", lambda t, *a: t.data_ptr())
+    monkeypatch.setattr(S, "_first", lambda t, *a: t.data_ptr())
+    t = torch.zeros(1, 4, dtype=torch.int32)
+    c = S.KvSeqs(t, t, t, 1 << 32, 1 << 40).c
+    assert c.max_new == c.max_len == 0xFFFFFFFF
