@@ -38,11 +38,13 @@
 // its own and all of their pages, and nothing is joined.
 //
 // Decode is bound by memory: 32 sequences of 1000 to 4000 tokens, 32 heads on 8
-// of 128, 38.6 us, 4.4 TB/s; two of up to 131072 62.8 us and 4.7 for the join,
-// 5.0 TB/s (the same pages read by nothing but loads: 5.8 to 6.0); one of 100
+// of 128, 38.2 us, 4.5 TB/s; two of up to 131072 62.0 us and 4.8 for the join,
+// 5.1 TB/s (the same pages read by nothing but loads: 5.8 to 6.0); one of 100
 // tokens 5.1 us, a launch and three dependent trips.  A float32 prompt of 8192
-// takes 1392 us, 395 TFLOP/s, bound by the vector operations that make digits
-// and join their products.
+// takes 1394 us, 394 TFLOP/s, bound by the vector operations that make digits
+// and join their products.  Sequences are dealt out by count, not by length: 31
+// of 1000 and one of 131072 take 696 us, the long one alone 47, as eight
+// workgroups, one a head, walk its pages.
 #include <type_traits>
 
 #include "kv_common.h"
@@ -524,14 +526,17 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attend_few_kernel(Atten
 // / 32) + 4 (a % 2) + b the probabilities stay in their lanes.
 //
 // Shared memory: 16-byte chunks of a row are permuted by the row's number, so
-// that lanes that read the same chunk of different rows do not meet in a bank.
+// that lanes that read the same chunk of different rows do not meet in a bank
+// (the stores, one to eight reads and fewer, do: 8 cycles each).
 //
-// Measured: a prompt of 8192 with 32 heads on 8 of 128, 582 us, 945 TFLOP/s (a
-// large bfloat16 product: 1360), bound by the matrix cores, the exponentials
-// between their two products and the page's barrier; three pieces of up to 500
-// rows under a window of 1024, 16 heads on 4 of 256, 60 us, 340 TFLOP/s: there
-// are 160 tiles for 256 compute units, and each operand of a product is read
-// from shared memory for 32 columns alone, as long as the product itself takes.
+// Measured: a prompt of 8192 with 32 heads on 8 of 128, 592 us, 929 TFLOP/s (a
+// large bfloat16 product: 1380).  By counters the matrix cores are busy in 38%
+// of the SIMDs' cycles and vector instructions issue in 42%; waves wait in 32%
+// of theirs (two a SIMD, a barrier a page), in 5% for shared memory, though each
+// operand of a product is read from there for 32 columns alone, at 128 bytes a
+// cycle as long as the product takes.  Three pieces of up to 500 rows under a
+// window of 1024, 16 heads on 4 of 256, 60 us, 342 TFLOP/s: the same, and 160
+// tiles for 256 compute units.
 
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
@@ -1091,9 +1096,10 @@ hipError_t join(const AttendArgs& a, uint32_t columns, hipStream_t s) {
 // wave at least: one sequence of 4000 tokens with 8 heads of 128 11.2 us, with 4
 // of 256 17.6; one: 9.9 and 14.4.)  Short sequences stay whole, as a second
 // kernel costs as much as their pages one after another, and its launch a call
-// more on the host (one sequence, whole / in pieces: 500 tokens of 8 heads of
-// 128 8.0 / 9.9 us, 1000 10.5 / 9.9; 1000 of 2 heads of 64 6.9 / 7.9; 500 of 4
-// heads of 256 13.0 / 14.0).
+// more on the host (one sequence, whole / in pieces, us in a graph: 500 tokens
+// of 8 heads of 128 8.0 / 9.3, 900 10.2 / 9.5, 1000 10.5 / 9.7; of 2 heads of 64
+// 1000 6.8 / 7.5, 1400 8.2 / 7.6; of 4 heads of 256 500 13.0 / 13.3, 550 14.6 /
+// 13.8: the limits lie where the second launch is worth what it saves).
 struct Plan {
     uint32_t tiles, pieces, per;
     Few few;
@@ -1142,13 +1148,15 @@ Plan plan_few(const qmv_kv_cache& c, const qmv_kv_seqs& s, uint32_t heads, uint3
 // multiply zeros) and the launch has work enough that its waves do not wait
 // for each page by themselves: kManyWork, in products of 16 columns with a
 // page, times D.  Measured (us, many / few), sequences x tokens, columns:
-//   D 128, 8 heads: 1 x 2000, 256: 32 / 18; 1 x 16000, 128 and 256: 32 / 36 and
-//     42 / 58; 8 x 3000, 64 and 128: 30 / 25 and 34 / 44; 64 x 1000, 64 and 128:
-//     59 / 49 and 61 / 79; whole prompts 2 x 500 27 / 24, 1 x 2000 79 / 119
-//   D 256, 4 heads: 1 x 16000, 128 and 256: 51 / 42 and 53 / 64; 8 x 3000, 128:
-//     46 / 48; 64 x 1000, 64 and 128: 55 / 52 and 60 / 93
-//   D 64, 8 heads: 8 x 3000, 128 and 256: 27 / 25 and 36 / 41; 64 x 1000, 128
-//     and 256: 50 / 42 and 67 / 71; whole prompts 1 x 1000 36 / 27, 1 x 4000 133 / 190
+//   D 128, 8 heads: 1 x 2000, 256: 32 / 16; 1 x 16000, 128 and 256: 31 / 34 and
+//     43 / 58; 8 x 3000, 128 and 256: 34 / 41 and 47 / 68; 64 x 1000, 128 and 256:
+//     61 / 79 and 90 / 132; whole prompts 2 x 500 27 / 24, 1 x 2000 79 / 114
+//   D 256, 4 heads: 1 x 16000, 64, 128 and 256: 38 / 27, 44 / 39 and 50 / 60; 8 x
+//     3000, 128: 44 / 43; 64 x 1000, 64 and 128: 50 / 51 and 55 / 91
+//   D 64, 8 heads: 8 x 3000, 256 and 512: 36 / 37 and 61 / 72; 64 x 1000, 256 and
+//     512: 68 / 71 and 119 / 120; whole prompts 1 x 1000 36 / 24, 1 x 4000 135 / 189
+// The faster one is taken at each of these but one, D 256, 1 x 16000 with 128
+// columns (44 for 39), just past the limit, and one more is even (8 x 3000).
 constexpr uint64_t kManyCols = 16384;
 constexpr double kManyWork = 2e6;
 

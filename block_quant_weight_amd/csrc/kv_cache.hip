@@ -22,10 +22,10 @@
 // words: odd, so that neighbouring dims fall into different banks).
 //
 // Bound by memory.  8 heads of 128: prompts of up to 4096 bfloat16 tokens (4
-// sequences) written in 18.7 us and read back in 15.9, 4.0 TB/s over both; one
-// float32 token for each of 64 sequences written in 7.2 us (a launch and two
+// sequences) written in 18.6 us and read back in 15.9, 4.0 TB/s over both; one
+// float32 token for each of 64 sequences written in 6.3 us (a launch and two
 // dependent trips to memory, the page's id and the page), their last 100 read
-// back in 15.6 us, 4.2 TB/s.
+// back in 15.8 us, 4.1 TB/s.
 #include "kv_common.h"
 
 namespace qmv {

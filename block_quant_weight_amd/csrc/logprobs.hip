@@ -15,8 +15,8 @@
 // Both searches list what reaches a bound that few pass, and place each listed
 // key by counting the larger ones.  Rows of up to 8192 are done by one kernel.
 //
-// 64 rows of 248320: 12.3 us for the first kernel, 5.2 TB/s, and 7.0 for the
-// second, a chain of six trips to memory or barriers; one row: 3.1 and 6.8.
+// 64 rows of 248320: 12.6 us for the first kernel, 5.0 TB/s, and 7.2 for the
+// second, a chain of six trips to memory or barriers; one row: 3.1 and 7.0.
 #include "device_common.h"
 #include "logprob_keys.h"
 #include "serve_kernels.h"

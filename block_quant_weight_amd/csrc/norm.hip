@@ -16,7 +16,7 @@
 //
 // Bound by memory: 8191 x 4096 with residual and bfloat16 output 78 us, 6.0
 // TB/s (a copy of a large array reaches 5.0); 512 x 4096 to Q8_0 8.6 us, 3.2
-// TB/s, where the launch and one trip to memory count; one row 2.9 us, the
+// TB/s, where the launch and one trip to memory count; one row 3.1 us, the
 // same two and the sum over the workgroup.
 #include "device_common.h"
 #include "serve_kernels.h"

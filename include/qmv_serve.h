@@ -93,7 +93,8 @@ typedef struct qmv_kv_cache {
  * are neither read nor written.  max_new, max_len: the largest count of rows
  * and the largest len among the sequences as far as the host knows; they
  * shape the launch: results are right whatever they are, and the same bits
- * for the same ones.
+ * for the same ones.  A max_len far above the lengths, or one length far above
+ * the others, leaves much of the GPU idle in qmv_kv_attend.
  * A position below 0 (more rows than len), past the table or in a page whose
  * id is outside [0, pages) has no place: nothing is written for it, it reads
  * as zero, and attention leaves it out.
@@ -111,13 +112,13 @@ typedef struct qmv_kv_seqs {
  * the largest magnitude of the new values there: need = the least power of
  * two d from 2^-126 with amax <= 127 d (0 if amax is 0; at most 2^121, where
  * codes end at 127); the scale becomes need if the page's first token is among
- * the new ones, else the larger of the old scale and need; earlier tokens' codes become code * old / scale,
- * and the new codes x / scale, both rounded to the nearest whole number,
- * halves to even.  A growing scale at least doubles, so whatever the order
- * of the writes every stored value stays within one scale of what was
- * written (half a scale if its page's scale did not grow after it).  An
- * infinite or NaN value makes the scale of its page, head and array NaN:
- * everything read from there is NaN until the page is begun anew.
+ * the new ones, else the larger of the old scale and need; earlier tokens'
+ * codes become code * old / scale, and the new codes x / scale, both rounded
+ * to the nearest whole number, halves to even.  A growing scale at least
+ * doubles, so whatever the order of the writes every stored value stays within
+ * one scale of what was written (half a scale if its page's scale did not grow
+ * after it).  An infinite or NaN value makes the scale of its page, head and
+ * array NaN: everything read from there is NaN until the page is begun anew.
  * A call must not write into one page twice, for two sequences or two places
  * of one table.  A page's first token is written before or with its others
  * (what is read of a page that was never begun is whatever its memory holds).
@@ -189,9 +190,9 @@ int qmv_kv_attend(const qmv_kv_cache *cache, const qmv_kv_seqs *seqs, uint32_t d
  * logit.
  * logits 4-byte aligned, the others 4-byte aligned; workspace: 16-byte
  * aligned, at least qmv_logprobs_workspace bytes.
- * Errors: QMV_E_ARG (logits NULL, no output, ids without lp or n_ids 0,
+ * Errors: QMV_E_ARG (logits NULL, no output, lp without ids or with n_ids 0,
  * top_ids or top_lp without the other or with top 0, misaligned pointer,
- * rows or vocab 0, workspace too small), QMV_E_SHAPE (vocab above 2^24, top
+ * rows or vocab 0, workspace NULL or too small), QMV_E_SHAPE (vocab above 2^24, top
  * above 32 or above vocab, rows above 2^22), QMV_E_DEVICE.
  */
 int qmv_logprobs_workspace(uint32_t rows, uint32_t vocab, uint32_t top, uint64_t *bytes);
