@@ -135,10 +135,22 @@ def workspace(nbytes, device="cuda"):
     return torch.empty(max(int(nbytes), 16), dtype=torch.uint8, device=device)
 
 
+def _kept(name):
+    """An attribute that keeps the tensor it is first given: the struct holds its address."""
+    at = "_" + name
+
+    def put(self, t):
+        if self.__dict__.setdefault(at, t) is not t:
+            raise AttributeError(f"{name} can only be changed in place")
+    return property(lambda self: self.__dict__[at], put)
+
+
 class KvCache:
     """The arrays of a cache (qmv_kv_cache): k int8 [pages, kv_heads, 64,
     head_dim], v int8 [pages, kv_heads, head_dim, 64], k_scale and v_scale
     float32 [pages, kv_heads].  KvCache.empty allocates them."""
+
+    k, v, k_scale, v_scale = map(_kept, ("k", "v", "k_scale", "v_scale"))
 
     def __init__(self, k, v, k_scale, v_scale):
         if k.dim() != 4 or k.shape[2] != QMV_KV_PAGE:
@@ -173,6 +185,8 @@ class KvSeqs:
     max_len, the largest number of rows and of tokens of one sequence, shape
     the launch only.  One object serves all layers of a step, and all steps of
     a graph: its tensors are changed in place."""
+
+    table, len, start = map(_kept, ("table", "len", "start"))
 
     def __init__(self, table, len, start, max_new, max_len):
         if table.dim() != 2:

@@ -168,3 +168,24 @@ def test_hints_past_32_bits_count_as_the_largest(monkeypatch):
     t = torch.zeros(1, 4, dtype=torch.int32)
     c = S.KvSeqs(t, t, t, 1 << 32, 1 << 40).c
     assert c.max_new == c.max_len == 0xFFFFFFFF
+
+
+def test_tensors_of_a_handle_are_changed_in_place_only(monkeypatch):
+    """A handle holds addresses: another tensor in an attribute's place would
+    leave the calls reading the first one's memory, which nothing keeps."""
+    import torch
+    monkeypatch.setattr(S, "_dev", lambda t, *a: t.data_ptr())
+    monkeypatch.setattr(S, "_first", lambda t, *a: t.data_ptr())
+    i = lambda *n: torch.zeros(*n, dtype=torch.int32)
+    s = S.KvSeqs(i(2, 3), i(2), i(3), 1, 1)
+    c = S.KvCache(torch.zeros(4, 1, 64, 64, dtype=torch.int8), torch.zeros(4, 1, 64, 64, dtype=torch.int8),
+                  torch.zeros(4, 1), torch.zeros(4, 1))
+    for handle, names in ((s, ("table", "len", "start")), (c, ("k", "v", "k_scale", "v_scale"))):
+        for name in names:
+            t = getattr(handle, name)
+            with pytest.raises(AttributeError, match="in place"):
+                setattr(handle, name, t.clone())
+            assert getattr(handle, name) is t and t.data_ptr() == getattr(handle.c, name)
+    s.len += 1
+    s.table[:] = 2
+    assert s.len.tolist() == [1, 1] and s.len.data_ptr() == s.c.len and int(s.table.sum()) == 12
