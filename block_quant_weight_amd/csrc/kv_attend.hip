@@ -507,18 +507,19 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attend_few_kernel(Atten
 // the bits 0x6400 | (code ^ 0x80); one packed operation takes the 1152 off
 // again) and lie there twice, so that one barrier a page is enough.
 //
-// All operands are exact: a query row is scaled by a power of two to a largest
-// magnitude in [2^14, 2^15) (bfloat16's 8 bits fit f16's 11), codes are whole
-// numbers.  The values' scales enter as powers of two relative to the unit of
-// the outputs so far, whose exponent follows the pages' largest: code 2^(e -
-// unit), exact in f16 from 2^-24 to 2^5.  For a page further below, the outputs
-// are moved to a lower unit and back after it, which takes nothing from them
-// down to 2^-96 of the largest.  Probabilities are rounded to f16 and their sum
-// is taken from the rounded ones, so that numerator and denominator agree.  They
-// are relative to a running reference, times 2^3, that is moved (and the outputs
-// scaled) where a page's maximum is 2^6 above it, or, where no maximum is sought,
-// where a lane's sum reaches 2^15, so that they stay f16; down to 2^-17 of the
-// reference they keep all of f16's bits, down to 2^-27 some.
+// The scores' operands are exact: a query row is scaled by a power of two to a
+// largest magnitude in [2^14, 2^15) (bfloat16's 8 bits fit f16's 11; what is below
+// 2^-31 of the largest is rounded to 2^-39 of it), codes are whole numbers.  The
+// values' scales enter as powers of two relative to the unit of the outputs so
+// far, whose exponent follows the pages' largest: code 2^(e - unit), exact in f16
+// from 2^-24 to 2^5.  For a page further below, the outputs are moved to a lower
+// unit and back after it, which takes nothing from them down to 2^-96 of the
+// largest.  Probabilities are rounded to f16 and their sum is taken from the
+// rounded ones, so that numerator and denominator agree.  They are relative to a
+// running reference, times 2^3, that is moved (and the outputs scaled) where a
+// page's maximum is 2^6 above it, or, where no maximum is sought, where a lane's
+// sum reaches 2^15, so that they stay f16; down to 2^-17 of the reference they
+// keep all of f16's bits, down to 2^-27 some.
 //
 // Rows and columns are arranged as above: the 32 x 32 output gives lane l,
 // register 4 a + b the row 8 a + 4 (l / 32) + b and takes the k-indexes 8 (l /

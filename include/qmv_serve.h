@@ -153,10 +153,11 @@ int qmv_kv_read(const qmv_kv_cache *cache, const qmv_kv_seqs *seqs, uint32_t dty
  * of up to 127 2^16 (a row's largest magnitude, a page's largest
  * probability), or, where bfloat16 queries are many (at least 16384 / head_dim
  * rows and heads to a sequence and key/value head, in a call of enough work,
- * by max_new and max_len), as float16: queries exactly, probabilities rounded
- * to 11 bits (below 2^-28 of the largest: to 0).  A query, or a page and head
- * that is seen, with a NaN or infinity gives NaN for the rows that see it and
- * touches no other.  Scores past float32's range may give NaN; values below
+ * by max_new and max_len), as float16: queries exactly down to 2^-31 of their
+ * row's largest (below it to 2^-39 of that), probabilities rounded to 11 bits
+ * (below 2^-28 of the largest: to 0).  A query, or a page and head that is seen,
+ * with a NaN or infinity gives NaN for the rows that see it and touches no
+ * other.  Scores past float32's range may give NaN; values below
  * 2^63 in magnitude never leave it.  Values below 2^-96, or below 2^-96 of the
  * largest of their sequence and head, may lose low bits or count as 0.  Scales
  * of the cache are taken to be powers of two, 0 or NaN, as qmv_kv_write makes
