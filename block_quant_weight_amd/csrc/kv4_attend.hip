@@ -1,0 +1,626 @@
+// Attention over the 4-bit cache.
+//
+// For a query row q at position p: s_j = scale q.k_j, out = sum_j e^{s_j} v_j
+// / sum_j e^{s_j} over the positions j it sees.
+//
+// A stored key or value is exact in bfloat16, and one instruction makes two of
+// them from their codes and their block's scale.  Both products run on the
+// bfloat16 matrix cores with float32 sums; the other operand is split so that
+// nothing that counts is rounded: float32 queries and probabilities into three
+// bfloat16 parts (24 bits, exact), bfloat16 queries are one part, and their
+// probabilities two (16 bits, where the output keeps 8).
+//
+// Layout: v_mfma_f32_16x16x32_bf16 takes from lane l eight k-indexes of row (or
+// column) l % 16, those of group l / 16, and gives lane l, register i the
+// output of row 4 (l / 16) + i and column l % 16.  The order of the k-indexes is
+// free as long as both operands agree, so
+//   keys: lane (t, g) has a quarter of token t's channels, from one load;
+//   scores: rows are tokens, so lane (column, g) gets those of the tokens 16 T +
+//     4 g + i, and these are the k-indexes that the output's product takes from
+//     it: probabilities stay in the lane that computed them;
+//   values: lane (c, g) has channel sixteenth c of the same tokens (the order
+//     in which they lie in the cache), and row r of the m-th product is channel
+//     (D / 16) r + m.
+// Neither operand goes through shared memory.
+//
+// Work: a workgroup of four waves has 16 columns (query row x head of one
+// key/value head) and a piece of the sequence's pages; each wave takes every
+// fourth page and keeps its own running maximum, sum and output, joined in
+// shared memory at the end.  Where there are columns enough, each wave has 16
+// of its own and all of their pages (SOLO).
+#include "kv4_common.h"
+
+namespace qmv {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+// The running reference moves when a maximum is further above it: e^s stays
+// below 2^8 times the reference's.
+constexpr float kMoveAt = 8.f;
+constexpr uint32_t kMaxPieces = 64;    // of a sequence
+constexpr uint32_t kScanSeqs = 1024;   // sequences up to which pieces are made
+
+struct Attend4Args {
+    qmv_kv4_cache c;
+    qmv_kv_seqs s;
+    const void* q;
+    void* out;
+    float* part;          // [room][kv_heads * group][D]: output sums of pieces
+    float2* stat;         // [room][kv_heads * group]: maximum, sum
+    float scale_log2;     // scale * log2(e)
+    uint32_t heads, group, window;
+    uint32_t target;      // pieces of all sequences that the launch aims at; 0: sequences stay whole
+    uint32_t least;       // pages of a piece, at least
+    uint32_t room;        // rows of pieces that the workspace holds
+};
+
+__device__ __forceinline__ float max_halves(float v) {
+    const uint32_t u = __builtin_bit_cast(uint32_t, v);
+    const auto a = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    const uint32_t x = a[0], y = a[1];
+    return fmaxf(__builtin_bit_cast(float, x), __builtin_bit_cast(float, y));
+}
+// Largest over the lanes 16, 32 and 48 apart.
+__device__ __forceinline__ float max_quads(float v) {
+    const uint32_t u = __builtin_bit_cast(uint32_t, v);
+    const auto a = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+    const uint32_t x = a[0], y = a[1];
+    return max_halves(fmaxf(__builtin_bit_cast(float, x), __builtin_bit_cast(float, y)));
+}
+
+// First position that a row at position p sees.
+__device__ __forceinline__ int32_t sees_from(uint32_t window, int32_t p) {
+    return window == 0 || window > static_cast<uint32_t>(max(p, 0)) ? 0 : p - static_cast<int32_t>(window) + 1;
+}
+
+// Positions that a table has room for.
+__device__ __forceinline__ int32_t room_of(const qmv_kv_seqs& s) {
+    return static_cast<int32_t>(min(s.table_stride, 0x7FFF0000u / kPage) * kPage);
+}
+
+// Pages [lo, hi) that any row of a sequence sees.
+struct Span {
+    int32_t lo, hi;
+};
+__device__ __forceinline__ Span span_of(const Attend4Args& a, const SeqRows& r) {
+    const int32_t hi = min(r.base + r.count, room_of(a.s));
+    Span o;
+    o.lo = sees_from(a.window, max(r.base, 0)) / kPage;
+    o.hi = max((max(hi, 0) + kPage - 1) / kPage, o.lo);
+    return o;
+}
+
+// How sequences are cut into pieces, the same in every wave that asks: the
+// pages of all are dealt out in `target` pieces of about one size, so a long
+// sequence beside short ones has more of them.  A sequence that is not whole
+// keeps its pieces' sums in the workspace's rows from `first` on, piece by
+// piece, its query rows one after another.
+struct Piece {
+    int32_t seq;                 // -1: none
+    uint32_t piece, pieces;
+    uint32_t first;
+};
+__device__ __forceinline__ uint32_t wave_sum_u32(uint32_t v) {
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1) v += static_cast<uint32_t>(__shfl_xor(static_cast<int>(v), m));
+    return v;
+}
+// Piece `slot` in the order of the sequences; with by_seq, piece 0 of sequence
+// `slot`.  All lanes of a wave call it together.
+__device__ __forceinline__ Piece find_piece(const Attend4Args& a, uint32_t slot, bool by_seq) {
+    const uint32_t seqs = a.s.seqs, lane = threadIdx.x & 63;
+    if (a.target == 0) return Piece{slot < seqs ? static_cast<int32_t>(slot) : -1, 0, 1, 0};
+    auto look = [&](uint32_t i, uint32_t* count) {
+        uint32_t pages = 0;
+        *count = 0;
+        if (i < seqs) {
+            const SeqRows r = seq_rows(a.s, i);
+            const Span sp = span_of(a, r);
+            *count = static_cast<uint32_t>(r.count);
+            pages = r.count > 0 ? static_cast<uint32_t>(sp.hi - sp.lo) : 0u;
+        }
+        return pages;
+    };
+    uint32_t count, mine = look(lane, &count), total = mine, most = mine;
+    for (uint32_t b = 64; b < seqs; b += 64) {
+        uint32_t n;
+        const uint32_t p = look(b + lane, &n);
+        total += p;                              // (at most 16 of 2^25 pages a lane)
+        most = max(most, p);
+    }
+    // (2^10 sequences of 2^25 pages: their sum is held in 64 bits)
+    uint64_t sum = total;
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1) {
+        const uint32_t lo = static_cast<uint32_t>(sum), hi = static_cast<uint32_t>(sum >> 32);
+        sum += static_cast<uint32_t>(__shfl_xor(static_cast<int>(lo), m)) |
+               static_cast<uint64_t>(static_cast<uint32_t>(__shfl_xor(static_cast<int>(hi), m))) << 32;
+        most = max(most, static_cast<uint32_t>(__shfl_xor(static_cast<int>(most), m)));
+    }
+    const uint32_t per = max(max(static_cast<uint32_t>((sum + a.target - 1) / a.target), a.least), (most + kMaxPieces - 1) / kMaxPieces);
+    uint32_t before = 0, kept = 0;               // pieces, and rows of the workspace, of the sequences before
+    for (uint32_t b = 0; b < seqs; b += 64) {
+        if (b > 0) mine = look(b + lane, &count);
+        uint32_t n = count > 0 ? max((mine + per - 1) / per, 1u) : 0u;
+        // (a sequence whose sums would not fit stays whole: rows below 2^31, pieces 64 at most)
+        uint64_t rows = n > 1 ? static_cast<uint64_t>(n) * count : 0u;
+        uint32_t need = rows > a.room ? a.room + 1 : static_cast<uint32_t>(rows);
+        uint32_t at = need, upto = n;
+        // inclusive sums over the lanes before (rows held to room + 1 and at most 2^31: no overflow in 64 bits)
+        uint64_t acc = need;
+#pragma unroll
+        for (int m = 1; m < 64; m <<= 1) {
+            const uint32_t lo = static_cast<uint32_t>(__shfl_up(static_cast<int>(static_cast<uint32_t>(acc)), m));
+            const uint32_t hi = static_cast<uint32_t>(__shfl_up(static_cast<int>(static_cast<uint32_t>(acc >> 32)), m));
+            if (lane >= static_cast<uint32_t>(m)) acc += lo | static_cast<uint64_t>(hi) << 32;
+        }
+        if (kept + acc > a.room) {               // from the first that does not fit on
+            if (n > 1) n = 1;
+            upto = n;
+        }
+        at = static_cast<uint32_t>(min(kept + acc - need, static_cast<uint64_t>(a.room)));
+#pragma unroll
+        for (int m = 1; m < 64; m <<= 1) {
+            const uint32_t u = static_cast<uint32_t>(__shfl_up(static_cast<int>(upto), m));
+            if (lane >= static_cast<uint32_t>(m)) upto += u;
+        }
+        const uint32_t start = before + upto - n;
+        const bool hit = by_seq ? b + lane == slot : (n > 0 && slot >= start && slot - start < n);
+        const uint64_t who = __ballot(hit);
+        if (who != 0) {
+            const int l = __builtin_ctzll(who);
+            Piece o;
+            o.seq = static_cast<int32_t>(b) + l;
+            o.pieces = static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(n), l));
+            o.piece = by_seq ? 0u : slot - static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(start), l));
+            o.first = static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(at), l));
+            return o;
+        }
+        before += static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(upto), 63));
+        const uint64_t end = kept + (static_cast<uint64_t>(static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(static_cast<uint32_t>(acc >> 32)), 63))) << 32 |
+                                     static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(static_cast<uint32_t>(acc)), 63)));
+        kept = end > a.room ? a.room + 1 : static_cast<uint32_t>(end);
+    }
+    return Piece{-1, 0, 1, 0};
+}
+
+// What a tile of columns is.  Columns of a sequence and key/value head (rows *
+// group, below 2^31) are numbered row first.
+struct Columns {
+    int32_t row;                 // this lane's query row in its sequence, -1: none
+    int32_t pos;                 // its position
+    uint32_t head;
+    int32_t first_pos, last_pos; // smallest and largest position of the columns
+    int32_t lo, hi;              // positions that any of the columns sees: [lo, hi)
+};
+template <uint32_t COLS>
+__device__ __forceinline__ Columns columns(const Attend4Args& a, const SeqRows& r, uint32_t kvh, uint32_t tile, uint32_t col) {
+    Columns o;
+    const uint32_t n = static_cast<uint32_t>(r.count) * a.group, c = tile * COLS + col;
+    const uint32_t t = c / a.group;
+    o.row = c < n ? static_cast<int32_t>(t) : -1;
+    o.pos = r.base + static_cast<int32_t>(t);
+    o.head = kvh * a.group + (c - t * a.group);
+    o.first_pos = r.base + static_cast<int32_t>(tile * COLS / a.group);
+    o.last_pos = r.base + static_cast<int32_t>(min(tile * COLS + COLS - 1, n - 1) / a.group);
+    o.hi = min(max(o.last_pos + 1, 0), room_of(a.s));
+    o.lo = sees_from(a.window, max(o.first_pos, 0));
+    return o;
+}
+
+// A float32 as N bfloat16 parts, the largest first (each cut off, so that the
+// next is exact; of three the sum is the number itself).
+template <int N>
+__device__ __forceinline__ void split(float x, uint32_t part[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const uint32_t b = __builtin_bit_cast(uint32_t, x);
+        part[i] = b;                             // (the upper half is taken)
+        x -= __builtin_bit_cast(float, b & 0xFFFF0000u);
+    }
+}
+// Upper halves of two words, as a pair.
+__device__ __forceinline__ uint32_t uppers(uint32_t lo, uint32_t hi) { return __builtin_amdgcn_perm(hi, lo, 0x07060302u); }
+__device__ __forceinline__ uint32_t lowers(uint32_t lo, uint32_t hi) { return __builtin_amdgcn_perm(hi, lo, 0x05040100u); }
+
+template <uint32_t DT, int D, bool SOLO>
+__global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attend4_few_kernel(Attend4Args a) {
+    typedef typename Elem<DT>::type T;
+    constexpr int STEP = SOLO ? 1 : 4;            // waves that share the pages
+    constexpr int NQ = DT == QMV_F32 ? 3 : 1;     // parts of a query
+    constexpr int NP = DT == QMV_F32 ? 3 : 2;     // parts of a probability
+    constexpr int KS = D / 32;                    // k-steps of a score tile
+    constexpr int W = D / 32;                     // words of a lane's quarter of a key, and of its four tokens' values
+    constexpr int E = D / 16;                     // channels of a sixteenth, and tiles of the output
+    __shared__ float acc[SOLO ? 1 : 4][SOLO ? 1 : 16][SOLO ? 1 : D + 1];
+    __shared__ float stat[SOLO ? 1 : 4][16][2];
+    const int lane = threadIdx.x & 63, quad = lane >> 4, col = lane & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint32_t kvh = blockIdx.x % a.c.kv_heads;
+    const Piece w0 = find_piece(a, blockIdx.x / a.c.kv_heads, false);
+    if (w0.seq < 0) return;
+    const uint32_t seq = static_cast<uint32_t>(w0.seq);
+    const SeqRows r = seq_rows(a.s, seq);
+    const uint32_t all = static_cast<uint32_t>(r.count) * a.group;
+    const uint32_t tiles = (all + 15) / 16;
+    const Span sp = span_of(a, r);
+    const int32_t per = (sp.hi - sp.lo + static_cast<int32_t>(w0.pieces) - 1) / static_cast<int32_t>(w0.pieces);
+    const int32_t b0 = min(sp.lo + static_cast<int32_t>(w0.piece) * per, sp.hi), b1 = min(b0 + per, sp.hi);
+    constexpr uint32_t kOwn = SOLO ? 4 : 1;       // tiles of a workgroup
+    // the last tiles see the most: they begin first
+    for (uint32_t turn = kOwn * blockIdx.y + (SOLO ? wave : 0); turn < tiles; turn += kOwn * gridDim.y) {
+        const uint32_t tile = tiles - 1 - turn;
+        const Columns w = columns<16>(a, r, kvh, tile, col);
+        const int32_t p0 = max(b0, w.lo / kPage), p1 = min(b1, (w.hi + kPage - 1) / kPage);
+        const int32_t see_lo = sees_from(a.window, w.pos);
+        // pages that every column sees whole: from full_lo up to full_hi
+        const int32_t full_lo = (sees_from(a.window, w.last_pos) + kPage - 1) / kPage;
+        const int32_t full_hi = max(w.first_pos + 1, 0) / kPage;
+
+        // Lane i has the id of the wave's page number i from here; keys and
+        // values of the next page are on the way while one is computed.
+        int32_t ids = -1;
+        auto look = [&](int32_t p) {
+            const int32_t mine = p + STEP * lane;
+            ids = mine < p1 ? page_id(a.c, a.s, seq, mine) : -1;
+        };
+        uint32_t kw[4][W], vw[4][W], ks[W > 4 ? 2 : 1], vs[4];
+        int32_t id = -1;
+        auto fetch_k = [&](int32_t at) {
+            // (where there is no page, page 0, which every cache has, is read and not used)
+            const uint64_t place = static_cast<uint64_t>(max(at, 0)) * a.c.kv_heads + kvh;
+            const uint8_t* kp = a.c.k + place * kCodeBytes<D> + k_at<D>(col, quad * W);
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int i = 0; i < W; ++i) kw[t][i] = reinterpret_cast<const uint32_t*>(kp + 16 * t * (D / 2))[i];
+            const uint8_t* sp = a.c.k_scale + place * kScaleBytes<D> + k_scale_at<D>(col, quad * W / 4);
+            ks[0] = reinterpret_cast<const uint32_t*>(sp)[0];
+            if constexpr (W > 4) ks[1] = reinterpret_cast<const uint32_t*>(sp)[1];
+        };
+        auto fetch_v = [&](int32_t at) {
+            const uint64_t place = static_cast<uint64_t>(max(at, 0)) * a.c.kv_heads + kvh;
+            const uint8_t* vp = a.c.v + place * kCodeBytes<D> + v_at<D>(4 * quad, E * col);
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int i = 0; i < W; ++i) vw[t][i] = reinterpret_cast<const uint32_t*>(vp + t * 16 * (D / 2))[i];
+            const uint4 s = *reinterpret_cast<const uint4*>(a.c.v_scale + place * kScaleBytes<D> + v_scale_at<D>(4 * quad, E * col / kBlock));
+            vs[0] = s.x; vs[1] = s.y; vs[2] = s.z; vs[3] = s.w;
+        };
+        look(p0 + (SOLO ? 0 : wave));
+        // the query: lane (column, g) has the channels that lane (t, g) has of a key
+        bf16x8 qf[KS][NQ];
+        {
+            const uint64_t row = static_cast<uint64_t>(r.first + max(w.row, 0));
+            const T* qp = static_cast<const T*>(a.q) + (row * a.heads + w.head) * D + quad * (D / 4);
+#pragma unroll
+            for (int s = 0; s < KS; ++s) {
+                float x[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[i] = 0.f;
+                if (w.row >= 0) load8<DT>(qp + 8 * s, x);
+                uint32_t part[8][NQ];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) split<NQ>(x[i], part[i]);
+#pragma unroll
+                for (int n = 0; n < NQ; ++n)
+                    qf[s][n] = __builtin_bit_cast(bf16x8, make_uint4(uppers(part[0][n], part[1][n]), uppers(part[2][n], part[3][n]),
+                                                                     uppers(part[4][n], part[5][n]), uppers(part[6][n], part[7][n])));
+            }
+        }
+        int n = 0;
+        id = __builtin_amdgcn_readlane(ids, 0);
+        fetch_k(id);
+        fetch_v(id);
+
+        f32x4 o[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] = f32x4{0.f, 0.f, 0.f, 0.f};
+        float m_run = -__builtin_inff(), l_run = 0.f;
+
+        for (int32_t p = p0 + (SOLO ? 0 : wave); p < p1; p += STEP) {
+            const int32_t here = id;
+            if (++n == 64) {
+                look(p + STEP);
+                n = 0;
+            }
+            id = __builtin_amdgcn_readlane(ids, n);
+            const bool edge = p < full_lo || p >= full_hi;
+            // scores
+            f32x4 sc[4];
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                sc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int s = 0; s < KS; ++s) {
+                    const uint32_t byte = ks[s / 4] >> (8 * t) & 0xFFu;
+                    const bf16x8 k = values8(kw[t][s], scale_of(byte));
+#pragma unroll
+                    for (int i = NQ - 1; i >= 0; --i) sc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k, qf[s][i], sc[t], 0, 0, 0);
+                }
+            }
+            fetch_k(id);
+            if (here >= 0) {
+                if (edge) {
+                    // scores of what a column does not see, and values that none does: the
+                    // memory behind a sequence's end may hold anything
+                    const int32_t t0 = p * kPage + 4 * quad;
+                    const int32_t to = w.row < 0 ? 0 : w.pos + 1;
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int32_t at = t0 + 16 * t + i;
+                            sc[t][i] = at >= see_lo && at < to ? sc[t][i] * a.scale_log2 : -__builtin_inff();
+                            if (at < w.lo || at >= w.hi) {
+                                vs[t] = (vs[t] & ~(0xFFu << (8 * i))) | 127u << (8 * i);
+                                if constexpr (W == 2) vw[t][i / 2] &= i % 2 == 0 ? 0xFFFF0000u : 0xFFFFu;
+                                else
+#pragma unroll
+                                    for (int u = 0; u < W / 4; ++u) vw[t][i * (W / 4) + u] = 0u;
+                            }
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) sc[t] *= a.scale_log2;
+                }
+                float mt = -__builtin_inff();
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) mt = fmaxf(mt, sc[t][i]);
+                mt = max_quads(mt);
+                if (__any(mt > m_run + kMoveAt || (m_run == -__builtin_inff() && mt > m_run))) {
+                    const float m_new = mt > m_run + kMoveAt || m_run == -__builtin_inff() ? fmaxf(mt, m_run) : m_run;
+                    const float keep = m_new == m_run ? 1.f : __builtin_amdgcn_exp2f(m_run - m_new);
+                    m_run = m_new;
+                    l_run *= keep;
+#pragma unroll
+                    for (int e = 0; e < E; ++e) o[e] *= keep;
+                }
+                // (a column that has seen nothing yet: e^-inf, not inf - inf)
+                const float base = m_run > -__builtin_inff() ? m_run : 0.f;
+                uint32_t pp[4][4][NP];
+                float l = 0.f;
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float x = __builtin_amdgcn_exp2f(sc[t][i] - base);
+                        l += x;
+                        split<NP>(x, pp[t][i]);
+                    }
+                l_run += l;
+                // outputs: two steps of 32 tokens
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    bf16x8 pf[NP];
+#pragma unroll
+                    for (int k = 0; k < NP; ++k)
+                        pf[k] = __builtin_bit_cast(bf16x8, make_uint4(uppers(pp[2 * s][0][k], pp[2 * s][1][k]), uppers(pp[2 * s][2][k], pp[2 * s][3][k]),
+                                                                      uppers(pp[2 * s + 1][0][k], pp[2 * s + 1][1][k]), uppers(pp[2 * s + 1][2][k], pp[2 * s + 1][3][k])));
+#pragma unroll
+                    for (int b = 0; b < E / 2; ++b) {      // a byte of a sixteenth: two channels
+                        uint32_t x[8];
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const int t = 2 * s + j / 4, i = j % 4, at = i * (E / 2) + b;
+                            const float d = scale_of(vs[t] >> (8 * i) & 0xFFu);
+                            const uint32_t u = vw[t][at / 4];
+                            x[j] = at % 4 == 0 ? pair_bf16<0>(u, d) : (at % 4 == 1 ? pair_bf16<1>(u, d) : (at % 4 == 2 ? pair_bf16<2>(u, d) : pair_bf16<3>(u, d)));
+                        }
+                        const bf16x8 even = __builtin_bit_cast(bf16x8, make_uint4(lowers(x[0], x[1]), lowers(x[2], x[3]), lowers(x[4], x[5]), lowers(x[6], x[7])));
+                        const bf16x8 odd = __builtin_bit_cast(bf16x8, make_uint4(uppers(x[0], x[1]), uppers(x[2], x[3]), uppers(x[4], x[5]), uppers(x[6], x[7])));
+#pragma unroll
+                        for (int k = NP - 1; k >= 0; --k) {
+                            o[2 * b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(even, pf[k], o[2 * b], 0, 0, 0);
+                            o[2 * b + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(odd, pf[k], o[2 * b + 1], 0, 0, 0);
+                        }
+                    }
+                }
+            }
+            fetch_v(id);
+        }
+        l_run += __shfl_xor(l_run, 16);
+        l_run += __shfl_xor(l_run, 32);
+
+        // where a column's output goes: into `out`, or to the piece's row
+        const uint64_t piece_row = w0.first + static_cast<uint64_t>(w0.piece) * static_cast<uint32_t>(r.count);
+        if constexpr (SOLO) {
+            if (w.row >= 0) {
+                const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
+                T* op = static_cast<T*>(a.out) + (static_cast<uint64_t>(r.first + w.row) * a.heads + w.head) * D;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int e = 0; e < E; e += 4) {
+                        const int ch = E * (4 * quad + i) + e;
+                        if constexpr (DT == QMV_F32) {
+                            *reinterpret_cast<float4*>(op + ch) = make_float4(o[e][i] * inv, o[e + 1][i] * inv, o[e + 2][i] * inv, o[e + 3][i] * inv);
+                        } else {
+                            typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+                            const bf16x4 v = {static_cast<__bf16>(o[e][i] * inv), static_cast<__bf16>(o[e + 1][i] * inv),
+                                              static_cast<__bf16>(o[e + 2][i] * inv), static_cast<__bf16>(o[e + 3][i] * inv)};
+                            *reinterpret_cast<bf16x4*>(op + ch) = v;
+                        }
+                    }
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int e = 0; e < E; ++e) acc[wave][col][E * (4 * quad + i) + e] = o[e][i];
+            if (quad == 0) {
+                stat[wave][col][0] = m_run;
+                stat[wave][col][1] = l_run;
+            }
+            __syncthreads();
+            // thread: a column, and a sixteenth of its channels
+            const int c = threadIdx.x >> 4, part = threadIdx.x & 15;
+            const uint32_t at = tile * 16 + c;
+            if (at < all) {
+                float m = stat[0][c][0];
+#pragma unroll
+                for (int k = 1; k < 4; ++k) m = fmaxf(m, stat[k][c][0]);
+                float f[4], l = 0.f;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    // (waves that saw nothing have the maximum -infinity and the sum 0)
+                    f[k] = stat[k][c][0] == m ? 1.f : __builtin_amdgcn_exp2f(stat[k][c][0] - m);
+                    l = fmaf(f[k], stat[k][c][1], l);
+                }
+                const uint32_t row = at / a.group, head = kvh * a.group + at % a.group;
+                const float inv = w0.pieces > 1 ? 1.f : (l == 0.f ? 0.f : 1.f / l);
+                const uint64_t slot = (piece_row + row) * a.heads + head;
+                if (w0.pieces > 1 && part == 0) a.stat[slot] = make_float2(m, l);
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    const int ch = part + 16 * e;
+                    float v = 0.f;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) v = fmaf(f[k], acc[k][c][ch], v);
+                    v *= inv;
+                    if (w0.pieces > 1) {
+                        a.part[slot * D + ch] = v;
+                    } else {
+                        const uint64_t to = (static_cast<uint64_t>(r.first + static_cast<int32_t>(row)) * a.heads + head) * D + ch;
+                        if constexpr (DT == QMV_F32) static_cast<float*>(a.out)[to] = v;
+                        else static_cast<__bf16*>(a.out)[to] = static_cast<__bf16>(v);
+                    }
+                }
+            }
+            __syncthreads();
+        }
+    }
+}
+
+// Joins the pieces of each column of a sequence that was cut: a wave has a
+// column, lane z piece z's maximum and sum, and the pieces' outputs are added
+// in their order, D / 64 values a lane.
+template <uint32_t DT, int D>
+__global__ __launch_bounds__(256) void attend4_join_kernel(Attend4Args a) {
+    constexpr int V = D / 64;
+    const int lane = threadIdx.x & 63;
+    const uint32_t wave = static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6)));
+    const Piece w = find_piece(a, blockIdx.x, true);
+    if (w.seq < 0 || w.pieces <= 1) return;
+    const SeqRows r = seq_rows(a.s, static_cast<uint32_t>(w.seq));
+    const uint64_t n = static_cast<uint64_t>(r.count) * a.heads;
+    for (uint64_t i = static_cast<uint64_t>(blockIdx.y) * 4 + wave; i < n; i += static_cast<uint64_t>(gridDim.y) * 4) {
+        // (a piece's rows and heads are as those of the output)
+        const uint64_t from = static_cast<uint64_t>(w.first) * a.heads + i;
+        float2 st = make_float2(-__builtin_inff(), 0.f);
+        if (static_cast<uint32_t>(lane) < w.pieces) st = a.stat[from + lane * n];
+        float m = st.x;
+#pragma unroll
+        for (int k = 1; k < 64; k <<= 1) m = fmaxf(m, __shfl_xor(m, k));
+        const float f = st.x == m ? 1.f : __builtin_amdgcn_exp2f(st.x - m);
+        float l = f * st.y;
+#pragma unroll
+        for (int k = 1; k < 64; k <<= 1) l += __shfl_xor(l, k);
+        float v[V];
+#pragma unroll
+        for (int k = 0; k < V; ++k) v[k] = 0.f;
+        for (uint32_t z = 0; z < w.pieces; z += 8) {
+            float x[8][V];
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+#pragma unroll
+                for (int k = 0; k < V; ++k) x[u][k] = z + u < w.pieces ? a.part[(from + (z + u) * n) * D + lane * V + k] : 0.f;
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const float g = z + u < w.pieces ? read_lane(f, static_cast<int>(z + u)) : 0.f;
+#pragma unroll
+                for (int k = 0; k < V; ++k) v[k] = fmaf(g, x[u][k], v[k]);
+            }
+        }
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const uint64_t to = (static_cast<uint64_t>(r.first) * a.heads + i) * D + lane * V;
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            if constexpr (DT == QMV_F32) static_cast<float*>(a.out)[to + k] = v[k] * inv;
+            else static_cast<__bf16*>(a.out)[to + k] = static_cast<__bf16>(v[k] * inv);
+        }
+    }
+}
+
+// Pages that a tile of columns may see, as far as the host knows.
+uint64_t span_pages(const qmv_kv_seqs& s, uint32_t window, uint64_t rows) {
+    uint64_t span = s.max_len;
+    if (window != 0 && span > uint64_t{window} + rows) span = uint64_t{window} + rows;
+    return (span + kPage - 1) / kPage + 1;
+}
+
+struct Plan {
+    bool solo;
+    uint32_t tiles, target, least, slots;
+    uint64_t room;
+};
+constexpr uint32_t kWorkgroups = 512;          // that a launch aims at
+constexpr uint32_t kWhole = 16;                // pages up to which a sequence is not cut
+
+Plan plan_of(const qmv_kv4_cache& c, const qmv_kv_seqs& s, uint32_t heads, uint32_t window) {
+    const uint64_t group = heads / c.kv_heads;
+    const uint64_t most = s.max_new < s.rows ? (s.max_new == 0 ? 1 : s.max_new) : s.rows;
+    uint64_t tiles = (most * group + 15) / 16;
+    const uint64_t wgs = uint64_t{s.seqs} * c.kv_heads * tiles, pages = span_pages(s, window, most);
+    Plan p{};
+    p.solo = wgs >= 1024;
+    if (p.solo) tiles = (tiles + 3) / 4;
+    p.tiles = static_cast<uint32_t>(tiles > 65535 ? 65535 : tiles);
+    p.slots = s.seqs;
+    if (p.solo || s.seqs > kScanSeqs || pages <= kWhole) return p;
+    uint64_t target = (kWorkgroups + c.kv_heads * tiles - 1) / (c.kv_heads * tiles);
+    if (target < s.seqs / 2) target = s.seqs / 2;
+    if (target < 1) target = 1;
+    p.target = static_cast<uint32_t>(target);
+    p.least = 4;
+    p.slots = p.target + s.seqs;
+    const uint64_t pieces = target < kMaxPieces ? target : kMaxPieces;
+    uint64_t room = pieces * s.rows;
+    if (room > p.slots * most) room = p.slots * most;
+    p.room = room > 0x7FFFFFFFu ? 0x7FFFFFFFu : room;
+    return p;
+}
+
+template <uint32_t DT, int D>
+hipError_t go(const Attend4Args& a, const Plan& p, hipStream_t s) {
+    const dim3 grid(p.slots * a.c.kv_heads, p.tiles), block(256);
+    if (p.solo) hipLaunchKernelGGL((attend4_few_kernel<DT, D, true>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((attend4_few_kernel<DT, D, false>), grid, block, 0, s, a);
+    hipError_t e = hipGetLastError();
+    if (e == hipSuccess && p.target != 0) {
+        const uint64_t most = a.s.max_new < a.s.rows ? a.s.max_new : a.s.rows;
+        uint64_t y = (most * a.heads + 3) / 4;
+        if (y < 1) y = 1;
+        if (y > 65535) y = 65535;
+        hipLaunchKernelGGL((attend4_join_kernel<DT, D>), dim3(a.s.seqs, static_cast<uint32_t>(y)), block, 0, s, a);
+        e = hipGetLastError();
+    }
+    return e;
+}
+template <uint32_t DT>
+hipError_t go(const Attend4Args& a, const Plan& p, hipStream_t s) {
+    if (a.c.head_dim == 64) return go<DT, 64>(a, p, s);
+    if (a.c.head_dim == 128) return go<DT, 128>(a, p, s);
+    return go<DT, 256>(a, p, s);
+}
+
+}  // namespace
+
+uint64_t kv4_attend_workspace_bytes(const qmv_kv4_cache& c, const qmv_kv_seqs& s, uint32_t, uint32_t heads, uint32_t window) {
+    return plan_of(c, s, heads, window).room * heads * (c.head_dim + 2) * 4;
+}
+
+hipError_t launch_kv4_attend(const qmv_kv4_cache& c, const qmv_kv_seqs& s, uint32_t dtype, uint32_t heads, float scale, uint32_t window,
+                             const void* q, void* out, void* workspace, hipStream_t stream) {
+    const Plan p = plan_of(c, s, heads, window);
+    float* part = static_cast<float*>(workspace);
+    const Attend4Args a{c, s, q, out, part, reinterpret_cast<float2*>(part + p.room * heads * c.head_dim), scale * kLog2e, heads,
+                        heads / c.kv_heads, window, p.target, p.least, static_cast<uint32_t>(p.room)};
+    return dtype == QMV_F32 ? go<QMV_F32>(a, p, stream) : go<QMV_BF16>(a, p, stream);
+}
+
+}  // namespace qmv

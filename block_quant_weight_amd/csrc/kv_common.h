@@ -24,7 +24,8 @@ __device__ __forceinline__ SeqRows seq_rows(const qmv_kv_seqs& s, uint32_t i) {
 }
 
 // Page id of a sequence's page number p, or -1 where there is none.
-__device__ __forceinline__ int32_t page_id(const qmv_kv_cache& c, const qmv_kv_seqs& s, uint32_t seq, int32_t p) {
+template <typename Cache>
+__device__ __forceinline__ int32_t page_id(const Cache& c, const qmv_kv_seqs& s, uint32_t seq, int32_t p) {
     if (p < 0 || static_cast<uint32_t>(p) >= s.table_stride) return -1;
     const int32_t id = s.table[static_cast<uint64_t>(seq) * s.table_stride + p];
     return id >= 0 && static_cast<uint32_t>(id) < c.pages ? id : -1;

@@ -1,8 +1,9 @@
 /*
  * qmv_serve.h - the operators between a quantized model's products, on one
- * MI355X (gfx950): the norm in front of a product, a key/value cache held in
- * 8 bits, attention over that cache, and the log probabilities of the LM
- * head's logits.  Plain C ABI beside qmv.h, whose products take what these
+ * MI355X (gfx950): the norm in front of a product, the heads' norm with the
+ * position's rotation, a key/value cache held in 8 or in 4 bits, attention
+ * over either, the log probabilities of the LM head's logits, and the next
+ * token drawn from them.  Plain C ABI beside qmv.h, whose products take what these
  * calls give: the status codes, the meaning of `stream` and "device pointer"
  * are the ones of qmv.h.
  *
@@ -175,6 +176,110 @@ int qmv_kv_attend(const qmv_kv_cache *cache, const qmv_kv_seqs *seqs, uint32_t d
                   void *workspace, uint64_t workspace_bytes, void *stream);
 
 /*
+ * Norm of query and key heads, with the position's rotation in the same pass.
+ * For each of `rows` rows and each head x of head_dim values, with n =
+ * head_dim, in float32 (squares are summed in 64 bits):
+ *   y = (x r) w, r = 1 / sqrt(sum x^2 / n + eps)   (y = x where w is NULL)
+ * and then, for i < rot / 2, with the angle pos[row] freq[i] taken in 64 bits,
+ * c and s its cosine and sine times mscale, each pair (a, b) of y becomes
+ *   (a c - b s, b c + a s);
+ * pairs are (y[i], y[i + rot / 2]), or with neighbours != 0 (y[2 i], y[2 i +
+ * 1]).  Channels from rot on stay as they are.  Any frequency scheme is a
+ * choice of freq and mscale.  The result is rounded once to out_dtype.
+ * q, k: the heads of the queries and of the keys; either may be NULL.
+ *   x, y        dtype and out_dtype, [rows][heads][head_dim], rows x_stride
+ *               and y_stride elements apart: slices of one array of all
+ *               projections, say.  y may be x itself (the same stride and type).
+ *   w           float32 [head_dim], or NULL: no norm
+ * pos: int32 [rows], any value.  freq: float32 [rot / 2] (may be NULL if rot
+ * is 0).  Device memory; x, y, w 16-byte aligned, pos and freq 4-byte aligned;
+ * head_dim a multiple of 8, at most 512; rot a multiple of 16, at most
+ * head_dim; strides multiples of 8, at least heads * head_dim.
+ * Errors: QMV_E_ARG (q and k NULL, a NULL or misaligned pointer, a dtype
+ * unknown, rows or heads 0, eps negative, infinite or NaN, mscale infinite or
+ * NaN, y is x with another stride or type), QMV_E_SHAPE (head_dim, rot, strides,
+ * heads above 2^20, rows above 2^31 - 2^16, strides above 2^40), QMV_E_DEVICE.
+ */
+typedef struct qmv_heads {
+    const void *x;
+    void *y;
+    const float *w;
+    uint64_t x_stride, y_stride;
+    uint32_t heads;
+} qmv_heads;
+int qmv_qk_rotate(const qmv_heads *q, const qmv_heads *k, uint32_t rows, uint32_t head_dim,
+                  uint32_t dtype, uint32_t out_dtype, float eps, const int32_t *pos,
+                  const float *freq, uint32_t rot, uint32_t neighbours, float mscale, void *stream);
+
+/*
+ * A key/value cache in 4 bits: pages of QMV_KV_PAGE tokens; each block of 32
+ * channels of one token and head has a scale byte b and 32 codes of 4 bits, a
+ * sign (8) above an index into 0, .5, 1, 1.5, 2, 3, 4, 6: a stored value is
+ * that times 2^(b - 127), exact in float32 and in bfloat16.  4.25 bits a
+ * value.  All arrays are the caller's device memory, 16-byte aligned:
+ *   k, v               uint8 [pages][kv_heads][64 * head_dim / 2]
+ *   k_scale, v_scale   uint8 [pages][kv_heads][64 * head_dim / 32]
+ * head_dim is 64, 128 or 256.  Within a page and head, token t keeps (two
+ * codes a byte, the lower channel in the lower half; all byte offsets)
+ *   channel c of its key      at t * head_dim / 2 + c / 2
+ *   block b's scale of it     at ((t % 16) * (head_dim / 32) + b) * 4 + t / 16
+ *   channel c of its value    at ((t / 4 * 16 + c / e) * 4 + t % 4) * e / 2 + c % e / 2,
+ *                             e = head_dim / 16
+ *   block b's scale of it     at ((t / 4 % 4 * (head_dim / 32) + b) * 4 + t / 16) * 4 + t % 4
+ * A new cache needs no initialisation.  A token's bytes depend on that token
+ * alone; pages may be copied as they are.
+ */
+typedef struct qmv_kv4_cache {
+    uint8_t *k;
+    uint8_t *v;
+    uint8_t *k_scale;
+    uint8_t *v_scale;
+    uint32_t pages, kv_heads, head_dim;
+} qmv_kv4_cache;
+
+/*
+ * Writes the rows of k and v ([rows][kv_heads][head_dim], dtype) into the
+ * cache: for each block, with amax its largest magnitude, d the least power of
+ * two from 2^-125 to 2^125 with amax <= 7 d (the ends where there is none), and
+ * codes of x / d to the nearest value, halves to the even code, at most 6 (so
+ * a stored value is within d / 4 of values below 2 d, d / 2 below 4 d, d above).
+ * An infinite or NaN value makes its token's keys and values of that head NaN
+ * (key scale bytes 255, values 0) until the token is written again.
+ * A call must not write one place twice.  seqs as for qmv_kv_write.
+ * Errors: as qmv_kv_write.
+ */
+int qmv_kv4_write(const qmv_kv4_cache *cache, const qmv_kv_seqs *seqs, uint32_t dtype,
+                  const void *k, const void *v, void *stream);
+
+/*
+ * Reads the rows' tokens back into k and v ([rows][kv_heads][head_dim],
+ * dtype), exactly.  Either of k and v may be NULL.  Errors: as qmv_kv_read.
+ */
+int qmv_kv4_read(const qmv_kv4_cache *cache, const qmv_kv_seqs *seqs, uint32_t dtype, void *k,
+                 void *v, void *stream);
+
+/*
+ * Attention of the rows over the cache: as qmv_kv_attend, with its arguments,
+ * positions, window and zero rows.  Scores, the softmax's statistics and the
+ * output sums are float32.  Queries enter the products exactly; probabilities
+ * exactly with float32, with 16 bits or, where bfloat16 queries are many,
+ * 11 bits.  A query, or a token and head that is seen, with a NaN or infinity
+ * gives NaN for the rows that see it and touches no other.  Scores past
+ * float32's range may give NaN; values below 2^62 in magnitude never leave it.
+ * Values below 2^-96 may lose low bits or count as 0.
+ * A sequence's pages are cut into pieces by its own length beside the others',
+ * so one long sequence among short ones uses the whole GPU; max_new and max_len
+ * only choose the kernel and how many pieces there are in all.
+ * workspace: device memory of at least qmv_kv4_attend_workspace bytes (may be
+ * NULL where that is 0), 16-byte aligned.  Errors: as qmv_kv_attend.
+ */
+int qmv_kv4_attend_workspace(const qmv_kv4_cache *cache, const qmv_kv_seqs *seqs, uint32_t dtype,
+                             uint32_t heads, uint32_t window, uint64_t *bytes);
+int qmv_kv4_attend(const qmv_kv4_cache *cache, const qmv_kv_seqs *seqs, uint32_t dtype,
+                   uint32_t heads, float scale, uint32_t window, const void *q, void *out,
+                   void *workspace, uint64_t workspace_bytes, void *stream);
+
+/*
  * Log probabilities of given tokens, with the distribution's entropy and its
  * top alternatives, from logits [rows][vocab] (float32, as qmv_gemv writes
  * an LM head's).  With p = softmax of a row:
@@ -200,6 +305,38 @@ int qmv_logprobs_workspace(uint32_t rows, uint32_t vocab, uint32_t top, uint64_t
 int qmv_logprobs(const float *logits, uint32_t rows, uint32_t vocab, const int32_t *ids,
                  uint32_t n_ids, uint32_t top, float *lp, float *entropy, int32_t *top_ids,
                  float *top_lp, void *workspace, uint64_t workspace_bytes, void *stream);
+
+/*
+ * The next token of each row, drawn from logits [rows][vocab] (float32, as
+ * qmv_gemv writes an LM head's) with a given random number.  For a row with
+ * temperature T, tokens in the order of their logits x, the largest first,
+ * equal ones by the lower index, and weights w = e^((x - x_max) / T):
+ *   top_k  k > 0: the first k tokens stay (k <= 0: all)
+ *   top_p  p < 1: of these, a token stays if the weights before it sum to
+ *          less than p times the sum of all of these; the first always stays
+ *   min_p  of these, a token stays if w >= m; the first always stays
+ * and ids[row] is the first token, by index, at which the sum of the weights
+ * of the tokens that stayed exceeds u times their total.  lp[row] = ln of that
+ * token's weight over the total.  T = 0 takes the first token in the order
+ * (lp 0).  u outside [0, 1) counts as the nearer end, NaN as 0.  A row that
+ * holds a NaN or +infinity, or nothing but -infinity, or whose T is negative,
+ * infinite or NaN, gets the id -1 and lp NaN.  A NaN in top_p or min_p turns
+ * that filter off; p below 0 counts as 0, m above 1 as 1.
+ * Weights are whole multiples of 2^-39 of the largest; sums are whole numbers,
+ * so a row's result depends on that row alone.
+ * u, temperature, top_p, min_p: float32 [rows], top_k: int32 [rows]; each of
+ * the last four may be NULL (T = 1, or no such filter).  ids: int32 [rows];
+ * lp: float32 [rows], may be NULL.  All 4-byte aligned device memory;
+ * workspace: 16-byte aligned, at least qmv_sample_workspace bytes.
+ * Errors: QMV_E_ARG (logits, u or ids NULL, misaligned pointer, rows or vocab
+ * 0, workspace NULL or too small), QMV_E_SHAPE (vocab above 2^24, rows above
+ * 2^22), QMV_E_DEVICE.
+ */
+int qmv_sample_workspace(uint32_t rows, uint32_t vocab, uint64_t *bytes);
+int qmv_sample(const float *logits, uint32_t rows, uint32_t vocab, const float *u,
+               const float *temperature, const int32_t *top_k, const float *top_p,
+               const float *min_p, int32_t *ids, float *lp, void *workspace,
+               uint64_t workspace_bytes, void *stream);
 
 #ifdef __cplusplus
 }
