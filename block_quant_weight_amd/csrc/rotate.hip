@@ -31,6 +31,17 @@ __device__ __forceinline__ double group_sum(double v) {
     return v;
 }
 
+// 1 / sqrt(v): the instruction's estimate and two of Newton's steps y (3 - v
+// y^2) / 2, each of which doubles its correct bits.
+__device__ __forceinline__ float root(double v) {
+    double y = __builtin_amdgcn_rsq(v);
+    if (v > 0.0 && v < __builtin_inf()) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) y = fma(0.5 * y, fma(-v * y, y, 1.0), y);
+    }
+    return static_cast<float>(y);
+}
+
 template <uint32_t IN, uint32_t OUT, int G, bool NEIGHBOURS>
 __global__ __launch_bounds__(kThreads) void rotate_kernel(RotateArgs a) {
     typedef typename Elem<IN>::type TI;
@@ -87,8 +98,7 @@ __global__ __launch_bounds__(kThreads) void rotate_kernel(RotateArgs a) {
                 double sum = 0.0;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) sum = fma(static_cast<double>(x[i]), static_cast<double>(x[i]), sum);
-                const float v = static_cast<float>(fma(group_sum<G>(sum), a.inv_dim, static_cast<double>(a.eps)));
-                const float r = 1.f / sqrtf(v);
+                const float r = root(fma(group_sum<G>(sum), a.inv_dim, static_cast<double>(a.eps)));
                 if (live) {
                     const float4 lo = reinterpret_cast<const float4*>(w + at)[0], hi = reinterpret_cast<const float4*>(w + at)[1];
                     const float u[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};

@@ -453,8 +453,10 @@ def qmv_qk_rotate(q, k, pos, freq, q_out, k_out, q_w=None, k_w=None, eps=1e-6, n
     pos: int32 [rows]; freq: float32 [rot / 2], radians a position, of the
     first rot channels, paired by halves or with neighbours=True side by side."""
     t, o = (q, q_out) if q is not None else (k, k_out)
-    if t is None or o is None:
+    if t is None:
         raise QmvError(QMV_E_ARG, "qmv_qk_rotate")
+    if o is None:
+        raise ValueError("an output is missing")
     if t.dim() != 3:
         raise ValueError("q and k must be [rows, heads, head_dim]")
     rows, _, dim = t.shape
