@@ -20,7 +20,11 @@ namespace {
 
 #pragma clang fp contract(off)
 
-constexpr int kThreads = 1024, kWaves = kThreads / 64;
+// An address in shared memory, as a function that is called takes it: through a
+// plain pointer its reads and writes would not be known to go there.
+typedef __attribute__((address_space(3))) uint8_t* Lds;
+
+constexpr int kThreads = 512, kWaves = kThreads / 64;
 constexpr int kBins = 2048;
 constexpr float kUnit = 0x1p39f;            // the largest weight as a whole number
 
@@ -30,27 +34,44 @@ __device__ __forceinline__ uint32_t key_of(float x) {
     return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
-__device__ __forceinline__ uint64_t shfl_u64(uint64_t v, int from) {
-    const uint32_t lo = static_cast<uint32_t>(__shfl(static_cast<int>(static_cast<uint32_t>(v)), from));
-    const uint32_t hi = static_cast<uint32_t>(__shfl(static_cast<int>(static_cast<uint32_t>(v >> 32)), from));
-    return static_cast<uint64_t>(hi) << 32 | lo;
+// A value from the lanes that CTRL names, 0 where there is none (or in rows of
+// 16 lanes that ROWS leaves out).
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint64_t dpp_u64(uint64_t v) {
+    const int lo = __builtin_amdgcn_update_dpp(0, static_cast<int>(static_cast<uint32_t>(v)), CTRL, ROWS, 0xF, true);
+    const int hi = __builtin_amdgcn_update_dpp(0, static_cast<int>(static_cast<uint32_t>(v >> 32)), CTRL, ROWS, 0xF, true);
+    return static_cast<uint64_t>(static_cast<uint32_t>(hi)) << 32 | static_cast<uint32_t>(lo);
 }
-// Sum over a wave, in every lane; and over the lanes up to this one.
-__device__ __forceinline__ uint64_t wave_sum(uint64_t v) {
-    const int lane = threadIdx.x & 63;
-#pragma unroll
-    for (int m = 1; m < 64; m <<= 1) v += shfl_u64(v, lane ^ m);
-    return v;
+__device__ __forceinline__ uint64_t read_lane_u64(uint64_t v, int lane) {
+    return static_cast<uint64_t>(static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(static_cast<uint32_t>(v >> 32)), lane))) << 32 |
+           static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(static_cast<uint32_t>(v)), lane));
 }
+// Sums over the lanes of a row of 16 up to this one.
+__device__ __forceinline__ uint64_t row_scan(uint64_t v) {
+    v += dpp_u64<0x111, 0xF>(v);   // lanes 1, 2, 4, 8 before
+    v += dpp_u64<0x112, 0xF>(v);
+    v += dpp_u64<0x114, 0xF>(v);
+    return v + dpp_u64<0x118, 0xF>(v);
+}
+// Sums over the lanes of a wave up to this one; over all.
 __device__ __forceinline__ uint64_t wave_scan(uint64_t v) {
-    const int lane = threadIdx.x & 63;
-#pragma unroll
-    for (int m = 1; m < 64; m <<= 1) {
-        const uint64_t u = shfl_u64(v, lane >= m ? lane - m : lane);
-        if (lane >= m) v += u;
-    }
-    return v;
+    v = row_scan(v);
+    v += dpp_u64<0x142, 0xA>(v);   // a row's last lane to the next row
+    return v + dpp_u64<0x143, 0xC>(v);   // the first half's last lane to the second half
 }
+__device__ __forceinline__ uint64_t wave_sum(uint64_t v) { return read_lane_u64(wave_scan(v), 63); }
+// Largest over a row of 16 lanes, in each.
+__device__ __forceinline__ float row_max(float v) {
+    v = fmaxf(v, dpp_mov<0xB1>(v));    // lanes 1 apart
+    v = fmaxf(v, dpp_mov<0x4E>(v));    // 2 apart
+    v = fmaxf(v, dpp_mov<0x141>(v));   // half rows mirrored
+    return fmaxf(v, dpp_mov<0x140>(v));
+}
+__device__ __forceinline__ float wave_max(float v) {
+    v = row_max(v);
+    return fmaxf(fmaxf(read_lane(v, 0), read_lane(v, 16)), fmaxf(read_lane(v, 32), read_lane(v, 48)));
+}
+__device__ __forceinline__ int this_wave() { return __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6)); }
 
 // How a row's weights are formed.
 struct Weigher {
@@ -65,8 +86,8 @@ struct Weigher {
         const float hi = d * c;
         return make_float2(hi, fmaf(e, c, fmaf(d, c_low, fmaf(d, c, -hi))));
     }
-    __device__ __forceinline__ uint64_t operator()(float x) const {
-        const float2 t = log2_of(x);
+    __device__ __forceinline__ uint64_t operator()(float x) const { return weight_of(log2_of(x)); }
+    __device__ __forceinline__ uint64_t weight_of(float2 t) const {
         if (!(t.x > -42.f)) return 0;        // (below half a unit; also where the low part is no number)
         const float w = __builtin_amdgcn_exp2f(t.x);
         const float v = fminf(fmaf(w, t.y * 0.6931471805599453f, w), 1.f) * 0x1p15f;
@@ -144,7 +165,7 @@ __device__ __forceinline__ void first_bin(Shared& s, F f, uint64_t target, uint3
 // pick(sum of all); all sums below 2^64.  n > 0.
 template <typename F, typename P>
 __device__ __forceinline__ uint32_t locate(Shared& s, uint32_t n, F f, P pick, uint64_t* total) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wave = this_wave();
     uint32_t from = 0, size = n;
     uint64_t target = 0;
     bool first = true;
@@ -247,10 +268,14 @@ __device__ __forceinline__ Floor floor_of(float m) {
 __device__ __forceinline__ uint64_t aim(float u, uint64_t total) {
     return min(static_cast<uint64_t>(floor(static_cast<double>(u) * static_cast<double>(total))), total - 1);
 }
-__device__ __forceinline__ void answer(const SampleArgs& a, uint64_t row, uint32_t index, float x, float max, float t, double total) {
+// ln of the token's weight over the total, a number of 2^-39 of the largest;
+// what the total has above the largest is exact.
+__device__ __forceinline__ void answer(const SampleArgs& a, uint64_t row, uint32_t index, float x, const Weigher& g, bool greedy, uint64_t total) {
     a.ids[row] = static_cast<int32_t>(index);
-    if (a.lp != nullptr)
-        a.lp[row] = t == 0.f ? 0.f : static_cast<float>((static_cast<double>(x) - static_cast<double>(max)) / static_cast<double>(t) - log(total * 0x1p-39));
+    if (a.lp == nullptr) return;
+    const float2 t = g.log2_of(x);
+    const float above = static_cast<float>(static_cast<int64_t>(total) - static_cast<int64_t>(kUnit)) * (1.f / kUnit);
+    a.lp[row] = greedy ? 0.f : fmaf(t.x, 0.6931471805599453f, fmaf(t.x, 1.9046542e-9f, t.y * 0.6931471805599453f)) - log1pf(fmaxf(above, 0.f));
 }
 __device__ __forceinline__ void no_answer(const SampleArgs& a, uint64_t row) {
     a.ids[row] = -1;
@@ -259,7 +284,8 @@ __device__ __forceinline__ void no_answer(const SampleArgs& a, uint64_t row) {
 
 // A whole row by one workgroup, whatever its values and wishes: the maximum m
 // and T > 0 are numbers.
-__device__ __noinline__ void draw_from_row(const SampleArgs& a, uint64_t row, const Wish& w, float m, Shared& s) {
+__device__ __noinline__ void draw_from_row(SampleArgs a, uint64_t row, Wish w, float m, Lds at_s) {
+    Shared& s = *(Shared*)at_s;
     const int tid = threadIdx.x;
     const RowSource src{a.logits + row * a.vocab, a.vocab};
     const Weigher g = weigher_of(m, w.t);
@@ -307,19 +333,34 @@ __device__ __noinline__ void draw_from_row(const SampleArgs& a, uint64_t row, co
         const float x = src.value(i);
         return stays(key_of(x), i) && (x == m || f.passes(g.log2_of(x))) ? g(x) : uint64_t{0};
     }, [&](uint64_t all) { return aim(w.u, all); }, &total);
-    if (tid == 0) answer(a, row, at, src.value(at), m, w.t, static_cast<double>(total));
+    if (tid == 0) answer(a, row, at, src.value(at), g, false, total);
     __syncthreads();
 }
 
-// ---- rows of up to 2^20: a list of the likely tokens -------------------------
+// The first of the largest logits of a row, by one workgroup.
+__device__ __noinline__ void take_first(SampleArgs a, uint64_t row, float m, Lds at_s) {
+    Shared& s = *(Shared*)at_s;
+    const float* p = a.logits + row * a.vocab;
+    uint64_t total;
+    const uint32_t at = locate(s, a.vocab, [&](uint32_t i) { return static_cast<uint64_t>(p[i] == m); }, [](uint64_t) { return uint64_t{0}; }, &total);
+    if (threadIdx.x == 0) answer(a, row, at, m, Weigher{m, 1.f, 0.f}, true, 0);
+    __syncthreads();
+}
+
+// ---- rows of up to 2^19: a list of the likely tokens -------------------------
 
 constexpr uint32_t kChunk = 1024;          // tokens of a wave of the scan
 constexpr uint32_t kKept = 256;            // likely ones that it can hand on
 constexpr uint32_t kList = 8192;           // of a row
+constexpr uint32_t kShort = 2048;         // of a row whose workgroups share a compute unit
 constexpr uint32_t kGather = 512;          // of a histogram's bin
-constexpr uint32_t kSlots = kList / kThreads;
-constexpr uint32_t kSamples = 512;
+constexpr uint32_t kSamples = 2048, kMost = 4;   // read of a row; of kMost the largest counts
+constexpr uint32_t kAhead = 256 * 16 / kThreads;
 constexpr uint32_t kOver = 0x80000000u;    // more likely tokens than kKept
+
+struct __attribute__((packed, aligned(4))) Four {
+    float v[4];
+};
 
 // What a wave of the scan says of its tokens: the largest, the sum of their
 // weights relative to that, and how many are in its list.
@@ -327,10 +368,15 @@ struct Record {
     float max, sum;
     uint32_t count, pad;
 };
+// What the first kernel finds out of a row: the bound of its list, and the
+// numbers that its weights and min_p go by.
+struct __attribute__((aligned(16))) Row {
+    float bound, c, c_low, floor_hi, floor_lo, pad[3];
+};
 struct Work {
     Record* records;       // [rows][chunks]
     float2* lists;         // [rows][chunks][kKept]: logit, index
-    float* bounds;         // [rows]
+    Row* rows;             // [rows]
     uint32_t chunks;
 };
 
@@ -338,42 +384,69 @@ __device__ __forceinline__ bool wants_list(const Wish& w) { return w.t == 0.f ||
 __device__ __forceinline__ bool wants_sum(const Wish& w) { return w.t > 0.f && w.k == 0 && (w.p < 1.f || !(w.m > 0.f)); }
 __device__ __forceinline__ bool drawable(const Wish& w) { return w.t >= 0.f && w.t < __builtin_inff(); }
 
-// A bound above which a row has some thousands of its tokens, from 512 of them
-// evenly apart: the r-th largest (its upper 16 bits, rounded down).
-__global__ __launch_bounds__(64) void sample_bound_kernel(SampleArgs a, Work k) {
-    constexpr int kEach = kSamples / 64;
-    const int lane = threadIdx.x;
+// A bound above which a row has some hundreds or thousands of its tokens, from
+// 2048 of them, 512 times four beside each other: the r-th largest of the fours'
+// largest (its upper 16 bits, rounded down).  Of a row of 248320, r = 6 are about 730 tokens:
+// at least 40 of them but for 2 rows in a million.
+// Four waves read, one finds the bound, another the row's numbers.
+__global__ __launch_bounds__(256) void sample_bound_kernel(SampleArgs a, Work k) {
+    constexpr int kEach = kSamples / kMost / 64;
+    __shared__ uint32_t keys[kSamples / kMost];
+    const uint32_t tid = threadIdx.x, lane = tid & 63;
+    const int wave = this_wave();
     for (uint64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
-        const Wish w = wish_of(a, row);
         const float* x = a.logits + row * a.vocab;
-        uint32_t key[kEach];
+        Four v[kSamples / kMost / 256];
 #pragma unroll
-        for (int i = 0; i < kEach; ++i) key[i] = key_of(x[(static_cast<uint64_t>(64 * i + lane) * a.vocab) / kSamples]) >> 16;
-        const uint64_t some = w.t == 0.f ? 1 : (w.k != 0 ? 3ull * w.k + 1000 : 2500);
-        const uint32_t least = w.t == 0.f ? 1 : 5;
-        const uint32_t r = min(max(static_cast<uint32_t>(some * kSamples / a.vocab), least), kSamples);
-        uint32_t bound = 0;
+        for (uint32_t i = 0; i < kSamples / kMost / 256; ++i)
+            v[i] = *reinterpret_cast<const Four*>(x + (static_cast<uint64_t>(i * 256 + tid) * (a.vocab - 3)) / (kSamples / kMost));
+        const Wish w = wish_of(a, row);
 #pragma unroll
-        for (int b = 15; b >= 0; --b) {
-            const uint32_t at = bound | 1u << b;
-            uint32_t n = 0;
+        for (uint32_t i = 0; i < kSamples / kMost / 256; ++i) {
+            uint32_t key = 0;
 #pragma unroll
-            for (int i = 0; i < kEach; ++i) n += static_cast<uint32_t>(__popcll(__ballot(key[i] >= at)));
-            if (n >= r) bound = at;
+            for (uint32_t j = 0; j < kMost; ++j) key = max(key, key_of(v[i].v[j]) >> 16);
+            keys[i * 256 + tid] = key;
         }
-        const uint32_t bits = bound << 16;
-        // (rounded down, -infinity is no number: all that is finite is listed then)
-        float v = __builtin_bit_cast(float, bits & 0x80000000u ? bits & 0x7FFFFFFFu : ~bits);
-        if (!(v > -3.4028235e38f)) v = -3.4028235e38f;
-        if (lane == 0) k.bounds[row] = wants_list(w) && drawable(w) ? v : __builtin_inff();
+        __syncthreads();
+        if (wave == 0) {
+            uint32_t key[kEach];
+#pragma unroll
+            for (int i = 0; i < kEach; ++i) key[i] = keys[64 * i + lane];
+            const uint64_t some = w.t == 0.f ? 1 : (w.k != 0 ? 6ull * w.k + 500 : 2500);
+            const uint32_t least = w.t == 0.f ? 1 : 5;
+            const uint32_t r = min(max(static_cast<uint32_t>(some * kSamples / a.vocab), least), kSamples / kMost);
+            uint32_t bound = 0;
+#pragma unroll
+            for (int b = 15; b >= 0; --b) {
+                const uint32_t at = bound | 1u << b;
+                uint32_t n = 0;
+#pragma unroll
+                for (int i = 0; i < kEach; ++i) n += static_cast<uint32_t>(__popcll(__ballot(key[i] >= at)));
+                if (n >= r) bound = at;
+            }
+            const uint32_t bits = bound << 16;
+            // (rounded down, -infinity is no number: all that is finite is listed then)
+            float low = __builtin_bit_cast(float, bits & 0x80000000u ? bits & 0x7FFFFFFFu : ~bits);
+            if (!(low > -3.4028235e38f)) low = -3.4028235e38f;
+            if (lane == 0) k.rows[row].bound = wants_list(w) && drawable(w) ? low : __builtin_inff();
+        } else if (wave == 1) {
+            const Weigher g = weigher_of(0.f, w.t == 0.f ? 1.f : w.t);
+            const Floor f = floor_of(w.m);
+            if (lane == 0) {
+                Row& to = k.rows[row];
+                to.c = g.c;
+                to.c_low = g.c_low;
+                to.floor_hi = f.hi;
+                to.floor_lo = f.lo;
+            }
+        }
+        __syncthreads();
     }
 }
 
 // Reads every logit once: a wave has 1024, 16 a lane.
 __global__ __launch_bounds__(256) void sample_scan_kernel(SampleArgs a, Work k) {
-    struct __attribute__((packed, aligned(4))) Four {
-        float v[4];
-    };
     const uint32_t lane = threadIdx.x & 63;
     const uint32_t chunk = blockIdx.x * 4 + static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6)));
     if (chunk >= k.chunks) return;
@@ -398,7 +471,8 @@ __global__ __launch_bounds__(256) void sample_scan_kernel(SampleArgs a, Work k) 
                 }
         }
         const Wish w = wish_of(a, row);
-        const float bound = k.bounds[row];
+        const Row of = k.rows[row];
+        const float bound = of.bound;
         float m = -__builtin_inff();
         bool bad = false;
 #pragma unroll
@@ -408,12 +482,11 @@ __global__ __launch_bounds__(256) void sample_scan_kernel(SampleArgs a, Work k) 
                 bad |= !(x[i][j] < __builtin_inff());
                 m = fmaxf(m, x[i][j]);
             }
-#pragma unroll
-        for (int b = 1; b < 64; b <<= 1) m = fmaxf(m, __shfl_xor(m, b));
+        m = wave_max(m);
         if (__any(bad)) m = __builtin_inff();
         float sum = 0.f;
         if (wants_sum(w) && m > -__builtin_inff() && m < __builtin_inff()) {
-            const Weigher g = weigher_of(m, w.t);
+            const Weigher g{m, of.c, of.c_low};
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -423,8 +496,7 @@ __global__ __launch_bounds__(256) void sample_scan_kernel(SampleArgs a, Work k) 
                     const float t = fmaxf(fmaf(d, g.c, d * g.c_low), d * g.c - 1.f);
                     sum += d == 0.f ? 1.f : __builtin_amdgcn_exp2f(t);
                 }
-#pragma unroll
-            for (int b = 1; b < 64; b <<= 1) sum += __shfl_xor(sum, b);
+            sum = wave_reduce(sum);
         }
         // the list, in the order of the indexes
         const uint64_t slot = row * k.chunks + chunk;
@@ -456,12 +528,15 @@ __global__ __launch_bounds__(256) void sample_scan_kernel(SampleArgs a, Work k) 
     }
 }
 
-// Shared memory of the kernel that picks.
+// Shared memory of the kernel that picks among N tokens.
+constexpr uint64_t kBelow = 1ull << 63;   // of a weight: min_p does not let the token pass
+template <uint32_t N, bool DIRECT>
 struct Picks {
-    union {
+    union {                              // (first: the functions for whole rows take it by the address of all)
         struct {
-            float x[kList];
-            uint32_t index[kList];
+            uint64_t q[N];
+            float x[N];
+            uint32_t index[DIRECT ? 1 : N];
         };
         Shared row;
     };
@@ -469,98 +544,139 @@ struct Picks {
     uint32_t count[kThreads];
     uint64_t g_weight[kGather];
     uint32_t g_key[kGather], g_at[kGather];
-    uint64_t sums[kWaves], sums2[kWaves];
+    uint64_t sums[4][2][kWaves];     // one for each use
     float maxes[kWaves], mins[kWaves];
     uint32_t flags[kWaves];
     uint32_t bin, gathered, key, at;
     uint64_t before, inside;
 };
 
-// Exclusive sums of a and b over the workgroup's threads, and their totals.
-__device__ __forceinline__ void scan2(Picks& s, uint64_t a, uint64_t b, uint64_t* a_before, uint64_t* b_before, uint64_t* a_all, uint64_t* b_all) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+// (The kernel that picks runs its few thousand instructions once a row, so
+// their fetching is what counts: loops are not unrolled, and what is used
+// twice is a function.)
+
+// Sums of a and b over the workgroup's threads before this one, and over all.
+struct Sums {
+    uint64_t a_before, b_before, a_all, b_all;
+};
+__device__ __noinline__ Sums scan2(Lds at_sums, uint64_t a, uint64_t b) {
+    uint64_t(*sums)[kWaves] = (uint64_t(*)[kWaves])at_sums;
+    const int lane = threadIdx.x & 63, wave = this_wave();
     const uint64_t ua = wave_scan(a), ub = wave_scan(b);
     if (lane == 63) {
-        s.sums[wave] = ua;
-        s.sums2[wave] = ub;
+        sums[0][wave] = ua;
+        sums[1][wave] = ub;
     }
     __syncthreads();
-    uint64_t pa = ua - a, pb = ub - b, ta = 0, tb = 0;
-#pragma unroll
-    for (int i = 0; i < kWaves; ++i) {
-        if (i == wave) {
-            pa += ta;
-            pb += tb;
-        }
-        ta += s.sums[i];
-        tb += s.sums2[i];
-    }
-    *a_before = pa;
-    *b_before = pb;
-    *a_all = ta;
-    *b_all = tb;
-    __syncthreads();
+    const uint64_t sa = row_scan(sums[0][lane % kWaves]), sb = row_scan(sums[1][lane % kWaves]);
+    return Sums{ua - a + (wave > 0 ? read_lane_u64(sa, wave - 1) : 0), ub - b + (wave > 0 ? read_lane_u64(sb, wave - 1) : 0),
+                read_lane_u64(sa, kWaves - 1), read_lane_u64(sb, kWaves - 1)};
 }
 
-// The tokens of bin `bin` into the gather list; how many they are (past kGather they are not all there).
-template <typename X, typename Q, typename B>
-__device__ __forceinline__ uint32_t gather(Picks& s, uint32_t bin, uint32_t first, const X& x, const Q& q, const B& bins) {
-    if (threadIdx.x == 0) s.gathered = 0;
+// A row's tokens in shared memory, and the bins of their histogram: bin 0 has
+// the largest logits; tokens below `low` are in none.
+struct Bins {
+    float max, low, per;
+    __device__ __forceinline__ uint32_t operator()(float x) const {
+        return x >= low ? static_cast<uint32_t>(fminf((max - x) * per, kThreads - 1.f)) : 0xFFFFFFFFu;
+    }
+};
+
+// Of the tokens of a bin (kGather at most, or the answer is false) the first,
+// in the order of the logits, at which the running sum of what they weigh, or
+// of their count, exceeds `target`: its key and place to s.key and s.at, the
+// weights up to it to s.inside.
+template <uint32_t N, bool DIRECT>
+__device__ __noinline__ bool cut_in_bin(Lds at_s, uint32_t bin, uint32_t n, uint64_t target, bool by_count, Bins bins) {
+    Picks<N, DIRECT>& s = *(Picks<N, DIRECT>*)at_s;
+    const uint32_t tid = threadIdx.x;
+    if (tid == 0) s.gathered = 0;
     __syncthreads();
-#pragma unroll
-    for (uint32_t i = 0; i < kSlots; ++i) {
-        if (bins[i] == bin) {
+#pragma unroll 1
+    for (uint32_t i = tid; i < n; i += kThreads) {
+        const float x = s.x[i];
+        const uint64_t q = s.q[i];
+        if (bins(x) == bin) {
             const uint32_t at = atomicAdd(&s.gathered, 1u);
             if (at < kGather) {
-                s.g_key[at] = key_of(x[i]);
-                s.g_at[at] = first + 64 * i;
-                s.g_weight[at] = q[i];
+                s.g_key[at] = key_of(x);
+                s.g_at[at] = i;
+                s.g_weight[at] = q & ~kBelow;
             }
         }
     }
     __syncthreads();
-    return s.gathered;
+    const uint32_t got = s.gathered;
+    if (got > kGather) return false;
+    if (tid < got) {
+        const uint32_t ka = s.g_key[tid], pa = s.g_at[tid];
+        const uint64_t q = s.g_weight[tid];
+        uint64_t weight = 0;
+        uint32_t count = 0;
+#pragma unroll 4
+        for (uint32_t j = 0; j < got; ++j) {
+            const uint32_t kb = s.g_key[j], pb = s.g_at[j];
+            const uint64_t qb = s.g_weight[j];
+            const bool ahead = kb > ka || (kb == ka && pb < pa);
+            weight += ahead ? qb : 0;
+            count += ahead ? 1u : 0u;
+        }
+        const uint64_t sum = by_count ? count : weight;
+        if (sum <= target && target - sum < (by_count ? 1u : q)) {
+            s.key = ka;
+            s.at = pa;
+            s.inside = weight + q;
+        }
+    }
+    __syncthreads();
+    return true;
 }
 
-// DIRECT: rows of at most kList, read here; else the row's list is.
-template <bool DIRECT>
+// DIRECT: rows of at most N, read here; else the row's list is.
+template <uint32_t N, bool DIRECT>
 __global__ __launch_bounds__(kThreads) void sample_pick_kernel(SampleArgs a, Work k) {
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-    Picks& s = *reinterpret_cast<Picks*>(lds);
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    Picks<N, DIRECT>& s = *reinterpret_cast<Picks<N, DIRECT>*>(lds);
+    const int tid = threadIdx.x, lane = tid & 63, wave = this_wave();
+#pragma unroll 1
     for (uint64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
         const Wish w = wish_of(a, row);
         __syncthreads();
         s.weight[tid] = 0;
         s.count[tid] = 0;
         // the row's largest logit, its number of listed tokens, the sum of its weights
-        float x[kSlots], m = -__builtin_inff(), low = __builtin_inff();
-        uint32_t n, first, flag = 0;
+        float m = -__builtin_inff(), low = __builtin_inff();
+        uint32_t n = a.vocab, flag = 0;
         Record r{-__builtin_inff(), 0.f, 0, 0};
-        const float bound = DIRECT ? -__builtin_inff() : k.bounds[row];
+        float2 ahead[kAhead];
+        Row of_row{-__builtin_inff(), 0.f, 0.f, 0.f, 0.f, {}};
+        if constexpr (!DIRECT) of_row = k.rows[row];
+        const float bound = of_row.bound;
         if constexpr (DIRECT) {
-            n = a.vocab;
-            first = wave * (((n + kThreads - 1) / kThreads) * 64) + lane;
-            const uint32_t end = min((wave + 1) * (((n + kThreads - 1) / kThreads) * 64), n);
-#pragma unroll
-            for (uint32_t i = 0; i < kSlots; ++i) {
-                x[i] = first + 64 * i < end ? a.logits[row * a.vocab + first + 64 * i] : -__builtin_inff();
-                if (!(x[i] < __builtin_inff())) flag = kOver;
-                m = fmaxf(m, x[i]);
-                if (x[i] > -__builtin_inff()) low = fminf(low, x[i]);
+            bool bad = false;
+#pragma unroll 2
+            for (uint32_t i = tid; i < n; i += kThreads) {
+                const float x = a.logits[row * a.vocab + i];
+                s.x[i] = x;
+                bad |= !(x < __builtin_inff());
+                m = fmaxf(m, x);
+                if (x > -__builtin_inff()) low = fminf(low, x);
             }
-            if (flag != 0) m = __builtin_inff();
-            flag = 0;
+            if (bad) m = __builtin_inff();
         } else {
             if (static_cast<uint32_t>(tid) < k.chunks) r = k.records[row * k.chunks + tid];
+            // the lists' first 16 tokens, of the first 256 chunks, before their counts are known
+            // (behind a list's end is memory of the workspace, read and not used)
+#pragma unroll
+            for (uint32_t i = 0; i < kAhead; ++i) {
+                const uint32_t c = (tid >> 4) + kThreads / 16 * i;
+                ahead[i] = c < k.chunks ? k.lists[(row * k.chunks + c) * kKept + (tid & 15)] : make_float2(0.f, 0.f);
+            }
             m = r.max;
             flag = r.count & kOver;
         }
-#pragma unroll
-        for (int b = 1; b < 64; b <<= 1) {
-            m = fmaxf(m, __shfl_xor(m, b));
-            if constexpr (DIRECT) low = fminf(low, __shfl_xor(low, b));
-        }
+        m = wave_max(m);
+        if constexpr (DIRECT) low = -wave_max(-low);
         flag = __any(flag != 0) ? 1u : 0u;
         if (lane == 0) {
             s.maxes[wave] = m;
@@ -568,218 +684,196 @@ __global__ __launch_bounds__(kThreads) void sample_pick_kernel(SampleArgs a, Wor
             s.flags[wave] = flag;
         }
         __syncthreads();
-#pragma unroll
-        for (int i = 0; i < kWaves; ++i) {
-            m = fmaxf(m, s.maxes[i]);
-            low = fminf(low, s.mins[i]);
-            flag |= s.flags[i];
-        }
+        m = row_max(s.maxes[lane % kWaves]);
+        if constexpr (DIRECT) low = -row_max(-s.mins[lane % kWaves]);
+        else flag = __any(s.flags[lane % kWaves] != 0) ? 1u : 0u;
+        m = read_lane(m, 0);
         if (!(m > -__builtin_inff() && m < __builtin_inff()) || !drawable(w)) {
             if (tid == 0) no_answer(a, row);
             continue;
         }
         const bool greedy = w.t == 0.f;
-        const Weigher g = weigher_of(m, greedy ? 1.f : w.t);
+        const Weigher g = DIRECT ? weigher_of(m, greedy ? 1.f : w.t) : Weigher{m, of_row.c, of_row.c_low};
         uint64_t all = 0;                        // the weights of the whole row
         if constexpr (!DIRECT) {
             // records' weights as whole numbers, and the places of their lists
-            uint64_t mine = 0, before, n_before, n_all;
-            if (r.max > -__builtin_inff()) {
+            uint64_t mine = 0;
+            if (wants_sum(w) && r.max > -__builtin_inff()) {
                 const float2 t = g.log2_of(r.max);
-                if (t.x > -60.f) mine = static_cast<uint64_t>(static_cast<double>(r.sum) * exp2(static_cast<double>(t.x) + static_cast<double>(t.y)) * 0x1p39);
+                if (t.x > -60.f) mine = static_cast<uint64_t>(static_cast<double>(r.sum * __builtin_amdgcn_exp2f(t.x) * (1.f + t.y * 0.6931471805599453f)) * 0x1p39);
             }
-            scan2(s, mine, r.count & ~kOver, &before, &n_before, &all, &n_all);
+            const Sums of = scan2((Lds)s.sums[0], mine, r.count & ~kOver);
+            all = of.a_all;
             if (!wants_list(w)) {
-                // drawn from all: the record, then its tokens one a thread
+                // drawn from all: the record, then its tokens two a thread
                 const uint64_t target = aim(w.u, max(all, uint64_t{1}));
-                if (mine != 0 && before <= target && target - before < mine) {
+                if (mine != 0 && of.a_before <= target && target - of.a_before < mine) {
                     s.bin = tid;
-                    s.before = target - before;
+                    s.before = target - of.a_before;
                 }
                 __syncthreads();
-                const uint32_t at = s.bin * kChunk + tid;
-                const float v = at < a.vocab ? a.logits[row * a.vocab + at] : -__builtin_inff();
-                const uint64_t q = g(v);
-                uint64_t q_before, unused, q_all, unused_all;
+                const uint32_t at = s.bin * kChunk + 2 * tid;
                 const uint64_t want = s.before;
-                scan2(s, q, 0, &q_before, &unused, &q_all, &unused_all);
-                const uint64_t place = q_all == 0 ? 0 : min(want, q_all - 1);
-                if (q_all == 0 ? tid == 0 : (q_before <= place && place - q_before < q)) answer(a, row, at, v, m, w.t, static_cast<double>(all));
+                const float u = at < a.vocab ? a.logits[row * a.vocab + at] : -__builtin_inff();
+                const float v = at + 1 < a.vocab ? a.logits[row * a.vocab + at + 1] : -__builtin_inff();
+                const uint64_t q = g(u), q2 = g(v);
+                const Sums in = scan2((Lds)s.sums[1], q + q2, 0);
+                const uint64_t place = in.a_all == 0 ? 0 : min(want, in.a_all - 1);
+                if (in.a_all == 0 ? tid == 0 : (in.a_before <= place && place - in.a_before < q + q2)) {
+                    const bool second = in.a_all != 0 && place - in.a_before >= q;
+                    answer(a, row, second ? at + 1 : at, second ? v : u, g, false, all);
+                }
                 continue;
             }
-            n = static_cast<uint32_t>(min(n_all, static_cast<uint64_t>(kList)));
-            flag |= n_all > kList ? 1u : 0u;
+            n = static_cast<uint32_t>(min(of.b_all, static_cast<uint64_t>(N)));
+            flag |= of.b_all > N ? 1u : 0u;
             if (flag == 0) {
                 // lists into shared memory, 16 lanes a list
-                if (static_cast<uint32_t>(tid) < k.chunks) {
-                    s.weight[tid] = n_before << 32 | r.count;   // (the histogram's memory, cleared again below)
-                }
+                s.weight[tid] = of.b_before << 32 | r.count;   // (the histogram's memory, cleared again below)
                 __syncthreads();
                 const uint32_t part = tid & 15;
-                for (uint32_t c = tid >> 4; c < k.chunks; c += kThreads / 16) {
-                    const uint32_t to = static_cast<uint32_t>(s.weight[c] >> 32), count = static_cast<uint32_t>(s.weight[c]);
-                    const float2* list = k.lists + (row * k.chunks + c) * kKept;
-                    for (uint32_t j = part; j < count; j += 16) {
-                        const float2 v = list[j];
-                        s.x[to + j] = v.x;
-                        s.index[to + j] = __builtin_bit_cast(uint32_t, v.y);
+                const auto put = [&](uint64_t of, uint32_t from, float2 v) {
+                    if (from < static_cast<uint32_t>(of)) {
+                        s.x[(of >> 32) + from] = v.x;
+                        s.index[(of >> 32) + from] = __builtin_bit_cast(uint32_t, v.y);
+                    }
+                };
+                uint64_t at[kAhead];
+                uint32_t most = 0;
+#pragma unroll
+                for (uint32_t i = 0; i < kAhead; ++i) {
+                    const uint32_t c = (tid >> 4) + kThreads / 16 * i;
+                    at[i] = c < k.chunks ? s.weight[c] : 0;
+                }
+#pragma unroll
+                for (uint32_t i = 0; i < kAhead; ++i) {
+                    put(at[i], part, ahead[i]);
+                    most = max(most, static_cast<uint32_t>(at[i]));
+                }
+                // what is left: longer lists, and chunks behind the first 256
+                if (__any(most > 16) || k.chunks > 256) {
+#pragma unroll 1
+                    for (uint32_t c = tid >> 4; c < k.chunks; c += kThreads / 16) {
+                        const uint64_t of_c = s.weight[c];
+#pragma unroll 1
+                        for (uint32_t j = c < 256 ? part + 16 : part; j < static_cast<uint32_t>(of_c); j += 16)
+                            put(of_c, j, k.lists[(row * k.chunks + c) * kKept + j]);
                     }
                 }
                 __syncthreads();
                 s.weight[tid] = 0;
             }
-            const uint32_t each = ((n + kThreads - 1) / kThreads) * 64;
-            first = wave * each + lane;
-            const uint32_t end = min((wave + 1) * each, n);
-#pragma unroll
-            for (uint32_t i = 0; i < kSlots; ++i) x[i] = flag == 0 && first + 64 * i < end ? s.x[first + 64 * i] : -__builtin_inff();
         }
-        const auto index_of = [&](uint32_t at) { return DIRECT ? at : s.index[at]; };
         // tokens below `low` weigh nothing, or are in no list
         const float nothing = m - 29.2f * w.t;
         const bool complete = DIRECT || bound <= nothing;
         low = greedy ? m : fmaxf(DIRECT ? low : bound, nothing);
-        const float per = m > low ? (kThreads - 0.01f) / (m - low) : 0.f;
-        uint64_t q[kSlots];
-        uint32_t bins[kSlots];
+        const Bins bins{m, low, m > low ? (kThreads - 0.01f) / (m - low) : 0.f};
+        const Floor f = DIRECT ? floor_of(greedy ? 0.f : w.m) : Floor{w.m > 0.f && !greedy, of_row.floor_hi, of_row.floor_lo};
+        bool cut = false, lost = flag != 0;
+        if (lost) n = 0;
         __syncthreads();
-#pragma unroll
-        for (uint32_t i = 0; i < kSlots; ++i) {
-            const bool in = x[i] >= low;
-            q[i] = in ? g(x[i]) : 0;
-            bins[i] = in ? static_cast<uint32_t>(fminf((m - x[i]) * per, kThreads - 1.f)) : 0xFFFFFFFFu;
-            if (in) {
-                atomicAdd(&s.count[bins[i]], 1u);
-                if (!greedy && q[i] != 0) atomicAdd(reinterpret_cast<unsigned long long*>(&s.weight[bins[i]]), static_cast<unsigned long long>(q[i]));
+#pragma unroll 1
+        for (uint32_t i = tid; i < n; i += kThreads) {
+            const float x = s.x[i];
+            const uint32_t bin = bins(x);
+            uint64_t q = 0;
+            if (bin != 0xFFFFFFFFu) {
+                const float2 t = g.log2_of(x);
+                q = g.weight_of(t);
+                atomicAdd(&s.count[bin], 1u);
+                atomicAdd(reinterpret_cast<unsigned long long*>(&s.weight[bin]), static_cast<unsigned long long>(q));
+                if (x != m && !f.passes(t)) q |= kBelow;
             }
+            s.q[i] = q;
         }
         __syncthreads();
-        uint64_t c_before, w_before, c_all, w_all;
-        scan2(s, s.count[tid], s.weight[tid], &c_before, &w_before, &c_all, &w_all);
-        // (w.k etc. are the row's, so the workgroup goes one way)
-        bool cut = false, lost = flag != 0;
+        const uint32_t c_mine = s.count[tid];
+        const uint64_t w_mine = s.weight[tid];
+        const Sums of = scan2((Lds)s.sums[2], c_mine, w_mine);
+        // (the wishes are the row's, so the workgroup goes one way)
         uint32_t key = 0, last = 0xFFFFFFFFu;
-        uint64_t among = complete ? w_all : all;
+        uint64_t among = complete ? of.b_all : all;
         const uint32_t want_k = greedy ? 1u : w.k;
         if (!lost && want_k != 0) {
-            if (c_all >= want_k) {
-                if (c_before < want_k && c_before + s.count[tid] >= want_k) {
+            if (of.a_all >= want_k) {
+                if (of.a_before < want_k && of.a_before + c_mine >= want_k) {
                     s.bin = tid;
-                    s.before = w_before;
-                    s.at = want_k - static_cast<uint32_t>(c_before);
+                    s.before = of.b_before;
+                    s.at = want_k - static_cast<uint32_t>(of.a_before);
                 }
-                if (tid == 0) s.inside = 0;
                 __syncthreads();
-                const uint32_t need = s.at, got = gather(s, s.bin, first, x, q, bins);
-                if (got > kGather) {
-                    lost = true;
-                } else {
-                    if (static_cast<uint32_t>(tid) < got) {
-                        const uint32_t ka = s.g_key[tid], pa = s.g_at[tid];
-                        uint32_t rank = 0;
-                        for (uint32_t j = 0; j < got; ++j) rank += s.g_key[j] > ka || (s.g_key[j] == ka && s.g_at[j] < pa) ? 1u : 0u;
-                        if (rank < need) atomicAdd(reinterpret_cast<unsigned long long*>(&s.inside), static_cast<unsigned long long>(s.g_weight[tid]));
-                        if (rank == need - 1) {
-                            s.key = ka;
-                            s.at = pa;
-                        }
-                    }
-                    __syncthreads();
-                    key = s.key;
-                    last = s.at;
-                    among = s.before + s.inside;
-                    cut = true;
-                }
-            } else if (complete) {
-                cut = true;                      // all that weigh anything stay
+                const uint32_t need = s.at;
+                lost = !cut_in_bin<N, DIRECT>((Lds)lds, s.bin, n, need - 1, true, bins);
+                key = s.key;
+                last = s.at;
+                among = s.before + s.inside;
+                cut = true;
             } else {
-                lost = true;
+                cut = complete;                  // all that weigh anything stay
+                lost = !complete;
             }
         }
         __syncthreads();
-        if (!lost && !greedy && w.p < 1.f && (w.k != 0 || complete || all != 0)) {
+        if (!lost && !greedy && w.p < 1.f) {
             const double want = ceil(static_cast<double>(w.p) * static_cast<double>(among));
             const uint64_t target = want < 1.0 ? 0 : min(static_cast<uint64_t>(want), among) - 1;
-            if (target < w_all) {
-                const uint64_t mine = s.weight[tid];
-                if (mine != 0 && w_before <= target && target - w_before < mine) {
+            if (target < of.b_all) {
+                if (w_mine != 0 && of.b_before <= target && target - of.b_before < w_mine) {
                     s.bin = tid;
-                    s.before = w_before;
+                    s.before = target - of.b_before;
                 }
                 __syncthreads();
-                const uint32_t got = gather(s, s.bin, first, x, q, bins);
-                if (got > kGather) {
-                    lost = true;
-                } else {
-                    if (static_cast<uint32_t>(tid) < got) {
-                        const uint32_t ka = s.g_key[tid], pa = s.g_at[tid];
-                        uint64_t sum = s.before;
-                        for (uint32_t j = 0; j < got; ++j) sum += s.g_key[j] > ka || (s.g_key[j] == ka && s.g_at[j] < pa) ? s.g_weight[j] : uint64_t{0};
-                        if (sum <= target && target - sum < s.g_weight[tid]) {
-                            s.key = ka;
-                            s.at = pa;
-                        }
-                    }
-                    __syncthreads();
-                    key = s.key;
-                    last = s.at;
-                    cut = true;
-                }
+                const uint64_t in = s.before;
+                lost = !cut_in_bin<N, DIRECT>((Lds)lds, s.bin, n, in, false, bins);
+                key = s.key;
+                last = s.at;
+                cut = true;
             } else if (!cut) {
                 lost = true;
             }
         }
-        const Floor f = floor_of(greedy ? 0.f : w.m);
         // (without another cut, a list that ends above what min_p lets pass is none)
         if (!cut && !complete && !(f.on && !f.passes(g.log2_of(bound)))) lost = true;
         if (lost) {
             __syncthreads();
-            if (greedy) {
-                uint64_t total;
-                const float* p = a.logits + row * a.vocab;
-                const uint32_t at = locate(s.row, a.vocab, [&](uint32_t i) { return static_cast<uint64_t>(p[i] == m); }, [](uint64_t) { return uint64_t{0}; }, &total);
-                if (tid == 0) answer(a, row, at, m, m, 0.f, 1.0);
-                __syncthreads();
-            } else {
-                draw_from_row(a, row, w, m, s.row);
-            }
+            if (greedy) take_first(a, row, m, (Lds)lds);
+            else draw_from_row(a, row, w, m, (Lds)lds);
             continue;
         }
         // the draw: a wave's tokens are consecutive, 64 a step
+        const uint32_t each = ((n + kThreads - 1) / kThreads) * 64, begin = wave * each, end = min(begin + each, n);
+        const auto weight = [&](uint32_t i) {
+            if (i >= end) return uint64_t{0};
+            const uint32_t ka = key_of(s.x[i]);
+            const uint64_t q = s.q[i];
+            return (ka > key || (ka == key && i <= last)) && (q & kBelow) == 0 ? q : uint64_t{0};
+        };
         uint64_t sum = 0;
-#pragma unroll
-        for (uint32_t i = 0; i < kSlots; ++i) {
-            const uint32_t ka = key_of(x[i]);
-            const bool stays = bins[i] != 0xFFFFFFFFu && (ka > key || (ka == key && first + 64 * i <= last)) && (x[i] == m || f.passes(g.log2_of(x[i])));
-            q[i] = stays ? (greedy ? uint64_t{1} : q[i]) : uint64_t{0};
-            sum += q[i];
-        }
+#pragma unroll 1
+        for (uint32_t i = begin + lane; i < begin + each; i += 64) sum += weight(i);
         sum = wave_sum(sum);
+        if (lane == 0) s.sums[3][0][wave] = sum;
         __syncthreads();
-        if (lane == 0) s.sums[wave] = sum;
-        __syncthreads();
-        uint64_t total = 0, before = 0;
-#pragma unroll
-        for (int i = 0; i < kWaves; ++i) {
-            before += i < wave ? s.sums[i] : 0;
-            total += s.sums[i];
-        }
+        const uint64_t upto_wave = row_scan(s.sums[3][0][lane % kWaves]), total = read_lane_u64(upto_wave, kWaves - 1);
+        uint64_t before = read_lane_u64(upto_wave, wave) - sum;
         const uint64_t target = aim(greedy ? 0.f : w.u, total);
         if (before <= target && target - before < sum) {      // (one wave)
-#pragma unroll
-            for (uint32_t i = 0; i < kSlots; ++i) {
-                const uint64_t upto = wave_scan(q[i]) + before;
-                if (upto > target && upto - q[i] <= target) answer(a, row, index_of(first + 64 * i), x[i], m, w.t, static_cast<double>(total));
-                before = shfl_u64(upto, 63);
+#pragma unroll 1
+            for (uint32_t i = begin + lane; i < begin + each; i += 64) {
+                const uint64_t q = weight(i);
+                const uint64_t upto = wave_scan(q) + before;
+                if (upto > target && upto - q <= target) answer(a, row, DIRECT ? i : s.index[i], s.x[i], g, greedy, total);
+                before = read_lane_u64(upto, 63);
             }
         }
     }
 }
 
-// Rows past 2^20: a workgroup a row.
+// Rows past 2^19: a workgroup a row.
 __global__ __launch_bounds__(kThreads) void sample_row_kernel(SampleArgs a) {
     __shared__ Shared s;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int tid = threadIdx.x, lane = tid & 63, wave = this_wave();
     for (uint64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
         const float* p = a.logits + row * a.vocab;
         const Wish w = wish_of(a, row);
@@ -791,8 +885,7 @@ __global__ __launch_bounds__(kThreads) void sample_row_kernel(SampleArgs a) {
             bad |= !(x < __builtin_inff());
             m = fmaxf(m, x);
         }
-#pragma unroll
-        for (int b = 1; b < 64; b <<= 1) m = fmaxf(m, __shfl_xor(m, b));
+        m = wave_max(m);
         if (__any(bad)) m = __builtin_inff();
         if (lane == 0) s.maxes[wave] = m;
         __syncthreads();
@@ -801,12 +894,9 @@ __global__ __launch_bounds__(kThreads) void sample_row_kernel(SampleArgs a) {
         if (!(m > -__builtin_inff() && m < __builtin_inff()) || !drawable(w)) {
             if (tid == 0) no_answer(a, row);
         } else if (w.t == 0.f) {
-            uint64_t total;
-            const uint32_t at = locate(s, a.vocab, [&](uint32_t i) { return static_cast<uint64_t>(p[i] == m); }, [](uint64_t) { return uint64_t{0}; }, &total);
-            if (tid == 0) answer(a, row, at, m, m, 0.f, 1.0);
-            __syncthreads();
+            take_first(a, row, m, (Lds)&s);
         } else {
-            draw_from_row(a, row, w, m, s);
+            draw_from_row(a, row, w, m, (Lds)&s);
         }
     }
 }
@@ -814,11 +904,14 @@ __global__ __launch_bounds__(kThreads) void sample_row_kernel(SampleArgs a) {
 uint32_t chunks_of(uint32_t vocab) { return (vocab + kChunk - 1) / kChunk; }
 bool listed(uint32_t vocab) { return vocab > kList && vocab <= kThreads * kChunk; }
 
-template <bool DIRECT>
+template <uint32_t N, bool DIRECT>
 hipError_t pick(const SampleArgs& a, const Work& k, uint32_t grid, hipStream_t s) {
-    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(sample_pick_kernel<DIRECT>), hipFuncAttributeMaxDynamicSharedMemorySize, sizeof(Picks));
-    if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((sample_pick_kernel<DIRECT>), dim3(grid), dim3(kThreads), sizeof(Picks), s, a, k);
+    constexpr int bytes = sizeof(Picks<N, DIRECT>);
+    if constexpr (bytes > 65536) {
+        const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(sample_pick_kernel<N, DIRECT>), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e != hipSuccess) return e;
+    }
+    hipLaunchKernelGGL((sample_pick_kernel<N, DIRECT>), dim3(grid), dim3(kThreads), bytes, s, a, k);
     return hipGetLastError();
 }
 
@@ -827,13 +920,14 @@ hipError_t pick(const SampleArgs& a, const Work& k, uint32_t grid, hipStream_t s
 uint64_t sample_workspace_bytes(uint32_t rows, uint32_t vocab) {
     if (!listed(vocab)) return 16;
     const uint64_t slots = uint64_t{rows} * chunks_of(vocab);
-    return slots * (sizeof(Record) + kKept * sizeof(float2)) + (uint64_t{rows} * 4 + 15) / 16 * 16;
+    return slots * (sizeof(Record) + kKept * sizeof(float2)) + rows * sizeof(Row);
 }
 
 hipError_t launch_sample(const SampleArgs& a, void* workspace, hipStream_t stream) {
     const uint32_t grid = a.rows < (1u << 20) ? a.rows : (1u << 20);
     Work k{};
-    if (a.vocab <= kList) return pick<true>(a, k, grid, stream);
+    if (a.vocab <= kShort) return pick<kShort, true>(a, k, grid, stream);
+    if (a.vocab <= kList) return pick<kList, true>(a, k, grid, stream);
     if (!listed(a.vocab)) {
         hipLaunchKernelGGL(sample_row_kernel, dim3(grid), dim3(kThreads), 0, stream, a);
         return hipGetLastError();
@@ -842,13 +936,13 @@ hipError_t launch_sample(const SampleArgs& a, void* workspace, hipStream_t strea
     const uint64_t slots = uint64_t{a.rows} * k.chunks;
     k.records = static_cast<Record*>(workspace);
     k.lists = reinterpret_cast<float2*>(k.records + slots);
-    k.bounds = reinterpret_cast<float*>(k.lists + slots * kKept);
-    hipLaunchKernelGGL(sample_bound_kernel, dim3(grid), dim3(64), 0, stream, a, k);
+    k.rows = reinterpret_cast<Row*>(k.lists + slots * kKept);
+    hipLaunchKernelGGL(sample_bound_kernel, dim3(grid), dim3(256), 0, stream, a, k);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(sample_scan_kernel, dim3((k.chunks + 3) / 4, a.rows < 65535 ? a.rows : 65535), dim3(256), 0, stream, a, k);
     e = hipGetLastError();
-    return e != hipSuccess ? e : pick<false>(a, k, grid, stream);
+    return e != hipSuccess ? e : pick<kList, false>(a, k, grid, stream);
 }
 
 }  // namespace qmv
