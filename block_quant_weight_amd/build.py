@@ -31,7 +31,8 @@ HOST_SOURCES = ["qmv_host.cpp"]  # no HIP: plain g++
 # Per-file flags.  The int8 product reads every matrix-core result with
 # vector instructions; in the accumulation-register form each result would
 # first be copied out (one extra instruction per output per block).
-FILE_FLAGS = {"gemm_i8.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
+FILE_FLAGS = {"gemm_i8.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+              "kv4_attend.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
 
 
 def _run(cmd):

@@ -496,6 +496,425 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attend4_few_kernel(Atte
     }
 }
 
+// ---- many queries -----------------------------------------------------------
+
+// Many bfloat16 queries to a key/value head: a workgroup of eight waves has 32
+// columns a wave, and walks the pages together.  Values are made float16 once
+// for all, in shared memory; keys stay codes there, which each wave turns into
+// bfloat16 on the way to its products: an operand read from shared memory feeds
+// one product of 32 columns, and were both of 2 bytes a value, these reads
+// would take as long as the products.
+//
+// v_mfma_f32_32x32x16 takes from lane l eight k-indexes of row (or column) l %
+// 32, those of half l / 32, and gives lane l, register i the output of row 8 (i
+// / 4) + 4 (l / 32) + i % 4 and column l % 32.  Keys: lane (row, h) reads the 32
+// codes of block 2 B + h, the operands of four k-steps.  Tokens are the rows of
+// the scores, and the output's k-index 16 s + 8 h + e is token 16 s + 8 (e / 4) +
+// 4 h + e % 4 of a tile of 32, register 8 s + e of the lane that scored it:
+// probabilities stay in their lane.  Row r of the values in shared memory is
+// channel (D / 16) (r % 16) + r / 16.
+//
+// Scores are bfloat16 products, exact in both operands.  The output's are
+// float16: probabilities keep 11 bits there (their sum is taken of the rounded
+// ones), not 8.  They are 4 at a column's reference m, e^(s - m), which moves
+// once a lane's sum of a page would pass 2^15: no maximum is sought in the
+// middle of a sequence.  Down to 2^-16 of the reference they keep all their
+// bits, and below 2^-27 they count as 0.  A page's values are times 2^-unit,
+// with a unit 4 above its largest exponent that stays while pages' largest are
+// within 10 below and 13 above it, so blocks down to 2^-13 of a page's largest
+// are exact whatever came before.
+//
+// Head dims of 256 hold too many registers for a wave of 32 columns: waves w
+// and w + 4 have the same 32.  Each scores half of a page's tokens, they
+// exchange maxima and probabilities through shared memory, and each adds up
+// half of the output channels.
+template <int D>
+struct Many {
+    static constexpr bool kPair = D == 256;
+    static constexpr int kThreads = 512, kCols = kPair ? 128 : 256;
+    static constexpr int kKeys = kCodeBytes<D>, kValueRow = 2 * kPage, kValues = D * kValueRow;   // bytes of a page
+    // (pairs: probabilities [4 column groups][4 k-steps][64 lanes], maxima [4][2 halves][32])
+    static constexpr int kExchange = kPair ? 4 * 4 * 64 * 16 + 4 * 2 * 32 * 4 : 0;
+    static constexpr int kBytes = 2 * (kKeys + kValues) + kExchange + 64;   // 64: the pages' largest exponents, of each wave
+};
+constexpr float kSumLimit = 0x1p15f;       // of a page's probabilities in a lane
+constexpr float kBias = 2.f;               // log2 of a probability at the reference
+constexpr float kMoveManyAt = 4.f;
+constexpr int32_t kNoUnit = -1000;
+
+template <int D>
+__global__ __launch_bounds__(512, 2) void attend4_many_kernel(Attend4Args a) {
+    typedef Many<D> M;
+    typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+    typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+    constexpr bool PAIR = M::kPair;
+    constexpr int QS = D / 16;                    // k-steps of a score
+    constexpr int KB = D / kBlock;                // blocks of a token
+    constexpr int ST = PAIR ? 1 : 2;              // tiles of 32 tokens that a wave scores
+    constexpr int ET = D / (PAIR ? 64 : 32);      // tiles of output channels that a wave adds up
+    // pieces of 16 bytes of codes: of keys (32 channels of a token), of values (four tokens, 128 / D sixteenths)
+    constexpr int PIECES = kPage * D / 32, PER = PIECES > 512 / 2 ? 1 : 0;   // PER: a thread has both
+    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+    uint8_t* const v_lds = lds + 2 * M::kKeys;
+    uint8_t* const p_lds = v_lds + 2 * M::kValues;                            // (pairs)
+    float* const m_lds = reinterpret_cast<float*>(p_lds + (PAIR ? 4 * 4 * 64 * 16 : 0));
+    uint32_t* const most = reinterpret_cast<uint32_t*>(lds + M::kBytes - 64);   // [2][8 waves]
+    const int tid = threadIdx.x, lane = tid & 63, col = lane & 31, half = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int group = PAIR ? wave & 3 : wave, part = PAIR ? wave >> 2 : 0;
+    const uint32_t kvh = blockIdx.x % a.c.kv_heads;
+    const Piece w0 = find_piece(a, blockIdx.x / a.c.kv_heads, false);
+    if (w0.seq < 0) return;
+    const uint32_t seq = static_cast<uint32_t>(w0.seq);
+    const SeqRows r = seq_rows(a.s, seq);
+    const uint32_t all = static_cast<uint32_t>(r.count) * a.group;
+    const uint32_t tiles = (all + M::kCols - 1) / M::kCols;
+    const Span sp = span_of(a, r);
+    const int32_t per = (sp.hi - sp.lo + static_cast<int32_t>(w0.pieces) - 1) / static_cast<int32_t>(w0.pieces);
+    const int32_t b0 = min(sp.lo + static_cast<int32_t>(w0.piece) * per, sp.hi), b1 = min(b0 + per, sp.hi);
+    const float fm = fabsf(a.scale_log2);         // (a negative scale's sign is in the queries)
+    // the last tiles see the most: they begin first
+    for (uint32_t turn = blockIdx.y; turn < tiles; turn += gridDim.y) {
+        const uint32_t tile = tiles - 1 - turn;
+        const Columns w = columns<M::kCols>(a, r, kvh, tile, 32 * group + col);
+        const int32_t p0 = max(b0, w.lo / kPage), p1 = min(b1, (w.hi + kPage - 1) / kPage);
+        // positions that the column sees (one without a row has a zero query and sees what the last has)
+        const int32_t see_hi = (w.row < 0 ? w.last_pos : w.pos) + 1, see_lo = sees_from(a.window, see_hi - 1);
+        // positions that all of the wave's columns see: [full_lo, full_hi)
+        const uint32_t c0 = tile * M::kCols + 32 * group;
+        const int32_t full_lo = sees_from(a.window, r.base + static_cast<int32_t>(min(c0 + 31, all - 1) / a.group));
+        const int32_t full_hi = r.base + static_cast<int32_t>(min(c0, all - 1) / a.group) + 1;
+
+        // the queries, the second operand of the scores: k-step 4 B + i has channels 8 i .. 8 i + 7 of block 2 B + half
+        bf16x8 qf[QS];
+        {
+            const uint16_t* qp = static_cast<const uint16_t*>(a.q) + (static_cast<uint64_t>(r.first + max(w.row, 0)) * a.heads + w.head) * D + kBlock * half;
+            const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;
+#pragma unroll
+            for (int s = 0; s < QS; ++s) {
+                uint4 u = make_uint4(0, 0, 0, 0);
+                if (w.row >= 0) u = *reinterpret_cast<const uint4*>(qp + 2 * kBlock * (s / 4) + 8 * (s % 4));
+                qf[s] = __builtin_bit_cast(bf16x8, make_uint4(u.x ^ flip, u.y ^ flip, u.z ^ flip, u.w ^ flip));
+            }
+        }
+
+        // Lane i has the id of page at + i (-1: none).
+        int32_t at = p0, ids = -1;
+        auto look = [&](int32_t p) {
+            at = p;
+            ids = p + lane < p1 ? page_id(a.c, a.s, seq, p + lane) : -1;
+        };
+        auto place = [&](int32_t p) {
+            const int32_t id = __builtin_amdgcn_readlane(ids, (p - at) & 63);
+            return p < p1 ? id : -1;
+        };
+
+        // The thread's pieces of a page's keys and values, and the scales of the keys that its lane multiplies, on the
+        // way from memory (where there is no page, page 0 is read and not used).
+        const bool has_k = PER != 0 || tid < PIECES, has_v = PER != 0 || (tid >= PIECES && tid < 2 * PIECES);
+        const int vi = PER != 0 ? tid : tid - PIECES;
+        constexpr int VC = D / 8;                 // pieces (16 bytes) of a group of four tokens
+        const uint32_t v_group = (vi / VC) & 15, v_piece = vi % VC;
+        uint4 kc = make_uint4(0, 0, 0, 0), vc = kc;
+        uint32_t vs = 0, ks[KB / 2], ks_next[KB / 2];
+        auto fetch = [&](int32_t p) {
+            const uint64_t pl = static_cast<uint64_t>(max(place(p), 0)) * a.c.kv_heads + kvh;
+            if (has_k) kc = *reinterpret_cast<const uint4*>(a.c.k + pl * kCodeBytes<D> + 16 * tid);
+            if (has_v) {
+                vc = *reinterpret_cast<const uint4*>(a.c.v + pl * kCodeBytes<D> + 16 * vi);
+                vs = *reinterpret_cast<const uint32_t*>(a.c.v_scale + pl * kScaleBytes<D> + v_scale_at<D>(4 * v_group, v_piece * 8 / kBlock));
+            }
+            // (tokens row % 16 + 16 i of block 2 B + half: byte i)
+#pragma unroll
+            for (int b = 0; b < KB / 2; ++b)
+                ks_next[b] = *reinterpret_cast<const uint32_t*>(a.c.k_scale + pl * kScaleBytes<D> + k_scale_at<D>(col & 15, 2 * b + half));
+        };
+        // (shifted so that tile t's is byte 2 t)
+        auto take_scales = [&] {
+#pragma unroll
+            for (int b = 0; b < KB / 2; ++b) ks[b] = ks_next[b] >> (8 * (col >> 4));
+        };
+        // Whether a column may see token i of the thread's four.
+        auto seen = [&](int32_t p, int i) {
+            const int32_t t = p * kPage + 4 * static_cast<int32_t>(v_group) + i;
+            return (t >= w.lo) & (t < w.hi) & (place(p) >= 0);
+        };
+        // The largest exponent byte among the values of a page that are seen, into shared memory.
+        auto tell = [&](int32_t p) {
+            uint32_t m = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) m = max(m, has_v && seen(p, i) ? vs >> (8 * i) & 0xFFu : 0u);
+            m = wave_max_u32(m);
+            if (lane == 0) most[8 * (p & 1) + wave] = m;
+        };
+        int32_t want = kNoUnit, unit = kNoUnit;   // the unit's exponent (biased) of the page staged; of the outputs
+        auto settle = [&](int32_t p) {
+            const uint4 u = reinterpret_cast<const uint4*>(most + 8 * (p & 1))[0], v = reinterpret_cast<const uint4*>(most + 8 * (p & 1))[1];
+            const int32_t m = __builtin_amdgcn_readfirstlane(static_cast<int>(max(max(max(u.x, u.y), max(u.z, u.w)), max(max(v.x, v.y), max(v.z, v.w)))));
+            // (0: nothing is seen)
+            if (m != 0 && (want == kNoUnit || m > want + 13 || m < want - 10)) want = m + 4;
+        };
+        // Into shared memory.  Rows of 16-byte chunks, permuted so that reads meet in no bank.
+        constexpr int kKeyRow = D / 2;
+        auto key_chunk = [](uint32_t row, uint32_t c) { return D == 256 ? c ^ ((row >> 1) & 7) : (D == 128 ? c ^ ((row >> 2) & 3) : c); };
+        auto stage_k = [&](int32_t p) {
+            const uint32_t row = tid / KB, c = tid % KB;
+            if (has_k) *reinterpret_cast<uint4*>(lds + (p & 1) * M::kKeys + row * kKeyRow + 16 * key_chunk(row, c)) = kc;
+        };
+        auto stage_v = [&](int32_t p) {
+            if (!has_v) return;
+            uint32_t word[4] = {vc.x, vc.y, vc.z, vc.w};
+            float d[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int32_t byte = static_cast<int32_t>(vs >> (8 * i) & 0xFFu) - want + 127;
+                const bool in = seen(p, i);              // what no column sees may be anything: 0
+                d[i] = in ? scale_of(static_cast<uint32_t>(max(byte, 1))) : 1.f;
+                if constexpr (D == 64) {                 // (token i: 16 bits of words i / 2 and 2 + i / 2)
+                    const uint32_t keep = in ? 0xFFFFFFFFu : (i % 2 == 0 ? 0xFFFF0000u : 0xFFFFu);
+                    word[i / 2] &= keep;
+                    word[2 + i / 2] &= keep;
+                } else if constexpr (D == 128) {
+                    word[i] = in ? word[i] : 0u;
+                }
+            }
+            if constexpr (D == 256) {                    // (a piece is two of the tokens, 8 bytes each)
+                const int i0 = 2 * (v_piece & 1);
+                const bool in0 = seen(p, i0), in1 = seen(p, i0 + 1);
+                word[0] = in0 ? word[0] : 0u;
+                word[1] = in0 ? word[1] : 0u;
+                word[2] = in1 ? word[2] : 0u;
+                word[3] = in1 ? word[3] : 0u;
+            }
+            // group 4 s + g of a page is the (0, 2, 1, 3)-th of its 16 tokens
+            const uint32_t chunk = 2 * (v_group / 4) + (v_group & 1), eighth = (v_group >> 1) & 1;
+            uint8_t* buf = v_lds + (p & 1) * M::kValues;
+            auto row_at = [&](uint32_t row) { return buf + row * M::kValueRow + 16 * (chunk ^ ((row >> 1) & 7)) + 8 * eighth; };
+            if constexpr (D == 256) {
+                const uint32_t c = v_piece / 2, i0 = 2 * (v_piece & 1);
+                const float d0 = i0 == 0 ? d[0] : d[2], d1 = i0 == 0 ? d[1] : d[3];
+#pragma unroll
+                for (int b = 0; b < 8; ++b) {            // a byte: two channels of two tokens
+                    const uint32_t u = word[b / 4], v = word[2 + b / 4];
+                    const uint32_t x = b % 4 == 0 ? pair_f16<0>(u, d0) : (b % 4 == 1 ? pair_f16<1>(u, d0) : (b % 4 == 2 ? pair_f16<2>(u, d0) : pair_f16<3>(u, d0)));
+                    const uint32_t y = b % 4 == 0 ? pair_f16<0>(v, d1) : (b % 4 == 1 ? pair_f16<1>(v, d1) : (b % 4 == 2 ? pair_f16<2>(v, d1) : pair_f16<3>(v, d1)));
+                    *reinterpret_cast<uint32_t*>(row_at((2 * b) * 16 + c) + 2 * i0) = lowers(x, y);
+                    *reinterpret_cast<uint32_t*>(row_at((2 * b + 1) * 16 + c) + 2 * i0) = uppers(x, y);
+                }
+            } else {
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {            // a byte: two channels of four tokens
+                    uint32_t x[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        // D 128: word i is token i, 8 channels; 64: words 2 h and 2 h + 1 are sixteenth h's 4 channels
+                        const uint32_t u = D == 64 ? word[2 * (b / 2) + i / 2] : word[i];
+                        const int byte_at = D == 64 ? 2 * (i % 2) + b % 2 : b;
+                        x[i] = byte_at == 0 ? pair_f16<0>(u, d[i]) : (byte_at == 1 ? pair_f16<1>(u, d[i]) : (byte_at == 2 ? pair_f16<2>(u, d[i]) : pair_f16<3>(u, d[i])));
+                    }
+                    // channels of the byte: sixteenth c, its channels m and m + 1: rows m * 16 + c
+                    const uint32_t c = D == 64 ? 2 * v_piece + b / 2 : v_piece, m0 = D == 64 ? 2 * (b % 2) : 2 * b;
+                    *reinterpret_cast<uint2*>(row_at(m0 * 16 + c)) = make_uint2(lowers(x[0], x[1]), lowers(x[2], x[3]));
+                    *reinterpret_cast<uint2*>(row_at((m0 + 1) * 16 + c)) = make_uint2(uppers(x[0], x[1]), uppers(x[2], x[3]));
+                }
+            }
+        };
+
+        f32x16 o[ET];
+        float m_run = -__builtin_inff(), l_run = 0.f;
+#pragma unroll
+        for (int e = 0; e < ET; ++e)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[e][i] = 0.f;
+        bool begun = false;                      // every column of the wave has a reference
+
+        auto scores = [&](int32_t p, f32x16 (&sc)[ST]) {
+            const uint8_t* buf = lds + (p & 1) * M::kKeys;
+#pragma unroll
+            for (int t = 0; t < ST; ++t) {
+                const uint32_t row = 32 * (t + part) + col;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) sc[t][i] = 0.f;
+#pragma unroll
+                for (int b = 0; b < KB / 2; ++b) {
+                    const uint4 u = *reinterpret_cast<const uint4*>(buf + row * kKeyRow + 16 * key_chunk(row, 2 * b + half));
+                    const float d = scale_of(ks[b] >> (PAIR ? 16 * part : 16 * t) & 0xFFu);
+                    const uint32_t word[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) sc[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(values8(word[i], d), qf[4 * b + i], sc[t], 0, 0, 0);
+                }
+            }
+        };
+        const uint32_t v_from = static_cast<uint32_t>((32 * ET * part + col) * M::kValueRow + 16 * (half ^ ((col >> 1) & 7)));
+        auto values = [&](int32_t p, const f16x8 (&pf)[4]) {
+            const uint8_t* buf = v_lds + (p & 1) * M::kValues;
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+#pragma unroll
+                for (int e = 0; e < ET; ++e)
+                    o[e] = __builtin_amdgcn_mfma_f32_32x32x16_f16(*reinterpret_cast<const f16x8*>(buf + (v_from ^ (32 * s)) + e * 32 * M::kValueRow), pf[s], o[e], 0, 0, 0);
+        };
+        // Probabilities e^(sc mul - base), and their sum in the lane (of the rounded ones).
+        auto weigh = [&](const f32x16 (&sc)[ST], float mul, float base, f16x8 (&pf)[2 * ST]) {
+            const f16x2 one = {static_cast<_Float16>(1.f), static_cast<_Float16>(1.f)};
+            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int t = 0; t < ST; ++t)
+#pragma unroll
+                for (int i = 0; i < 16; i += 2) {
+                    const float x = __builtin_amdgcn_exp2f(fmaf(sc[t][i], mul, -base));
+                    const float y = __builtin_amdgcn_exp2f(fmaf(sc[t][i + 1], mul, -base));
+                    const f16x2 h = {static_cast<_Float16>(x), static_cast<_Float16>(y)};
+                    sum[(i >> 1) & 3] = __builtin_amdgcn_fdot2(h, one, sum[(i >> 1) & 3], false);
+                    pf[2 * t + (i >> 3)][i & 7] = h[0];
+                    pf[2 * t + (i >> 3)][(i & 7) + 1] = h[1];
+                }
+            return (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        };
+        auto scale_outputs = [&](float f) {
+#pragma unroll
+            for (int e = 0; e < ET; ++e)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[e][i] *= f;
+        };
+        // The scores of a page times fm, those that are not seen -infinity, and the largest of the column.
+        auto masked = [&](int32_t p, f32x16 (&sc)[ST]) {
+            float mt = -__builtin_inff();
+#pragma unroll
+            for (int t = 0; t < ST; ++t) {
+                const int32_t t0 = p * kPage + 32 * (t + part) + 4 * half, lo = see_lo - t0, hi = see_hi - t0;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const int32_t k = 8 * (i >> 2) + (i & 3);
+                    sc[t][i] = k >= lo && k < hi ? sc[t][i] * fm : -__builtin_inff();
+                    mt = fmaxf(mt, sc[t][i]);
+                }
+            }
+            return max_halves(mt);
+        };
+        // Moves the reference, where the largest score of a page is above it.
+        auto refer = [&](int32_t p, float mt) {
+            // (of tokens that give only NaN the reference is 0)
+            if (mt == -__builtin_inff() && m_run == mt && max(see_lo, p * kPage) < min(see_hi, p * kPage + kPage)) mt = 0.f;
+            if (__any(mt > m_run + kMoveManyAt)) {
+                const float m_new = mt > m_run + kMoveManyAt ? mt : m_run;
+                const float keep = m_new == m_run ? 1.f : __builtin_amdgcn_exp2f(m_run - m_new);
+                m_run = m_new;
+                l_run *= keep;
+                scale_outputs(keep);
+            }
+            begun = __all(m_run > -__builtin_inff());
+            return (m_run > -__builtin_inff() ? m_run : 0.f) - kBias;
+        };
+
+        if (p0 < p1) {
+            look(p0);
+            fetch(p0);
+            if (tid < 16) most[tid] = 0;
+            __syncthreads();
+            tell(p0);
+            stage_k(p0);
+            __syncthreads();
+            settle(p0);
+            stage_v(p0);
+            take_scales();
+            fetch(p0 + 1);
+            unit = want;
+            __syncthreads();
+#pragma unroll 1
+            for (int32_t p = p0; p < p1; ++p) {
+                const bool there = place(p) >= 0;
+                const bool full = p * kPage >= full_lo && p * kPage + kPage <= full_hi;
+                if (there) {
+                    f32x16 sc[ST];
+                    f16x8 pf[4];
+                    scores(p, sc);
+                    if constexpr (PAIR) {
+                        float mt;
+                        if (full) {
+                            mt = -__builtin_inff();
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) mt = fmaxf(mt, sc[0][i] *= fm);
+                            mt = max_halves(mt);
+                        } else {
+                            mt = masked(p, sc);
+                        }
+                        if (half == 0) m_lds[(2 * group + part) * 32 + col] = mt;
+                        __syncthreads();
+                        mt = fmaxf(mt, m_lds[(2 * group + (part ^ 1)) * 32 + col]);
+                        f16x8 mine[2];
+                        l_run += weigh(sc, 1.f, refer(p, mt), mine);
+#pragma unroll
+                        for (int s = 0; s < 2; ++s) reinterpret_cast<f16x8*>(p_lds)[(4 * group + 2 * part + s) * 64 + lane] = mine[s];
+                        __syncthreads();
+#pragma unroll
+                        for (int s = 0; s < 4; ++s) pf[s] = reinterpret_cast<const f16x8*>(p_lds)[(4 * group + s) * 64 + lane];
+                    } else {
+                        float l = weigh(sc, fm, m_run - kBias, pf);
+                        // (no number stays none whatever the reference)
+                        if (!full || !begun || __any(l >= kSumLimit)) l = weigh(sc, 1.f, refer(p, masked(p, sc)), pf);
+                        l_run += l;
+                    }
+                    if (unit != want) {          // outputs so far in the unit of this page's values
+                        scale_outputs(ldexpf(1.f, unit - want));   // (kNoUnit: they are 0)
+                        unit = want;
+                    }
+                    values(p, pf);
+                }
+                tell(p + 1);
+                stage_k(p + 1);
+                __syncthreads();
+                settle(p + 1);
+                stage_v(p + 1);
+                take_scales();
+                if (p + 3 - at > 64) look(p);
+                fetch(p + 2);
+                __syncthreads();
+            }
+        }
+        const float v_scale = unit == kNoUnit ? 0.f : ldexpf(1.f, unit - 127);
+
+        float l = l_run + __shfl_xor(l_run, 32);
+        if constexpr (PAIR) {
+            __syncthreads();
+            if (half == 0) m_lds[(2 * group + part) * 32 + col] = l;
+            __syncthreads();
+            l = m_lds[2 * group * 32 + col] + m_lds[(2 * group + 1) * 32 + col];
+            __syncthreads();
+        }
+        if (w.row >= 0) {
+            const float inv = (w0.pieces > 1 ? 1.f : (l == 0.f ? 0.f : 1.f / l));
+            const uint64_t slot = (w0.first + static_cast<uint64_t>(w0.piece) * static_cast<uint32_t>(r.count) + static_cast<uint32_t>(w.row)) * a.heads + w.head;
+            const uint64_t to = (static_cast<uint64_t>(r.first + w.row) * a.heads + w.head) * D;
+            if (w0.pieces > 1 && half == 0 && part == 0) a.stat[slot] = make_float2(m_run, l);
+            // register 4 q + i of tile e is channel (D / 16) c + m, c = 8 (q % 2) + 4 half + i, m = 2 (e + ET part) + q / 2
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int ch = D / 16 * (8 * q + 4 * half + i) + 2 * ET * part;
+                    float v[2 * ET];
+#pragma unroll
+                    for (int e = 0; e < ET; ++e) {
+                        v[2 * e] = o[e][4 * q + i] * inv * v_scale;
+                        v[2 * e + 1] = o[e][8 + 4 * q + i] * inv * v_scale;
+                    }
+                    if (w0.pieces > 1) {
+#pragma unroll
+                        for (int e = 0; e < 2 * ET; e += 4) *reinterpret_cast<float4*>(a.part + slot * D + ch + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+                    } else {
+                        typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+#pragma unroll
+                        for (int e = 0; e < 2 * ET; e += 4) {
+                            const bf16x4 b = {static_cast<__bf16>(v[e]), static_cast<__bf16>(v[e + 1]), static_cast<__bf16>(v[e + 2]), static_cast<__bf16>(v[e + 3])};
+                            *reinterpret_cast<bf16x4*>(static_cast<__bf16*>(a.out) + to + ch + e) = b;
+                        }
+                    }
+                }
+        }
+    }
+}
+
 // Joins the pieces of each column of a sequence that was cut: a wave has a
 // column, lane z piece z's maximum and sum, and the pieces' outputs are added
 // in their order, D / 64 values a lane.
@@ -553,30 +972,46 @@ uint64_t span_pages(const qmv_kv_seqs& s, uint32_t window, uint64_t rows) {
     return (span + kPage - 1) / kPage + 1;
 }
 
+// How a call is dealt out: few queries with the waves of a workgroup sharing the
+// pages, or each with its own columns, or many.
+enum Kind { kShared, kSolo, kMany };
 struct Plan {
-    bool solo;
+    Kind kind;
     uint32_t tiles, target, least, slots;
     uint64_t room;
 };
-constexpr uint32_t kWorkgroups = 512;          // that a launch aims at
+constexpr uint32_t kWorkgroups = 512;          // that a launch of the kernel for few aims at
 constexpr uint32_t kWhole = 16;                // pages up to which a sequence is not cut
+constexpr uint64_t kManyCols = 16384;
+constexpr double kManyWork = 2e6;
 
-Plan plan_of(const qmv_kv4_cache& c, const qmv_kv_seqs& s, uint32_t heads, uint32_t window) {
+Plan plan_of(const qmv_kv4_cache& c, const qmv_kv_seqs& s, uint32_t dtype, uint32_t heads, uint32_t window) {
     const uint64_t group = heads / c.kv_heads;
     const uint64_t most = s.max_new < s.rows ? (s.max_new == 0 ? 1 : s.max_new) : s.rows;
-    uint64_t tiles = (most * group + 15) / 16;
-    const uint64_t wgs = uint64_t{s.seqs} * c.kv_heads * tiles, pages = span_pages(s, window, most);
+    const uint64_t pages = span_pages(s, window, most), cols = most * group;
     Plan p{};
-    p.solo = wgs >= 1024;
-    if (p.solo) tiles = (tiles + 3) / 4;
+    // (pages of the middle row)
+    qmv_kv_seqs mean = s;
+    mean.max_len -= static_cast<uint32_t>(most / 2 < s.max_len ? most / 2 : s.max_len);
+    const double work = static_cast<double>(uint64_t{s.seqs} * c.kv_heads) * static_cast<double>((cols + 15) / 16) *
+                        static_cast<double>(span_pages(mean, window, 16)) * c.head_dim;
+    if (dtype == QMV_BF16 && cols * c.head_dim >= kManyCols && work >= kManyWork) p.kind = kMany;
+    const uint64_t wide = p.kind == kMany ? (c.head_dim == 256 ? 128 : 256) : 16;
+    uint64_t tiles = (cols + wide - 1) / wide;
+    const uint64_t wgs = uint64_t{s.seqs} * c.kv_heads * tiles;
+    if (p.kind != kMany && wgs >= 1024) {
+        p.kind = kSolo;
+        tiles = (tiles + 3) / 4;
+    }
     p.tiles = static_cast<uint32_t>(tiles > 65535 ? 65535 : tiles);
     p.slots = s.seqs;
-    if (p.solo || s.seqs > kScanSeqs || pages <= kWhole) return p;
-    uint64_t target = (kWorkgroups + c.kv_heads * tiles - 1) / (c.kv_heads * tiles);
+    if (p.kind == kSolo || s.seqs > kScanSeqs || pages <= kWhole || (p.kind == kMany && wgs >= 192)) return p;
+    const uint64_t aim = p.kind == kMany ? 256 : kWorkgroups;
+    uint64_t target = (aim + c.kv_heads * tiles - 1) / (c.kv_heads * tiles);
     if (target < s.seqs / 2) target = s.seqs / 2;
     if (target < 1) target = 1;
     p.target = static_cast<uint32_t>(target);
-    p.least = 4;
+    p.least = p.kind == kMany ? 8 : 4;
     p.slots = p.target + s.seqs;
     const uint64_t pieces = target < kMaxPieces ? target : kMaxPieces;
     uint64_t room = pieces * s.rows;
@@ -588,7 +1023,20 @@ Plan plan_of(const qmv_kv4_cache& c, const qmv_kv_seqs& s, uint32_t heads, uint3
 template <uint32_t DT, int D>
 hipError_t go(const Attend4Args& a, const Plan& p, hipStream_t s) {
     const dim3 grid(p.slots * a.c.kv_heads, p.tiles), block(256);
-    if (p.solo) hipLaunchKernelGGL((attend4_few_kernel<DT, D, true>), grid, block, 0, s, a);
+    bool done = false;
+    if constexpr (DT == QMV_BF16) {
+        if (p.kind == kMany) {
+            constexpr int bytes = Many<D>::kBytes;
+            if constexpr (bytes > 65536) {
+                const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(attend4_many_kernel<D>), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+                if (e != hipSuccess) return e;
+            }
+            hipLaunchKernelGGL((attend4_many_kernel<D>), grid, dim3(Many<D>::kThreads), bytes, s, a);
+            done = true;
+        }
+    }
+    if (done) {
+    } else if (p.kind == kSolo) hipLaunchKernelGGL((attend4_few_kernel<DT, D, true>), grid, block, 0, s, a);
     else hipLaunchKernelGGL((attend4_few_kernel<DT, D, false>), grid, block, 0, s, a);
     hipError_t e = hipGetLastError();
     if (e == hipSuccess && p.target != 0) {
@@ -610,13 +1058,13 @@ hipError_t go(const Attend4Args& a, const Plan& p, hipStream_t s) {
 
 }  // namespace
 
-uint64_t kv4_attend_workspace_bytes(const qmv_kv4_cache& c, const qmv_kv_seqs& s, uint32_t, uint32_t heads, uint32_t window) {
-    return plan_of(c, s, heads, window).room * heads * (c.head_dim + 2) * 4;
+uint64_t kv4_attend_workspace_bytes(const qmv_kv4_cache& c, const qmv_kv_seqs& s, uint32_t dtype, uint32_t heads, uint32_t window) {
+    return plan_of(c, s, dtype, heads, window).room * heads * (c.head_dim + 2) * 4;
 }
 
 hipError_t launch_kv4_attend(const qmv_kv4_cache& c, const qmv_kv_seqs& s, uint32_t dtype, uint32_t heads, float scale, uint32_t window,
                              const void* q, void* out, void* workspace, hipStream_t stream) {
-    const Plan p = plan_of(c, s, heads, window);
+    const Plan p = plan_of(c, s, dtype, heads, window);
     float* part = static_cast<float*>(workspace);
     const Attend4Args a{c, s, q, out, part, reinterpret_cast<float2*>(part + p.room * heads * c.head_dim), scale * kLog2e, heads,
                         heads / c.kv_heads, window, p.target, p.least, static_cast<uint32_t>(p.room)};

@@ -64,6 +64,11 @@ template <int B>
 __device__ __forceinline__ uint32_t pair_bf16(uint32_t w, float d) {
     return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, d, B));
 }
+// As float16 (rounded below 2^-24, infinite past 65504).
+template <int B>
+__device__ __forceinline__ uint32_t pair_f16(uint32_t w, float d) {
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, d, B));
+}
 // Eight codes as bfloat16 values.
 __device__ __forceinline__ bf16x8 values8(uint32_t w, float d) {
     const uint4 u = make_uint4(pair_bf16<0>(w, d), pair_bf16<1>(w, d), pair_bf16<2>(w, d), pair_bf16<3>(w, d));

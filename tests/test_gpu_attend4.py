@@ -142,6 +142,70 @@ def test_many_columns(dtype):
     check([260, 70], [260, 70], 8, 2, 256, dtype, seed=23, window=100)
 
 
+FAR = (None, 1 << 20)      # a hint of long sequences: bfloat16 columns enough then go to the kernel for many
+
+
+@pytest.mark.parametrize("window", [0, 1, 50, 64, 200])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_kernel_for_many(dim, window):
+    """Tiles with and without rows to fill them, edges of causality and window
+    inside a page, groups that do not divide a tile, empty sequences."""
+    check([300, 40], [300, 40], 8, 2, dim, "bf16", seed=dim + window, window=window, hints=FAR)
+    check([700], [90], 5, 1, dim, "bf16", seed=dim + window + 1, window=window, hints=FAR)
+    check([0, 130, 64, 0, 1], [0, 130, 64, 3, 1], 24, 4, dim, "bf16", seed=dim + window + 2, window=window, hints=FAR)
+    check([3, 70, 0], [80, 200, 90], 4, 2, dim, "bf16", seed=dim + window + 3, window=window, hints=FAR)
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_kernel_for_many_in_pieces(dim):
+    """One sequence's pages shared by workgroups, joined afterwards; page ids more than a wave looks up at once."""
+    check([5000], [70], 4, 1, dim, "bf16", seed=dim, hints=FAR)
+    check([4500, 100], [64, 64], 4, 1, dim, "bf16", seed=dim + 1, scale=-0.05, hints=FAR)
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_kernel_for_many_rising_scores(dim):
+    """Scores that rise along the sequence, so that references move all the
+    time, and rows for which they fall; value scales that rise and fall by far
+    between the pages."""
+    g, c, table = make([900], 1, dim, 31, k_exp=(-2, -1))
+    c.code["k"][:] = 4                             # 2
+    for p in range(15):
+        c.byte["k"][table[0, p]] = 127 - 8 + p
+        c.byte["v"][table[0, p]] += (0, 30, 20, 60, 40, 10, 0, 3, 50, 0, 0, 25, 9, 1, 70)[p]
+    q = queries(g, 200, 2, dim)
+    q[::2] = np.abs(q[::2])
+    q[1::2] = -np.abs(q[1::2])
+    got = attend(to_gpu(c), seqs(table, [900], [0, 200], *((200, 1 << 20))), q, "bf16")
+    ref, b = M.attend(c, table, [900], [0, 200], q, np.float32(dim ** -0.5), 0)
+    near(got, ref, b, dim, 900, "bf16")
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_kernel_for_many_and_what_is_not_there(dim):
+    """Unknown pages between known ones, tokens and queries that are no number."""
+    g, c, table = make([500, 300], 2, dim, 32)
+    c.byte["v"][0, :, :, 0] = 255                  # (a page that none has: what stands in for unknown ones)
+    order = np.unique(table[table >= 0])
+    spare = [p for p in range(c.pages) if p not in order]
+    table = table.copy()
+    table[0, 2], table[0, 5], table[1, 0] = -7, c.pages, -1
+    c.byte["k"][table[0, 3], 1, 9], c.byte["v"][table[0, 3], 1, 9], c.code["v"][table[0, 3], 1, 9] = 255, 2, 0
+    start = [0, 300, 500]
+    q = queries(g, 500, 16, dim)
+    q[123, 2, 3] = np.nan
+    s = seqs(table, [500, 300], start, 300, 1 << 20)
+    got = attend(to_gpu(c), s, q, "bf16")
+    ref, b = M.attend(c, table, [500, 300], start, np.where(np.isnan(q), 0, q), np.float32(dim ** -0.5), 0)
+    nan = np.zeros((500, 16), dtype=bool)
+    nan[:300, 8:] = np.arange(200, 500)[:, None] >= 3 * 64 + 9
+    nan[123, 2] = True
+    assert np.array_equal(np.isnan(got).any(-1), nan) and np.array_equal(np.isnan(got).all(-1), nan)
+    assert len(spare) >= 1
+    ref, got = np.where(nan[..., None], 0, ref), np.where(nan[..., None], 0, got)
+    near(got, ref, {n: np.where(nan[..., None], 1, x) for n, x in b.items()}, dim, 500, "bf16")
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_more_rows_than_tokens(dtype):
     """Positions below 0 see nothing: zeros."""
