@@ -131,11 +131,11 @@ class Cache4:
 
 def attend(cache, table, lens, start, q, scale, window):
     """(out, sizes): outputs in 64 bits; mass: sum p |v|; smax: the largest |s|;
-    qk: the largest |scale| sum |q| |k|, of every row and head."""
+    qk: the largest |scale| sum |q| |k|; vmax: the largest |v|, of every row and head."""
     rows, heads, dim = q.shape
     g = heads // cache.heads
     out, mass = np.zeros(q.shape), np.zeros(q.shape)
-    smax, qk = np.zeros((rows, heads, 1)), np.zeros((rows, heads, 1))
+    smax, qk, vmax = np.zeros((rows, heads, 1)), np.zeros((rows, heads, 1)), np.zeros((rows, heads, 1))
     for i in range(len(lens)):
         n, new = int(lens[i]), start[i + 1] - start[i]
         if new == 0:
@@ -157,10 +157,11 @@ def attend(cache, table, lens, start, q, scale, window):
                     out[row, h], mass[row, h] = p @ vv, p @ np.abs(vv)
                     smax[row, h] = np.abs(s).max()
                     qk[row, h] = abs(scale) * (np.abs(kk) @ np.abs(qq)).max()
-    return out, {"mass": mass, "smax": smax, "qk": qk}
+                    vmax[row, h] = np.abs(vv).max()
+    return out, {"mass": mass, "smax": smax, "qk": qk, "vmax": vmax}
 
 
-def attend_bound(b, dim, longest, dtype):
+def attend_bound(b, dim, longest, dtype, many=False):
     """How far an output may be off.
 
     A score is a sum of at most 3 dim products (three parts of a float32 query
@@ -171,10 +172,12 @@ def attend_bound(b, dim, longest, dtype):
     (and pieces: fifty more), each addition rounding to 2^-24 of the sum of
     magnitudes.  With bfloat16 the probabilities may be rounded to 11 bits,
     2^-11 of each product and of each term of the sum: 2^-10; the output rounds
-    by half a step, 2^-8 (added by the caller)."""
+    by half a step, 2^-8 (added by the caller).  In the kernel for many they are
+    float16 numbers of which the largest is at least 4, so that the least are off
+    by up to 2^-25, 2^-27 of the sum: that times |v|max, for each token."""
     d = 3 * dim * 2.0 ** -24 * b["qk"] + 8 * 2.0 ** -24 * b["smax"] + 2.0 ** -21
     rel = np.expm1(2 * d) + (3 * longest + 50) * 2.0 ** -23
-    return b["mass"] * (rel + (2.0 ** -10 if dtype == "bf16" else 0.0))
+    return b["mass"] * (rel + (2.0 ** -10 if dtype == "bf16" else 0.0)) + (longest * 2.0 ** -27 * b["vmax"] if many else 0.0)
 
 
 # ---- the draw ---------------------------------------------------------------
