@@ -531,7 +531,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attend4_few_kernel(Atte
 template <int D>
 struct Many {
     static constexpr bool kPair = D == 256;
-    static constexpr int kThreads = 512, kCols = kPair ? 128 : 256;
+    static constexpr int kThreads = kPair ? 512 : 256, kCols = 128;
     static constexpr int kKeys = kCodeBytes<D>, kValueRow = 2 * kPage, kValues = D * kValueRow;   // bytes of a page
     // (pairs: probabilities [4 column groups][4 k-steps][64 lanes], maxima [4][2 halves][32])
     static constexpr int kExchange = kPair ? 4 * 4 * 64 * 16 + 4 * 2 * 32 * 4 : 0;
@@ -543,7 +543,7 @@ constexpr float kMoveManyAt = 4.f;
 constexpr int32_t kNoUnit = -1000;
 
 template <int D>
-__global__ __launch_bounds__(512, 2) void attend4_many_kernel(Attend4Args a) {
+__global__ __launch_bounds__(Many<D>::kThreads, 2) void attend4_many_kernel(Attend4Args a) {
     typedef Many<D> M;
     typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
     typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
@@ -553,7 +553,7 @@ __global__ __launch_bounds__(512, 2) void attend4_many_kernel(Attend4Args a) {
     constexpr int ST = PAIR ? 1 : 2;              // tiles of 32 tokens that a wave scores
     constexpr int ET = D / (PAIR ? 64 : 32);      // tiles of output channels that a wave adds up
     // pieces of 16 bytes of codes: of keys (32 channels of a token), of values (four tokens, 128 / D sixteenths)
-    constexpr int PIECES = kPage * D / 32, PER = PIECES > 512 / 2 ? 1 : 0;   // PER: a thread has both
+    constexpr int PIECES = kPage * D / 32, PER = PIECES > M::kThreads / 2 ? 1 : 0;   // PER: a thread has both
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
     uint8_t* const v_lds = lds + 2 * M::kKeys;
     uint8_t* const p_lds = v_lds + 2 * M::kValues;                            // (pairs)
@@ -616,18 +616,19 @@ __global__ __launch_bounds__(512, 2) void attend4_many_kernel(Attend4Args a) {
         constexpr int VC = D / 8;                 // pieces (16 bytes) of a group of four tokens
         const uint32_t v_group = (vi / VC) & 15, v_piece = vi % VC;
         uint4 kc = make_uint4(0, 0, 0, 0), vc = kc;
-        uint32_t vs = 0, ks[KB / 2], ks_next[KB / 2];
+        uint32_t vs = 0, vs_next = 0, ks[KB / 2], ks_next[KB / 2];
         auto fetch = [&](int32_t p) {
             const uint64_t pl = static_cast<uint64_t>(max(place(p), 0)) * a.c.kv_heads + kvh;
             if (has_k) kc = *reinterpret_cast<const uint4*>(a.c.k + pl * kCodeBytes<D> + 16 * tid);
-            if (has_v) {
-                vc = *reinterpret_cast<const uint4*>(a.c.v + pl * kCodeBytes<D> + 16 * vi);
-                vs = *reinterpret_cast<const uint32_t*>(a.c.v_scale + pl * kScaleBytes<D> + v_scale_at<D>(4 * v_group, v_piece * 8 / kBlock));
-            }
+            if (has_v) vc = *reinterpret_cast<const uint4*>(a.c.v + pl * kCodeBytes<D> + 16 * vi);
             // (tokens row % 16 + 16 i of block 2 B + half: byte i)
 #pragma unroll
             for (int b = 0; b < KB / 2; ++b)
                 ks_next[b] = *reinterpret_cast<const uint32_t*>(a.c.k_scale + pl * kScaleBytes<D> + k_scale_at<D>(col & 15, 2 * b + half));
+        };
+        auto fetch_next = [&](int32_t p) {
+            const uint64_t pl = static_cast<uint64_t>(max(place(p), 0)) * a.c.kv_heads + kvh;
+            if (has_v) vs_next = *reinterpret_cast<const uint32_t*>(a.c.v_scale + pl * kScaleBytes<D> + v_scale_at<D>(4 * v_group, v_piece * 8 / kBlock));
         };
         // (shifted so that tile t's is byte 2 t)
         auto take_scales = [&] {
@@ -643,7 +644,7 @@ __global__ __launch_bounds__(512, 2) void attend4_many_kernel(Attend4Args a) {
         auto tell = [&](int32_t p) {
             uint32_t m = 0;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) m = max(m, has_v && seen(p, i) ? vs >> (8 * i) & 0xFFu : 0u);
+            for (int i = 0; i < 4; ++i) m = max(m, has_v & seen(p, i) ? vs_next >> (8 * i) & 0xFFu : 0u);
             m = wave_max_u32(m);
             if (lane == 0) most[8 * (p & 1) + wave] = m;
         };
@@ -754,6 +755,18 @@ __global__ __launch_bounds__(512, 2) void attend4_many_kernel(Attend4Args a) {
                 for (int e = 0; e < ET; ++e)
                     o[e] = __builtin_amdgcn_mfma_f32_32x32x16_f16(*reinterpret_cast<const f16x8*>(buf + (v_from ^ (32 * s)) + e * 32 * M::kValueRow), pf[s], o[e], 0, 0, 0);
         };
+        // The output's products with the next page's way into shared memory between them, operands read ahead.
+        auto mixed = [] {
+            constexpr int N = 4 * ET, kAhead = 6;
+            __builtin_amdgcn_sched_group_barrier(0x100, kAhead, 0);
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                if (i < N - kAhead) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x002, 6, 0);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        };
         // Probabilities e^(sc mul - base), and their sum in the lane (of the rounded ones).
         auto weigh = [&](const f32x16 (&sc)[ST], float mul, float base, f16x8 (&pf)[2 * ST]) {
             const f16x2 one = {static_cast<_Float16>(1.f), static_cast<_Float16>(1.f)};
@@ -778,11 +791,11 @@ __global__ __launch_bounds__(512, 2) void attend4_many_kernel(Attend4Args a) {
                 for (int i = 0; i < 16; ++i) o[e][i] *= f;
         };
         // The scores of a page times fm, those that are not seen -infinity, and the largest of the column.
-        auto masked = [&](int32_t p, f32x16 (&sc)[ST]) {
+        auto masked = [&](int32_t p, bool there, f32x16 (&sc)[ST]) {
             float mt = -__builtin_inff();
 #pragma unroll
             for (int t = 0; t < ST; ++t) {
-                const int32_t t0 = p * kPage + 32 * (t + part) + 4 * half, lo = see_lo - t0, hi = see_hi - t0;
+                const int32_t t0 = p * kPage + 32 * (t + part) + 4 * half, lo = see_lo - t0, hi = there ? see_hi - t0 : -kPage;
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                     const int32_t k = 8 * (i >> 2) + (i & 3);
@@ -793,9 +806,9 @@ __global__ __launch_bounds__(512, 2) void attend4_many_kernel(Attend4Args a) {
             return max_halves(mt);
         };
         // Moves the reference, where the largest score of a page is above it.
-        auto refer = [&](int32_t p, float mt) {
+        auto refer = [&](int32_t p, bool there, float mt) {
             // (of tokens that give only NaN the reference is 0)
-            if (mt == -__builtin_inff() && m_run == mt && max(see_lo, p * kPage) < min(see_hi, p * kPage + kPage)) mt = 0.f;
+            if (there && mt == -__builtin_inff() && m_run == mt && max(see_lo, p * kPage) < min(see_hi, p * kPage + kPage)) mt = 0.f;
             if (__any(mt > m_run + kMoveManyAt)) {
                 const float m_new = mt > m_run + kMoveManyAt ? mt : m_run;
                 const float keep = m_new == m_run ? 1.f : __builtin_amdgcn_exp2f(m_run - m_new);
@@ -810,65 +823,74 @@ __global__ __launch_bounds__(512, 2) void attend4_many_kernel(Attend4Args a) {
         if (p0 < p1) {
             look(p0);
             fetch(p0);
+            fetch_next(p0);
             if (tid < 16) most[tid] = 0;
             __syncthreads();
             tell(p0);
+            vs = vs_next;
+            fetch_next(p0 + 1);
             stage_k(p0);
             __syncthreads();
             settle(p0);
+            tell(p0 + 1);
             stage_v(p0);
             take_scales();
+            vs = vs_next;
             fetch(p0 + 1);
+            fetch_next(p0 + 2);
             unit = want;
             __syncthreads();
+            // One barrier a page: while page p is computed, p + 1 goes into the other buffers, and what p + 2 holds at
+            // most is told.
 #pragma unroll 1
             for (int32_t p = p0; p < p1; ++p) {
                 const bool there = place(p) >= 0;
-                const bool full = p * kPage >= full_lo && p * kPage + kPage <= full_hi;
-                if (there) {
-                    f32x16 sc[ST];
-                    f16x8 pf[4];
-                    scores(p, sc);
-                    if constexpr (PAIR) {
-                        float mt;
-                        if (full) {
-                            mt = -__builtin_inff();
+                const bool full = there && p * kPage >= full_lo && p * kPage + kPage <= full_hi;
+                f32x16 sc[ST];
+                f16x8 pf[4];
+                scores(p, sc);
+                if constexpr (PAIR) {
+                    float mt;
+                    if (full) {
+                        mt = -__builtin_inff();
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) mt = fmaxf(mt, sc[0][i] *= fm);
-                            mt = max_halves(mt);
-                        } else {
-                            mt = masked(p, sc);
-                        }
-                        if (half == 0) m_lds[(2 * group + part) * 32 + col] = mt;
-                        __syncthreads();
-                        mt = fmaxf(mt, m_lds[(2 * group + (part ^ 1)) * 32 + col]);
-                        f16x8 mine[2];
-                        l_run += weigh(sc, 1.f, refer(p, mt), mine);
-#pragma unroll
-                        for (int s = 0; s < 2; ++s) reinterpret_cast<f16x8*>(p_lds)[(4 * group + 2 * part + s) * 64 + lane] = mine[s];
-                        __syncthreads();
-#pragma unroll
-                        for (int s = 0; s < 4; ++s) pf[s] = reinterpret_cast<const f16x8*>(p_lds)[(4 * group + s) * 64 + lane];
+                        for (int i = 0; i < 16; ++i) mt = fmaxf(mt, sc[0][i] *= fm);
+                        mt = max_halves(mt);
                     } else {
-                        float l = weigh(sc, fm, m_run - kBias, pf);
-                        // (no number stays none whatever the reference)
-                        if (!full || !begun || __any(l >= kSumLimit)) l = weigh(sc, 1.f, refer(p, masked(p, sc)), pf);
-                        l_run += l;
+                        mt = masked(p, there, sc);
                     }
-                    if (unit != want) {          // outputs so far in the unit of this page's values
-                        scale_outputs(ldexpf(1.f, unit - want));   // (kNoUnit: they are 0)
-                        unit = want;
-                    }
-                    values(p, pf);
+                    if (half == 0) m_lds[(2 * group + part) * 32 + col] = mt;
+                    __syncthreads();
+                    mt = fmaxf(mt, m_lds[(2 * group + (part ^ 1)) * 32 + col]);
+                    f16x8 mine[2];
+                    l_run += weigh(sc, 1.f, refer(p, there, mt), mine);
+#pragma unroll
+                    for (int s = 0; s < 2; ++s) reinterpret_cast<f16x8*>(p_lds)[(4 * group + 2 * part + s) * 64 + lane] = mine[s];
+                    __syncthreads();
+#pragma unroll
+                    for (int s = 0; s < 4; ++s) pf[s] = reinterpret_cast<const f16x8*>(p_lds)[(4 * group + s) * 64 + lane];
+                } else {
+                    float l = weigh(sc, fm, m_run - kBias, pf);
+                    // (no number stays none whatever the reference)
+                    if (!full || !begun || __any(l >= kSumLimit)) l = weigh(sc, 1.f, refer(p, there, masked(p, there, sc)), pf);
+                    l_run += l;
                 }
-                tell(p + 1);
-                stage_k(p + 1);
-                __syncthreads();
+                if (unit != want) {              // outputs so far in the unit of this page's values
+                    scale_outputs(ldexpf(1.f, unit - want));   // (kNoUnit: they are 0)
+                    unit = want;
+                }
                 settle(p + 1);
+                __builtin_amdgcn_sched_barrier(0);
+                values(p, pf);
+                stage_k(p + 1);
                 stage_v(p + 1);
+                tell(p + 2);
+                mixed();
                 take_scales();
-                if (p + 3 - at > 64) look(p);
+                vs = vs_next;
+                if (p + 4 - at > 64) look(p);
                 fetch(p + 2);
+                fetch_next(p + 3);
                 __syncthreads();
             }
         }
@@ -996,7 +1018,7 @@ Plan plan_of(const qmv_kv4_cache& c, const qmv_kv_seqs& s, uint32_t dtype, uint3
     const double work = static_cast<double>(uint64_t{s.seqs} * c.kv_heads) * static_cast<double>((cols + 15) / 16) *
                         static_cast<double>(span_pages(mean, window, 16)) * c.head_dim;
     if (dtype == QMV_BF16 && cols * c.head_dim >= kManyCols && work >= kManyWork) p.kind = kMany;
-    const uint64_t wide = p.kind == kMany ? (c.head_dim == 256 ? 128 : 256) : 16;
+    const uint64_t wide = p.kind == kMany ? 128 : 16;
     uint64_t tiles = (cols + wide - 1) / wide;
     const uint64_t wgs = uint64_t{s.seqs} * c.kv_heads * tiles;
     if (p.kind != kMany && wgs >= 1024) {
