@@ -533,8 +533,8 @@ struct Many {
     static constexpr bool kPair = D == 256;
     static constexpr int kThreads = kPair ? 512 : 256, kCols = 128;
     static constexpr int kKeys = kCodeBytes<D>, kValueRow = 2 * kPage, kValues = D * kValueRow;   // bytes of a page
-    // (pairs: probabilities [4 column groups][4 k-steps][64 lanes], maxima [4][2 halves][32])
-    static constexpr int kExchange = kPair ? 4 * 4 * 64 * 16 + 4 * 2 * 32 * 4 : 0;
+    // (pairs: probabilities [4 column groups][4 k-steps][64 lanes], maxima [4][2 halves][32], two flags)
+    static constexpr int kExchange = kPair ? 4 * 4 * 64 * 16 + 4 * 2 * 32 * 4 + 16 : 0;
     static constexpr int kBytes = 2 * (kKeys + kValues) + kExchange + 64;   // 64: the pages' largest exponents, of each wave
 };
 constexpr float kSumLimit = 0x1p15f;       // of a page's probabilities in a lane
@@ -550,7 +550,6 @@ __global__ __launch_bounds__(Many<D>::kThreads, 2) void attend4_many_kernel(Atte
     constexpr bool PAIR = M::kPair;
     constexpr int QS = D / 16;                    // k-steps of a score
     constexpr int KB = D / kBlock;                // blocks of a token
-    constexpr int ST = PAIR ? 1 : 2;              // tiles of 32 tokens that a wave scores
     constexpr int ET = D / (PAIR ? 64 : 32);      // tiles of output channels that a wave adds up
     // pieces of 16 bytes of codes: of keys (32 channels of a token), of values (four tokens, 128 / D sixteenths)
     constexpr int PIECES = kPage * D / 32, PER = PIECES > M::kThreads / 2 ? 1 : 0;   // PER: a thread has both
@@ -558,6 +557,7 @@ __global__ __launch_bounds__(Many<D>::kThreads, 2) void attend4_many_kernel(Atte
     uint8_t* const v_lds = lds + 2 * M::kKeys;
     uint8_t* const p_lds = v_lds + 2 * M::kValues;                            // (pairs)
     float* const m_lds = reinterpret_cast<float*>(p_lds + (PAIR ? 4 * 4 * 64 * 16 : 0));
+    uint32_t* const again = reinterpret_cast<uint32_t*>(m_lds + (PAIR ? 4 * 2 * 32 : 0));   // (pairs) [2]: the page's probabilities once more
     uint32_t* const most = reinterpret_cast<uint32_t*>(lds + M::kBytes - 64);   // [2][8 waves]
     const int tid = threadIdx.x, lane = tid & 63, col = lane & 31, half = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -635,25 +635,38 @@ __global__ __launch_bounds__(Many<D>::kThreads, 2) void attend4_many_kernel(Atte
 #pragma unroll
             for (int b = 0; b < KB / 2; ++b) ks[b] = ks_next[b] >> (8 * (col >> 4));
         };
-        // Whether a column may see token i of the thread's four.
+        // Whether a column may see token i of the thread's four, and whether one may see all of a page.
         auto seen = [&](int32_t p, int i) {
             const int32_t t = p * kPage + 4 * static_cast<int32_t>(v_group) + i;
             return (t >= w.lo) & (t < w.hi) & (place(p) >= 0);
         };
-        // The largest exponent byte among the values of a page that are seen, into shared memory.
-        auto tell = [&](int32_t p) {
-            uint32_t m = 0;
+        auto whole = [&](int32_t p) { return p * kPage >= w.lo && p * kPage + kPage <= w.hi && place(p) >= 0; };
+        // Exponent bytes of values that no column sees become 0.
+        auto visible = [&](int32_t p, uint32_t bytes) {
+            if (!whole(p)) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) m = max(m, has_v & seen(p, i) ? vs_next >> (8 * i) & 0xFFu : 0u);
-            m = wave_max_u32(m);
-            if (lane == 0) most[8 * (p & 1) + wave] = m;
+                for (int i = 0; i < 4; ++i) bytes &= seen(p, i) ? 0xFFFFFFFFu : ~(0xFFu << (8 * i));
+            }
+            return bytes;
         };
-        int32_t want = kNoUnit, unit = kNoUnit;   // the unit's exponent (biased) of the page staged; of the outputs
+        // The unit's exponent (biased) of the page staged, and of the outputs.  What the waves tell each other of a page
+        // ahead: 1: its largest exponent is too high for the unit so far, 2: high enough, and the largest byte above.
+        int32_t want = kNoUnit, unit = kNoUnit;
+        auto tell = [&](int32_t p) {
+            if (!has_v) return;                  // (a whole wave: it says nothing)
+            const uint32_t v = visible(p, vs_next), m = max(max(v & 0xFFu, v >> 8 & 0xFFu), max(v >> 16 & 0xFFu, v >> 24));
+            const bool high = __any(static_cast<int32_t>(m) > want + 13), enough = __any(static_cast<int32_t>(m) >= want - 10);
+            uint32_t word = 2;
+            if (high || !enough) word = 1 | wave_max_u32(m) << 8;   // (also: no unit so far)
+            if (lane == 0) most[8 * (p & 1) + wave] = word;
+        };
         auto settle = [&](int32_t p) {
             const uint4 u = reinterpret_cast<const uint4*>(most + 8 * (p & 1))[0], v = reinterpret_cast<const uint4*>(most + 8 * (p & 1))[1];
-            const int32_t m = __builtin_amdgcn_readfirstlane(static_cast<int>(max(max(max(u.x, u.y), max(u.z, u.w)), max(max(v.x, v.y), max(v.z, v.w)))));
-            // (0: nothing is seen)
-            if (m != 0 && (want == kNoUnit || m > want + 13 || m < want - 10)) want = m + 4;
+            const uint32_t some = __builtin_amdgcn_readfirstlane(static_cast<int>((u.x | u.y | u.z | u.w) | (v.x | v.y | v.z | v.w)));
+            if ((some & 1) == 0) return;
+            const int32_t m = __builtin_amdgcn_readfirstlane(static_cast<int>(max(max(max(u.x, u.y), max(u.z, u.w)), max(max(v.x, v.y), max(v.z, v.w))) >> 8));
+            // (0: nothing is seen; some waves may have exponents high enough where others have none)
+            if (m != 0 && (want == kNoUnit || m > want + 13 || ((some & 2) == 0 && m < want - 10))) want = m + 4;
         };
         // Into shared memory.  Rows of 16-byte chunks, permuted so that reads meet in no bank.
         constexpr int kKeyRow = D / 2;
@@ -662,59 +675,63 @@ __global__ __launch_bounds__(Many<D>::kThreads, 2) void attend4_many_kernel(Atte
             const uint32_t row = tid / KB, c = tid % KB;
             if (has_k) *reinterpret_cast<uint4*>(lds + (p & 1) * M::kKeys + row * kKeyRow + 16 * key_chunk(row, c)) = kc;
         };
-        auto stage_v = [&](int32_t p) {
-            if (!has_v) return;
+        // What no column sees may be anything: 0.  (Before the page goes into shared memory.)
+        auto hide = [&](int32_t p) {
+            if (whole(p)) return;
+            vs = visible(p, vs);
             uint32_t word[4] = {vc.x, vc.y, vc.z, vc.w};
-            float d[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int32_t byte = static_cast<int32_t>(vs >> (8 * i) & 0xFFu) - want + 127;
-                const bool in = seen(p, i);              // what no column sees may be anything: 0
-                d[i] = in ? scale_of(static_cast<uint32_t>(max(byte, 1))) : 1.f;
                 if constexpr (D == 64) {                 // (token i: 16 bits of words i / 2 and 2 + i / 2)
-                    const uint32_t keep = in ? 0xFFFFFFFFu : (i % 2 == 0 ? 0xFFFF0000u : 0xFFFFu);
+                    const uint32_t keep = seen(p, i) ? 0xFFFFFFFFu : (i % 2 == 0 ? 0xFFFF0000u : 0xFFFFu);
                     word[i / 2] &= keep;
                     word[2 + i / 2] &= keep;
                 } else if constexpr (D == 128) {
-                    word[i] = in ? word[i] : 0u;
+                    word[i] = seen(p, i) ? word[i] : 0u;
+                } else {
+                    word[i] = seen(p, 2 * (v_piece & 1) + i / 2) ? word[i] : 0u;
                 }
             }
-            if constexpr (D == 256) {                    // (a piece is two of the tokens, 8 bytes each)
-                const int i0 = 2 * (v_piece & 1);
-                const bool in0 = seen(p, i0), in1 = seen(p, i0 + 1);
-                word[0] = in0 ? word[0] : 0u;
-                word[1] = in0 ? word[1] : 0u;
-                word[2] = in1 ? word[2] : 0u;
-                word[3] = in1 ? word[3] : 0u;
+            vc = make_uint4(word[0], word[1], word[2], word[3]);
+        };
+        auto stage_v = [&](int32_t p) {
+            if (!has_v) return;
+            uint32_t word[4] = {vc.x, vc.y, vc.z, vc.w};
+            if constexpr (D == 256) {
+                // a piece is two tokens of a sixteenth's 16 channels, the next lane's the other two: each takes 8
+                // channels of the four
+                const bool odd = (v_piece & 1) != 0;
+                const uint32_t a0 = dpp_u32<0xB1>(odd ? word[0] : word[1]), a1 = dpp_u32<0xB1>(odd ? word[2] : word[3]);
+                const uint32_t b0 = odd ? word[1] : word[0], b1 = odd ? word[3] : word[2];
+                word[0] = odd ? a0 : b0;
+                word[1] = odd ? a1 : b1;
+                word[2] = odd ? b0 : a0;
+                word[3] = odd ? b1 : a1;
+            }
+            float d[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int32_t byte = static_cast<int32_t>(vs >> (8 * i) & 0xFFu);
+                d[i] = scale_of(static_cast<uint32_t>(max(byte, want - 126) - want + 127));
             }
             // group 4 s + g of a page is the (0, 2, 1, 3)-th of its 16 tokens
             const uint32_t chunk = 2 * (v_group / 4) + (v_group & 1), eighth = (v_group >> 1) & 1;
             uint8_t* buf = v_lds + (p & 1) * M::kValues;
             auto row_at = [&](uint32_t row) { return buf + row * M::kValueRow + 16 * (chunk ^ ((row >> 1) & 7)) + 8 * eighth; };
-            if constexpr (D == 256) {
-                const uint32_t c = v_piece / 2, i0 = 2 * (v_piece & 1);
-                const float d0 = i0 == 0 ? d[0] : d[2], d1 = i0 == 0 ? d[1] : d[3];
-#pragma unroll
-                for (int b = 0; b < 8; ++b) {            // a byte: two channels of two tokens
-                    const uint32_t u = word[b / 4], v = word[2 + b / 4];
-                    const uint32_t x = b % 4 == 0 ? pair_f16<0>(u, d0) : (b % 4 == 1 ? pair_f16<1>(u, d0) : (b % 4 == 2 ? pair_f16<2>(u, d0) : pair_f16<3>(u, d0)));
-                    const uint32_t y = b % 4 == 0 ? pair_f16<0>(v, d1) : (b % 4 == 1 ? pair_f16<1>(v, d1) : (b % 4 == 2 ? pair_f16<2>(v, d1) : pair_f16<3>(v, d1)));
-                    *reinterpret_cast<uint32_t*>(row_at((2 * b) * 16 + c) + 2 * i0) = lowers(x, y);
-                    *reinterpret_cast<uint32_t*>(row_at((2 * b + 1) * 16 + c) + 2 * i0) = uppers(x, y);
-                }
-            } else {
+            {
 #pragma unroll
                 for (int b = 0; b < 4; ++b) {            // a byte: two channels of four tokens
                     uint32_t x[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        // D 128: word i is token i, 8 channels; 64: words 2 h and 2 h + 1 are sixteenth h's 4 channels
+                        // word i is token i, 8 channels; D 64: words 2 h and 2 h + 1 are sixteenth h's 4 channels
                         const uint32_t u = D == 64 ? word[2 * (b / 2) + i / 2] : word[i];
                         const int byte_at = D == 64 ? 2 * (i % 2) + b % 2 : b;
                         x[i] = byte_at == 0 ? pair_f16<0>(u, d[i]) : (byte_at == 1 ? pair_f16<1>(u, d[i]) : (byte_at == 2 ? pair_f16<2>(u, d[i]) : pair_f16<3>(u, d[i])));
                     }
                     // channels of the byte: sixteenth c, its channels m and m + 1: rows m * 16 + c
-                    const uint32_t c = D == 64 ? 2 * v_piece + b / 2 : v_piece, m0 = D == 64 ? 2 * (b % 2) : 2 * b;
+                    const uint32_t c = D == 64 ? 2 * v_piece + b / 2 : (D == 128 ? v_piece : v_piece / 2);
+                    const uint32_t m0 = D == 64 ? 2 * (b % 2) : (D == 128 ? 0 : 8 * (v_piece & 1)) + 2 * b;
                     *reinterpret_cast<uint2*>(row_at(m0 * 16 + c)) = make_uint2(lowers(x[0], x[1]), lowers(x[2], x[3]));
                     *reinterpret_cast<uint2*>(row_at((m0 + 1) * 16 + c)) = make_uint2(uppers(x[0], x[1]), uppers(x[2], x[3]));
                 }
@@ -729,60 +746,49 @@ __global__ __launch_bounds__(Many<D>::kThreads, 2) void attend4_many_kernel(Atte
             for (int i = 0; i < 16; ++i) o[e][i] = 0.f;
         bool begun = false;                      // every column of the wave has a reference
 
-        auto scores = [&](int32_t p, f32x16 (&sc)[ST]) {
-            const uint8_t* buf = lds + (p & 1) * M::kKeys;
+        // The codes of tile t of a page (32 tokens; a pair's wave has one tile, `part`), and its scores.
+        auto codes = [&](int32_t p, int t, uint4 (&u)[KB / 2]) {
+            const uint32_t row = 32 * t + col;
+            const uint8_t* from = lds + (p & 1) * M::kKeys + row * kKeyRow;
 #pragma unroll
-            for (int t = 0; t < ST; ++t) {
-                const uint32_t row = 32 * (t + part) + col;
+            for (int b = 0; b < KB / 2; ++b) u[b] = *reinterpret_cast<const uint4*>(from + 16 * key_chunk(row, 2 * b + half));
+        };
+        auto scores = [&](const uint4 (&from)[KB / 2], int t, f32x16& sc) {
 #pragma unroll
-                for (int i = 0; i < 16; ++i) sc[t][i] = 0.f;
+            for (int i = 0; i < 16; ++i) sc[i] = 0.f;
 #pragma unroll
-                for (int b = 0; b < KB / 2; ++b) {
-                    const uint4 u = *reinterpret_cast<const uint4*>(buf + row * kKeyRow + 16 * key_chunk(row, 2 * b + half));
-                    const float d = scale_of(ks[b] >> (PAIR ? 16 * part : 16 * t) & 0xFFu);
-                    const uint32_t word[4] = {u.x, u.y, u.z, u.w};
+            for (int b = 0; b < KB / 2; ++b) {
+                const uint4 u = from[b];
+                const float d = scale_of(ks[b] >> (16 * t) & 0xFFu);
+                const uint32_t word[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) sc[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(values8(word[i], d), qf[4 * b + i], sc[t], 0, 0, 0);
-                }
+                for (int i = 0; i < 4; ++i) sc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(values8(word[i], d), qf[4 * b + i], sc, 0, 0, 0);
             }
         };
         const uint32_t v_from = static_cast<uint32_t>((32 * ET * part + col) * M::kValueRow + 16 * (half ^ ((col >> 1) & 7)));
-        auto values = [&](int32_t p, const f16x8 (&pf)[4]) {
+        // The output's products of a tile's two k-steps.
+        auto values = [&](int32_t p, int t, const f16x8 (&pf)[2]) {
             const uint8_t* buf = v_lds + (p & 1) * M::kValues;
 #pragma unroll
-            for (int s = 0; s < 4; ++s)
+            for (int s = 0; s < 2; ++s)
 #pragma unroll
                 for (int e = 0; e < ET; ++e)
-                    o[e] = __builtin_amdgcn_mfma_f32_32x32x16_f16(*reinterpret_cast<const f16x8*>(buf + (v_from ^ (32 * s)) + e * 32 * M::kValueRow), pf[s], o[e], 0, 0, 0);
+                    o[e] = __builtin_amdgcn_mfma_f32_32x32x16_f16(*reinterpret_cast<const f16x8*>(buf + (v_from ^ (64 * t + 32 * s)) + e * 32 * M::kValueRow), pf[s], o[e], 0, 0, 0);
         };
-        // The output's products with the next page's way into shared memory between them, operands read ahead.
-        auto mixed = [] {
-            constexpr int N = 4 * ET, kAhead = 6;
-            __builtin_amdgcn_sched_group_barrier(0x100, kAhead, 0);
-#pragma unroll
-            for (int i = 0; i < N; ++i) {
-                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-                if (i < N - kAhead) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-                __builtin_amdgcn_sched_group_barrier(0x002, 6, 0);
-            }
-            __builtin_amdgcn_sched_barrier(0);
-        };
-        // Probabilities e^(sc mul - base), and their sum in the lane (of the rounded ones).
-        auto weigh = [&](const f32x16 (&sc)[ST], float mul, float base, f16x8 (&pf)[2 * ST]) {
+        // A tile's probabilities e^(sc mul - base), and their sum in the lane (of the rounded ones).
+        auto weigh = [&](const f32x16& sc, float mul, float base, f16x8 (&pf)[2]) {
             const f16x2 one = {static_cast<_Float16>(1.f), static_cast<_Float16>(1.f)};
-            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+            float sum[2] = {0.f, 0.f};
 #pragma unroll
-            for (int t = 0; t < ST; ++t)
-#pragma unroll
-                for (int i = 0; i < 16; i += 2) {
-                    const float x = __builtin_amdgcn_exp2f(fmaf(sc[t][i], mul, -base));
-                    const float y = __builtin_amdgcn_exp2f(fmaf(sc[t][i + 1], mul, -base));
-                    const f16x2 h = {static_cast<_Float16>(x), static_cast<_Float16>(y)};
-                    sum[(i >> 1) & 3] = __builtin_amdgcn_fdot2(h, one, sum[(i >> 1) & 3], false);
-                    pf[2 * t + (i >> 3)][i & 7] = h[0];
-                    pf[2 * t + (i >> 3)][(i & 7) + 1] = h[1];
-                }
-            return (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            for (int i = 0; i < 16; i += 2) {
+                const float x = __builtin_amdgcn_exp2f(fmaf(sc[i], mul, -base));
+                const float y = __builtin_amdgcn_exp2f(fmaf(sc[i + 1], mul, -base));
+                const f16x2 h = {static_cast<_Float16>(x), static_cast<_Float16>(y)};
+                sum[(i >> 1) & 1] = __builtin_amdgcn_fdot2(h, one, sum[(i >> 1) & 1], false);
+                pf[i >> 3][i & 7] = h[0];
+                pf[i >> 3][(i & 7) + 1] = h[1];
+            }
+            return sum[0] + sum[1];
         };
         auto scale_outputs = [&](float f) {
 #pragma unroll
@@ -790,25 +796,22 @@ __global__ __launch_bounds__(Many<D>::kThreads, 2) void attend4_many_kernel(Atte
 #pragma unroll
                 for (int i = 0; i < 16; ++i) o[e][i] *= f;
         };
-        // The scores of a page times fm, those that are not seen -infinity, and the largest of the column.
-        auto masked = [&](int32_t p, bool there, f32x16 (&sc)[ST]) {
+        // A tile's scores times fm, those that are not seen -infinity, and the largest of the column.
+        auto masked = [&](int32_t t0, bool there, f32x16& sc) {
             float mt = -__builtin_inff();
+            const int32_t lo = see_lo - t0 - 4 * half, hi = there ? see_hi - t0 - 4 * half : -kPage;
 #pragma unroll
-            for (int t = 0; t < ST; ++t) {
-                const int32_t t0 = p * kPage + 32 * (t + part) + 4 * half, lo = see_lo - t0, hi = there ? see_hi - t0 : -kPage;
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int32_t k = 8 * (i >> 2) + (i & 3);
-                    sc[t][i] = k >= lo && k < hi ? sc[t][i] * fm : -__builtin_inff();
-                    mt = fmaxf(mt, sc[t][i]);
-                }
+            for (int i = 0; i < 16; ++i) {
+                const int32_t k = 8 * (i >> 2) + (i & 3);
+                sc[i] = k >= lo && k < hi ? sc[i] * fm : -__builtin_inff();
+                mt = fmaxf(mt, sc[i]);
             }
             return max_halves(mt);
         };
-        // Moves the reference, where the largest score of a page is above it.
-        auto refer = [&](int32_t p, bool there, float mt) {
+        // Moves the reference, where the largest score of `tokens` from t0 on is above it.
+        auto refer = [&](int32_t t0, int32_t tokens, bool there, float mt) {
             // (of tokens that give only NaN the reference is 0)
-            if (there && mt == -__builtin_inff() && m_run == mt && max(see_lo, p * kPage) < min(see_hi, p * kPage + kPage)) mt = 0.f;
+            if (there && mt == -__builtin_inff() && m_run == mt && max(see_lo, t0) < min(see_hi, t0 + tokens)) mt = 0.f;
             if (__any(mt > m_run + kMoveManyAt)) {
                 const float m_new = mt > m_run + kMoveManyAt ? mt : m_run;
                 const float keep = m_new == m_run ? 1.f : __builtin_amdgcn_exp2f(m_run - m_new);
@@ -825,6 +828,7 @@ __global__ __launch_bounds__(Many<D>::kThreads, 2) void attend4_many_kernel(Atte
             fetch(p0);
             fetch_next(p0);
             if (tid < 16) most[tid] = 0;
+            if (PAIR && tid < 2) again[tid] = 0;
             __syncthreads();
             tell(p0);
             vs = vs_next;
@@ -833,11 +837,8 @@ __global__ __launch_bounds__(Many<D>::kThreads, 2) void attend4_many_kernel(Atte
             __syncthreads();
             settle(p0);
             tell(p0 + 1);
+            hide(p0);
             stage_v(p0);
-            take_scales();
-            vs = vs_next;
-            fetch(p0 + 1);
-            fetch_next(p0 + 2);
             unit = want;
             __syncthreads();
             // One barrier a page: while page p is computed, p + 1 goes into the other buffers, and what p + 2 holds at
@@ -846,51 +847,90 @@ __global__ __launch_bounds__(Many<D>::kThreads, 2) void attend4_many_kernel(Atte
             for (int32_t p = p0; p < p1; ++p) {
                 const bool there = place(p) >= 0;
                 const bool full = there && p * kPage >= full_lo && p * kPage + kPage <= full_hi;
-                f32x16 sc[ST];
-                f16x8 pf[4];
-                scores(p, sc);
-                if constexpr (PAIR) {
-                    float mt;
-                    if (full) {
-                        mt = -__builtin_inff();
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) mt = fmaxf(mt, sc[0][i] *= fm);
-                        mt = max_halves(mt);
-                    } else {
-                        mt = masked(p, there, sc);
-                    }
-                    if (half == 0) m_lds[(2 * group + part) * 32 + col] = mt;
-                    __syncthreads();
-                    mt = fmaxf(mt, m_lds[(2 * group + (part ^ 1)) * 32 + col]);
-                    f16x8 mine[2];
-                    l_run += weigh(sc, 1.f, refer(p, there, mt), mine);
-#pragma unroll
-                    for (int s = 0; s < 2; ++s) reinterpret_cast<f16x8*>(p_lds)[(4 * group + 2 * part + s) * 64 + lane] = mine[s];
-                    __syncthreads();
-#pragma unroll
-                    for (int s = 0; s < 4; ++s) pf[s] = reinterpret_cast<const f16x8*>(p_lds)[(4 * group + s) * 64 + lane];
-                } else {
-                    float l = weigh(sc, fm, m_run - kBias, pf);
-                    // (no number stays none whatever the reference)
-                    if (!full || !begun || __any(l >= kSumLimit)) l = weigh(sc, 1.f, refer(p, there, masked(p, there, sc)), pf);
-                    l_run += l;
-                }
-                if (unit != want) {              // outputs so far in the unit of this page's values
+                // (while the page's codes are on their way) the scales of its keys, and what comes after the next page
+                auto ahead = [&] {
+                    take_scales();
+                    if (p + 3 - at > 64) look(p);
+                    fetch(p + 1);
+                    vs = vs_next;
+                    fetch_next(p + 2);
+                };
+                // (no number stays none whatever the reference)
+                auto fits = [&](float l) { return full && begun && !__any(l >= kSumLimit); };
+                auto turn_unit = [&] {           // outputs so far in the unit of this page's values
+                    if (unit == want) return;
                     scale_outputs(ldexpf(1.f, unit - want));   // (kNoUnit: they are 0)
                     unit = want;
+                };
+                auto stage = [&] {
+                    stage_k(p + 1);
+                    stage_v(p + 1);
+                };
+                if constexpr (PAIR) {
+                    // The probabilities go through shared memory relative to the reference so far; if that does for one
+                    // wave not, all take the way over the page's maximum.
+                    f32x16 sc;
+                    f16x8 mine[2], pf[2][2];
+                    f16x8* const mail = reinterpret_cast<f16x8*>(p_lds) + 4 * group * 64 + lane;
+                    auto send = [&] {
+#pragma unroll
+                        for (int s = 0; s < 2; ++s) mail[(2 * part + s) * 64] = mine[s];
+                    };
+                    {
+                        uint4 u[KB / 2];
+                        codes(p, part, u);
+                        ahead();
+                        scores(u, part, sc);
+                    }
+                    float l = weigh(sc, fm, m_run - kBias, mine);
+                    send();
+                    if (!fits(l) && lane == 0) again[p & 1] = 1;
+                    __syncthreads();
+                    if (again[p & 1] != 0) {
+                        const float mt = masked(p * kPage + 32 * part, there, sc);
+                        if (half == 0) m_lds[(2 * group + part) * 32 + col] = mt;
+                        __syncthreads();
+                        l = weigh(sc, 1.f, refer(p * kPage, kPage, there, fmaxf(mt, m_lds[(2 * group + (part ^ 1)) * 32 + col])), mine);
+                        send();
+                        __syncthreads();
+                    }
+                    if (tid == 0) again[(p + 1) & 1] = 0;
+                    l_run += l;
+                    turn_unit();
+                    settle(p + 1);
+                    hide(p + 1);
+                    tell(p + 2);
+#pragma unroll
+                    for (int s = 0; s < 4; ++s) pf[s / 2][s % 2] = mail[s * 64];
+                    values(p, 0, pf[0]);
+                    values(p, 1, pf[1]);
+                    stage();
+                } else {
+                    // Stretches of products of one tile beside the exponentials of the other.
+                    f32x16 s0, s1;
+                    f16x8 f0[2], f1[2];
+                    uint4 u0[KB / 2], u1[KB / 2];
+                    codes(p, 0, u0);
+                    codes(p, 1, u1);
+                    ahead();
+                    scores(u0, 0, s0);
+                    scores(u1, 1, s1);
+                    float l = weigh(s0, fm, m_run - kBias, f0);
+                    asm volatile("" : "+v"(l));      // (formed here, beside the products, not in the branch that takes it)
+                    turn_unit();
+                    if (!fits(l)) l = weigh(s0, 1.f, refer(p * kPage, 32, there, masked(p * kPage, there, s0)), f0);
+                    l_run += l;
+                    values(p, 0, f0);
+                    l = weigh(s1, fm, m_run - kBias, f1);
+                    asm volatile("" : "+v"(l));
+                    if (!fits(l)) l = weigh(s1, 1.f, refer(p * kPage + 32, 32, there, masked(p * kPage + 32, there, s1)), f1);
+                    l_run += l;
+                    settle(p + 1);
+                    hide(p + 1);
+                    tell(p + 2);
+                    values(p, 1, f1);
+                    stage();
                 }
-                settle(p + 1);
-                __builtin_amdgcn_sched_barrier(0);
-                values(p, pf);
-                stage_k(p + 1);
-                stage_v(p + 1);
-                tell(p + 2);
-                mixed();
-                take_scales();
-                vs = vs_next;
-                if (p + 4 - at > 64) look(p);
-                fetch(p + 2);
-                fetch_next(p + 3);
                 __syncthreads();
             }
         }
@@ -1004,8 +1044,19 @@ struct Plan {
 };
 constexpr uint32_t kWorkgroups = 512;          // that a launch of the kernel for few aims at
 constexpr uint32_t kWhole = 16;                // pages up to which a sequence is not cut
+// bfloat16 queries go to the kernel for many where a sequence has columns enough
+// for its tiles (kManyCols / D) and the call work enough (products of 16 columns
+// with a page, times D) that its waves' waiting for each other is paid for.
+// Measured (us, few / many), sequences x tokens, columns:
+//   D 128, 8 heads: 1 x 16000, 64, 128 and 256: 24 / 30, 34 / 36 and 55 / 50; 8 x
+//     3000, 128 and 256: 36 / 39 and 55 / 63; 64 x 1000, 128 and 256: 53 / 46 and
+//     88 / 81; whole prompts 2 x 500 18 / 22, 1 x 1000 28 / 35, 1 x 2000 71 / 62
+//   D 256, 4 heads: 1 x 16000, 256: 43 / 60; 8 x 3000, 128 and 256: 41 / 52 and
+//     62 / 58; 64 x 1000, 128: 60 / 59; prompts 2 x 500 24 / 35, 1 x 4000 219 / 202
+//   D 64, 8 heads: 8 x 3000, 256 and 512: 42 / 55 and 66 / 76; 64 x 1000, 256 and
+//     512: 62 / 67 and 104 / 93; prompts 1 x 1000 21 / 33, 1 x 4000 153 / 109
 constexpr uint64_t kManyCols = 16384;
-constexpr double kManyWork = 2e6;
+constexpr double kManyWork = 7e6, kManyWork64 = 12e6;   // head dims of 64: the second
 
 Plan plan_of(const qmv_kv4_cache& c, const qmv_kv_seqs& s, uint32_t dtype, uint32_t heads, uint32_t window) {
     const uint64_t group = heads / c.kv_heads;
@@ -1017,7 +1068,7 @@ Plan plan_of(const qmv_kv4_cache& c, const qmv_kv_seqs& s, uint32_t dtype, uint3
     mean.max_len -= static_cast<uint32_t>(most / 2 < s.max_len ? most / 2 : s.max_len);
     const double work = static_cast<double>(uint64_t{s.seqs} * c.kv_heads) * static_cast<double>((cols + 15) / 16) *
                         static_cast<double>(span_pages(mean, window, 16)) * c.head_dim;
-    if (dtype == QMV_BF16 && cols * c.head_dim >= kManyCols && work >= kManyWork) p.kind = kMany;
+    if (dtype == QMV_BF16 && cols * c.head_dim >= kManyCols && work >= (c.head_dim == 64 ? kManyWork64 : kManyWork)) p.kind = kMany;
     const uint64_t wide = p.kind == kMany ? 128 : 16;
     uint64_t tiles = (cols + wide - 1) / wide;
     const uint64_t wgs = uint64_t{s.seqs} * c.kv_heads * tiles;
