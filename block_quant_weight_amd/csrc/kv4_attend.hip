@@ -37,6 +37,13 @@ constexpr float kLog2e = 1.4426950408889634f;
 // The running reference moves when a maximum is further above it: e^s stays
 // below 2^8 times the reference's.
 constexpr float kMoveAt = 8.f;
+// How a call is dealt out: few queries to a key/value head, the waves of a
+// workgroup sharing the pages (packed: a tile's columns few enough that each
+// part of a probability has a column of its own) or each with its own columns;
+// or many.
+enum Kind { kShared, kPacked, kSolo, kMany };
+template <uint32_t DT>
+constexpr uint32_t kPackedCols = DT == QMV_F32 ? 4 : 8;
 constexpr uint32_t kMaxPieces = 64;    // of a sequence
 constexpr uint32_t kScanSeqs = 1024;   // sequences up to which pieces are made
 
@@ -47,7 +54,9 @@ struct Attend4Args {
     void* out;
     float* part;          // [room][kv_heads * group][D]: output sums of pieces
     float2* stat;         // [room][kv_heads * group]: maximum, sum
-    float scale_log2;     // scale * log2(e)
+    float scale_log2;     // |scale| * log2(e) (1 where the scale is 0)
+    float move;           // what kMoveAt is of a product with a key
+    uint32_t keep, flip;  // bits of a query that the scale leaves, and turns
     uint32_t heads, group, window;
     uint32_t target;      // pieces of all sequences that the launch aims at; 0: sequences stay whole
     uint32_t least;       // pages of a piece, at least
@@ -223,12 +232,15 @@ __device__ __forceinline__ void split(float x, uint32_t part[N]) {
 __device__ __forceinline__ uint32_t uppers(uint32_t lo, uint32_t hi) { return __builtin_amdgcn_perm(hi, lo, 0x07060302u); }
 __device__ __forceinline__ uint32_t lowers(uint32_t lo, uint32_t hi) { return __builtin_amdgcn_perm(hi, lo, 0x05040100u); }
 
-template <uint32_t DT, int D, bool SOLO>
+template <uint32_t DT, int D, int KIND>
 __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attend4_few_kernel(Attend4Args a) {
     typedef typename Elem<DT>::type T;
+    constexpr bool SOLO = KIND == kSolo, PACKED = KIND == kPacked;
     constexpr int STEP = SOLO ? 1 : 4;            // waves that share the pages
-    constexpr int NQ = DT == QMV_F32 ? 3 : 1;     // parts of a query
-    constexpr int NP = DT == QMV_F32 ? 3 : 2;     // parts of a probability
+    constexpr int PARTS = DT == QMV_F32 ? 3 : 2;  // of a probability
+    constexpr uint32_t kCols = PACKED ? kPackedCols<DT> : 16;   // columns of a tile
+    constexpr int NQ = DT == QMV_F32 && !PACKED ? 3 : 1;        // operands made of a query
+    constexpr int NP = PACKED ? 1 : PARTS;                      // and of a probability
     constexpr int KS = D / 32;                    // k-steps of a score tile
     constexpr int W = D / 32;                     // words of a lane's quarter of a key, and of its four tokens' values
     constexpr int E = D / 16;                     // channels of a sixteenth, and tiles of the output
@@ -242,7 +254,8 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attend4_few_kernel(Atte
     const uint32_t seq = static_cast<uint32_t>(w0.seq);
     const SeqRows r = seq_rows(a.s, seq);
     const uint32_t all = static_cast<uint32_t>(r.count) * a.group;
-    const uint32_t tiles = (all + 15) / 16;
+    const uint32_t tiles = (all + kCols - 1) / kCols;
+    const uint32_t own = col / kCols;             // (packed: the part that the lane has)
     const Span sp = span_of(a, r);
     const int32_t per = (sp.hi - sp.lo + static_cast<int32_t>(w0.pieces) - 1) / static_cast<int32_t>(w0.pieces);
     const int32_t b0 = min(sp.lo + static_cast<int32_t>(w0.piece) * per, sp.hi), b1 = min(b0 + per, sp.hi);
@@ -250,7 +263,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attend4_few_kernel(Atte
     // the last tiles see the most: they begin first
     for (uint32_t turn = kOwn * blockIdx.y + (SOLO ? wave : 0); turn < tiles; turn += kOwn * gridDim.y) {
         const uint32_t tile = tiles - 1 - turn;
-        const Columns w = columns<16>(a, r, kvh, tile, col);
+        const Columns w = columns<kCols>(a, r, kvh, tile, col % kCols);
         const int32_t p0 = max(b0, w.lo / kPage), p1 = min(b1, (w.hi + kPage - 1) / kPage);
         const int32_t see_lo = sees_from(a.window, w.pos);
         // pages that every column sees whole: from full_lo up to full_hi
@@ -302,7 +315,16 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attend4_few_kernel(Atte
                 if (w.row >= 0) load8<DT>(qp + 8 * s, x);
                 uint32_t part[8][NQ];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) split<NQ>(x[i], part[i]);
+                for (int i = 0; i < 8; ++i) {
+                    const float y = __builtin_bit_cast(float, (__builtin_bit_cast(uint32_t, x[i]) & a.keep) ^ a.flip);
+                    if constexpr (PACKED && DT == QMV_F32) {
+                        uint32_t of[3];
+                        split<3>(y, of);
+                        part[i][0] = own == 0 ? of[0] : (own == 1 ? of[1] : (own == 2 ? of[2] : 0u));
+                    } else {
+                        split<NQ>(y, part[i]);
+                    }
+                }
 #pragma unroll
                 for (int n = 0; n < NQ; ++n)
                     qf[s][n] = __builtin_bit_cast(bf16x8, make_uint4(uppers(part[0][n], part[1][n]), uppers(part[2][n], part[3][n]),
@@ -314,10 +336,13 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attend4_few_kernel(Atte
         fetch_k(id);
         fetch_v(id);
 
+        const uint32_t cut1 = own >= 1 ? 0xFFFF0000u : 0u, cut2 = own >= 2 ? 0xFFFF0000u : 0u;
         f32x4 o[E];
 #pragma unroll
         for (int e = 0; e < E; ++e) o[e] = f32x4{0.f, 0.f, 0.f, 0.f};
-        float m_run = -__builtin_inff(), l_run = 0.f;
+        // the largest product with a key so far, as far as the reference has
+        // moved; it times the scale; the sum
+        float m_run = -__builtin_inff(), base = 0.f, l_run = 0.f;
 
         for (int32_t p = p0 + (SOLO ? 0 : wave); p < p1; p += STEP) {
             const int32_t here = id;
@@ -342,6 +367,16 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attend4_few_kernel(Atte
             }
             fetch_k(id);
             if (here >= 0) {
+                if constexpr (PACKED && DT == QMV_F32) {
+                    // the sum of the parts' products, the same in all of them
+#pragma unroll
+                    for (int t = 0; t < 4; ++t)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float u = sc[t][i] + dpp_mov<0x128>(sc[t][i]);   // lanes 8 apart in a row of 16
+                            sc[t][i] = u + dpp_mov<0x124>(u);                      // 4 apart
+                        }
+                }
                 if (edge) {
                     // scores of what a column does not see, and values that none does: the
                     // memory behind a sequence's end may hold anything
@@ -352,7 +387,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attend4_few_kernel(Atte
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             const int32_t at = t0 + 16 * t + i;
-                            sc[t][i] = at >= see_lo && at < to ? sc[t][i] * a.scale_log2 : -__builtin_inff();
+                            sc[t][i] = at >= see_lo && at < to ? sc[t][i] : -__builtin_inff();
                             if (at < w.lo || at >= w.hi) {
                                 vs[t] = (vs[t] & ~(0xFFu << (8 * i))) | 127u << (8 * i);
                                 if constexpr (W == 2) vw[t][i / 2] &= i % 2 == 0 ? 0xFFFF0000u : 0xFFFFu;
@@ -362,9 +397,6 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attend4_few_kernel(Atte
                             }
                         }
                     }
-                } else {
-#pragma unroll
-                    for (int t = 0; t < 4; ++t) sc[t] *= a.scale_log2;
                 }
                 float mt = -__builtin_inff();
 #pragma unroll
@@ -372,25 +404,33 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attend4_few_kernel(Atte
 #pragma unroll
                     for (int i = 0; i < 4; ++i) mt = fmaxf(mt, sc[t][i]);
                 mt = max_quads(mt);
-                if (__any(mt > m_run + kMoveAt || (m_run == -__builtin_inff() && mt > m_run))) {
-                    const float m_new = mt > m_run + kMoveAt || m_run == -__builtin_inff() ? fmaxf(mt, m_run) : m_run;
-                    const float keep = m_new == m_run ? 1.f : __builtin_amdgcn_exp2f(m_run - m_new);
+                if (__any(mt > m_run + a.move || (m_run == -__builtin_inff() && mt > m_run))) {
+                    const float m_new = mt > m_run + a.move || m_run == -__builtin_inff() ? fmaxf(mt, m_run) : m_run;
+                    // (a column that has seen nothing yet: e^-inf, not inf - inf)
+                    const float base_new = m_new > -__builtin_inff() ? m_new * a.scale_log2 : 0.f;
+                    const float keep = m_run > -__builtin_inff() ? __builtin_amdgcn_exp2f(base - base_new) : 1.f;
                     m_run = m_new;
+                    base = base_new;
                     l_run *= keep;
 #pragma unroll
                     for (int e = 0; e < E; ++e) o[e] *= keep;
                 }
-                // (a column that has seen nothing yet: e^-inf, not inf - inf)
-                const float base = m_run > -__builtin_inff() ? m_run : 0.f;
                 uint32_t pp[4][4][NP];
                 float l = 0.f;
 #pragma unroll
                 for (int t = 0; t < 4; ++t)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const float x = __builtin_amdgcn_exp2f(sc[t][i] - base);
+                        const float x = __builtin_amdgcn_exp2f(fmaf(sc[t][i], a.scale_log2, -base));
                         l += x;
-                        split<NP>(x, pp[t][i]);
+                        if constexpr (PACKED) {
+                            // what is left of x before the lane's part: its upper half is the part
+                            float y = x - __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, x) & cut1);
+                            if constexpr (DT == QMV_F32) y -= __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, y) & cut2);
+                            pp[t][i][0] = __builtin_bit_cast(uint32_t, y);
+                        } else {
+                            split<NP>(x, pp[t][i]);
+                        }
                     }
                 l_run += l;
                 // outputs: two steps of 32 tokens
@@ -430,7 +470,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attend4_few_kernel(Atte
         const uint64_t piece_row = w0.first + static_cast<uint64_t>(w0.piece) * static_cast<uint32_t>(r.count);
         if constexpr (SOLO) {
             if (w.row >= 0) {
-                const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
+                const float inv = m_run == -__builtin_inff() && l_run == 0.f ? 0.f : 1.f / l_run;
                 T* op = static_cast<T*>(a.out) + (static_cast<uint64_t>(r.first + w.row) * a.heads + w.head) * D;
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
@@ -453,14 +493,14 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attend4_few_kernel(Atte
 #pragma unroll
                 for (int e = 0; e < E; ++e) acc[wave][col][E * (4 * quad + i) + e] = o[e][i];
             if (quad == 0) {
-                stat[wave][col][0] = m_run;
+                stat[wave][col][0] = m_run > -__builtin_inff() ? base : -__builtin_inff();
                 stat[wave][col][1] = l_run;
             }
             __syncthreads();
             // thread: a column, and a sixteenth of its channels
             const int c = threadIdx.x >> 4, part = threadIdx.x & 15;
-            const uint32_t at = tile * 16 + c;
-            if (at < all) {
+            const uint32_t at = tile * kCols + c;
+            if (static_cast<uint32_t>(c) < kCols && at < all) {
                 float m = stat[0][c][0];
 #pragma unroll
                 for (int k = 1; k < 4; ++k) m = fmaxf(m, stat[k][c][0]);
@@ -472,7 +512,8 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attend4_few_kernel(Atte
                     l = fmaf(f[k], stat[k][c][1], l);
                 }
                 const uint32_t row = at / a.group, head = kvh * a.group + at % a.group;
-                const float inv = w0.pieces > 1 ? 1.f : (l == 0.f ? 0.f : 1.f / l);
+                // (nothing seen: 0; a sum of 0 past float32's range: no number)
+                const float inv = w0.pieces > 1 ? 1.f : (m == -__builtin_inff() && l == 0.f ? 0.f : 1.f / l);
                 const uint64_t slot = (piece_row + row) * a.heads + head;
                 if (w0.pieces > 1 && part == 0) a.stat[slot] = make_float2(m, l);
 #pragma unroll
@@ -480,7 +521,15 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attend4_few_kernel(Atte
                     const int ch = part + 16 * e;
                     float v = 0.f;
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) v = fmaf(f[k], acc[k][c][ch], v);
+                    for (int k = 0; k < 4; ++k) {
+                        float x = acc[k][c][ch];
+                        if constexpr (PACKED) {
+                            x = acc[k][c + (PARTS - 1) * kCols][ch];
+#pragma unroll
+                            for (int b = PARTS - 2; b >= 0; --b) x += acc[k][c + b * kCols][ch];
+                        }
+                        v = fmaf(f[k], x, v);
+                    }
                     v *= inv;
                     if (w0.pieces > 1) {
                         a.part[slot * D + ch] = v;
@@ -572,7 +621,7 @@ __global__ __launch_bounds__(Many<D>::kThreads, 2) void attend4_many_kernel(Atte
     const Span sp = span_of(a, r);
     const int32_t per = (sp.hi - sp.lo + static_cast<int32_t>(w0.pieces) - 1) / static_cast<int32_t>(w0.pieces);
     const int32_t b0 = min(sp.lo + static_cast<int32_t>(w0.piece) * per, sp.hi), b1 = min(b0 + per, sp.hi);
-    const float fm = fabsf(a.scale_log2);         // (a negative scale's sign is in the queries)
+    const float fm = a.scale_log2;
     // the last tiles see the most: they begin first
     for (uint32_t turn = blockIdx.y; turn < tiles; turn += gridDim.y) {
         const uint32_t tile = tiles - 1 - turn;
@@ -589,12 +638,12 @@ __global__ __launch_bounds__(Many<D>::kThreads, 2) void attend4_many_kernel(Atte
         bf16x8 qf[QS];
         {
             const uint16_t* qp = static_cast<const uint16_t*>(a.q) + (static_cast<uint64_t>(r.first + max(w.row, 0)) * a.heads + w.head) * D + kBlock * half;
-            const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;
+            const uint32_t flip = a.flip | a.flip >> 16;
 #pragma unroll
             for (int s = 0; s < QS; ++s) {
                 uint4 u = make_uint4(0, 0, 0, 0);
                 if (w.row >= 0) u = *reinterpret_cast<const uint4*>(qp + 2 * kBlock * (s / 4) + 8 * (s % 4));
-                qf[s] = __builtin_bit_cast(bf16x8, make_uint4(u.x ^ flip, u.y ^ flip, u.z ^ flip, u.w ^ flip));
+                qf[s] = __builtin_bit_cast(bf16x8, make_uint4((u.x & a.keep) ^ flip, (u.y & a.keep) ^ flip, (u.z & a.keep) ^ flip, (u.w & a.keep) ^ flip));
             }
         }
 
@@ -979,19 +1028,33 @@ __global__ __launch_bounds__(Many<D>::kThreads, 2) void attend4_many_kernel(Atte
 
 // Joins the pieces of each column of a sequence that was cut: a wave has a
 // column, lane z piece z's maximum and sum, and the pieces' outputs are added
-// in their order, D / 64 values a lane.
-template <uint32_t DT, int D>
+// in their order, D / 64 values a lane.  SPREAD: the four waves of a workgroup
+// have a column, each every fourth piece (columns are few and have many).
+template <uint32_t DT, int D, bool SPREAD>
 __global__ __launch_bounds__(256) void attend4_join_kernel(Attend4Args a) {
     constexpr int V = D / 64;
+    constexpr uint32_t STEP = SPREAD ? 4 : 1, AT_ONCE = 8;
+    __shared__ float acc[SPREAD ? 4 : 1][SPREAD ? D : 1];
     const int lane = threadIdx.x & 63;
     const uint32_t wave = static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6)));
     const Piece w = find_piece(a, blockIdx.x, true);
     if (w.seq < 0 || w.pieces <= 1) return;
     const SeqRows r = seq_rows(a.s, static_cast<uint32_t>(w.seq));
     const uint64_t n = static_cast<uint64_t>(r.count) * a.heads;
-    for (uint64_t i = static_cast<uint64_t>(blockIdx.y) * 4 + wave; i < n; i += static_cast<uint64_t>(gridDim.y) * 4) {
+    constexpr uint32_t kOwn = SPREAD ? 1 : 4;     // columns of a workgroup
+    for (uint64_t i = static_cast<uint64_t>(blockIdx.y) * kOwn + (SPREAD ? 0 : wave); i < n; i += static_cast<uint64_t>(gridDim.y) * kOwn) {
         // (a piece's rows and heads are as those of the output)
         const uint64_t from = static_cast<uint64_t>(w.first) * a.heads + i;
+        float x[AT_ONCE][V];
+        auto load = [&](uint32_t z) {
+#pragma unroll
+            for (uint32_t u = 0; u < AT_ONCE; ++u)
+#pragma unroll
+                for (int k = 0; k < V; ++k)
+                    x[u][k] = z + u * STEP < w.pieces ? a.part[(from + (z + u * STEP) * n) * D + lane * V + k] : 0.f;
+        };
+        const uint32_t z0 = SPREAD ? wave : 0;
+        load(z0);
         float2 st = make_float2(-__builtin_inff(), 0.f);
         if (static_cast<uint32_t>(lane) < w.pieces) st = a.stat[from + lane * n];
         float m = st.x;
@@ -1004,25 +1067,35 @@ __global__ __launch_bounds__(256) void attend4_join_kernel(Attend4Args a) {
         float v[V];
 #pragma unroll
         for (int k = 0; k < V; ++k) v[k] = 0.f;
-        for (uint32_t z = 0; z < w.pieces; z += 8) {
-            float x[8][V];
+        for (uint32_t z = z0; z < w.pieces; z += AT_ONCE * STEP) {
+            if (z != z0) load(z);
 #pragma unroll
-            for (int u = 0; u < 8; ++u)
-#pragma unroll
-                for (int k = 0; k < V; ++k) x[u][k] = z + u < w.pieces ? a.part[(from + (z + u) * n) * D + lane * V + k] : 0.f;
-#pragma unroll
-            for (int u = 0; u < 8; ++u) {
-                const float g = z + u < w.pieces ? read_lane(f, static_cast<int>(z + u)) : 0.f;
+            for (uint32_t u = 0; u < AT_ONCE; ++u) {
+                const float g = z + u * STEP < w.pieces ? read_lane(f, static_cast<int>(z + u * STEP)) : 0.f;
 #pragma unroll
                 for (int k = 0; k < V; ++k) v[k] = fmaf(g, x[u][k], v[k]);
             }
         }
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        const uint64_t to = (static_cast<uint64_t>(r.first) * a.heads + i) * D + lane * V;
+        // (nothing seen: 0; a sum of 0 past float32's range: no number)
+        const float inv = m == -__builtin_inff() && l == 0.f ? 0.f : 1.f / l;
+        if constexpr (SPREAD) {
 #pragma unroll
-        for (int k = 0; k < V; ++k) {
-            if constexpr (DT == QMV_F32) static_cast<float*>(a.out)[to + k] = v[k] * inv;
-            else static_cast<__bf16*>(a.out)[to + k] = static_cast<__bf16>(v[k] * inv);
+            for (int k = 0; k < V; ++k) acc[wave][lane * V + k] = v[k];
+            __syncthreads();
+            const uint64_t to = (static_cast<uint64_t>(r.first) * a.heads + i) * D + threadIdx.x;
+            if (threadIdx.x < D) {
+                const float y = ((acc[0][threadIdx.x] + acc[1][threadIdx.x]) + (acc[2][threadIdx.x] + acc[3][threadIdx.x])) * inv;
+                if constexpr (DT == QMV_F32) static_cast<float*>(a.out)[to] = y;
+                else static_cast<__bf16*>(a.out)[to] = static_cast<__bf16>(y);
+            }
+            __syncthreads();
+        } else {
+            const uint64_t to = (static_cast<uint64_t>(r.first) * a.heads + i) * D + lane * V;
+#pragma unroll
+            for (int k = 0; k < V; ++k) {
+                if constexpr (DT == QMV_F32) static_cast<float*>(a.out)[to + k] = v[k] * inv;
+                else static_cast<__bf16*>(a.out)[to + k] = static_cast<__bf16>(v[k] * inv);
+            }
         }
     }
 }
@@ -1034,15 +1107,13 @@ uint64_t span_pages(const qmv_kv_seqs& s, uint32_t window, uint64_t rows) {
     return (span + kPage - 1) / kPage + 1;
 }
 
-// How a call is dealt out: few queries with the waves of a workgroup sharing the
-// pages, or each with its own columns, or many.
-enum Kind { kShared, kSolo, kMany };
 struct Plan {
     Kind kind;
     uint32_t tiles, target, least, slots;
     uint64_t room;
 };
 constexpr uint32_t kWorkgroups = 512;          // that a launch of the kernel for few aims at
+constexpr uint64_t kSpreadCols = 512;          // columns of a call up to which a workgroup joins one
 constexpr uint32_t kWhole = 16;                // pages up to which a sequence is not cut
 // bfloat16 queries go to the kernel for many where a sequence has columns enough
 // for its tiles (kManyCols / D) and the call work enough (products of 16 columns
@@ -1072,7 +1143,8 @@ Plan plan_of(const qmv_kv4_cache& c, const qmv_kv_seqs& s, uint32_t dtype, uint3
     const uint64_t wide = p.kind == kMany ? 128 : 16;
     uint64_t tiles = (cols + wide - 1) / wide;
     const uint64_t wgs = uint64_t{s.seqs} * c.kv_heads * tiles;
-    if (p.kind != kMany && wgs >= 1024) {
+    if (p.kind != kMany && cols <= (dtype == QMV_F32 ? kPackedCols<QMV_F32> : kPackedCols<QMV_BF16>)) p.kind = kPacked;
+    else if (p.kind != kMany && wgs >= 1024) {
         p.kind = kSolo;
         tiles = (tiles + 3) / 4;
     }
@@ -1109,15 +1181,19 @@ hipError_t go(const Attend4Args& a, const Plan& p, hipStream_t s) {
         }
     }
     if (done) {
-    } else if (p.kind == kSolo) hipLaunchKernelGGL((attend4_few_kernel<DT, D, true>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((attend4_few_kernel<DT, D, false>), grid, block, 0, s, a);
+    } else if (p.kind == kSolo) hipLaunchKernelGGL((attend4_few_kernel<DT, D, kSolo>), grid, block, 0, s, a);
+    else if (p.kind == kPacked) hipLaunchKernelGGL((attend4_few_kernel<DT, D, kPacked>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((attend4_few_kernel<DT, D, kShared>), grid, block, 0, s, a);
     hipError_t e = hipGetLastError();
     if (e == hipSuccess && p.target != 0) {
         const uint64_t most = a.s.max_new < a.s.rows ? a.s.max_new : a.s.rows;
-        uint64_t y = (most * a.heads + 3) / 4;
+        const bool spread = most * a.heads * a.s.seqs <= kSpreadCols;
+        uint64_t y = spread ? most * a.heads : (most * a.heads + 3) / 4;
         if (y < 1) y = 1;
         if (y > 65535) y = 65535;
-        hipLaunchKernelGGL((attend4_join_kernel<DT, D>), dim3(a.s.seqs, static_cast<uint32_t>(y)), block, 0, s, a);
+        const dim3 joins(a.s.seqs, static_cast<uint32_t>(y));
+        if (spread) hipLaunchKernelGGL((attend4_join_kernel<DT, D, true>), joins, block, 0, s, a);
+        else hipLaunchKernelGGL((attend4_join_kernel<DT, D, false>), joins, block, 0, s, a);
         e = hipGetLastError();
     }
     return e;
@@ -1139,7 +1215,10 @@ hipError_t launch_kv4_attend(const qmv_kv4_cache& c, const qmv_kv_seqs& s, uint3
                              const void* q, void* out, void* workspace, hipStream_t stream) {
     const Plan p = plan_of(c, s, dtype, heads, window);
     float* part = static_cast<float*>(workspace);
-    const Attend4Args a{c, s, q, out, part, reinterpret_cast<float2*>(part + p.room * heads * c.head_dim), scale * kLog2e, heads,
+    // (a scale of 0: queries of 0)
+    const float by = scale == 0.f ? 1.f : (scale < 0.f ? -scale : scale) * kLog2e;
+    const Attend4Args a{c, s, q, out, part, reinterpret_cast<float2*>(part + p.room * heads * c.head_dim), by, kMoveAt / by,
+                        scale == 0.f ? 0u : ~0u, scale < 0.f ? 0x80000000u : 0u, heads,
                         heads / c.kv_heads, window, p.target, p.least, static_cast<uint32_t>(p.room)};
     return dtype == QMV_F32 ? go<QMV_F32>(a, p, stream) : go<QMV_BF16>(a, p, stream);
 }
