@@ -26,8 +26,16 @@
 // Work: a workgroup of four waves has 16 columns (query row x head of one
 // key/value head) and a piece of the sequence's pages; each wave takes every
 // fourth page and keeps its own running maximum, sum and output, joined in
-// shared memory at the end.  Where there are columns enough, each wave has 16
-// of its own and all of their pages (SOLO).
+// shared memory at the end.  Where columns are few (PACKED), the parts of a
+// query and of a probability are columns of their own; where there are enough,
+// each wave has 16 and all of their pages (SOLO).
+//
+// Bound by memory for long contexts: 2 x 131072 bfloat16 (32 heads on 8 of 128,
+// 180 MB) 42.4 us, of which the join 5, the kernel 4.8 TB/s.  A decode step of 32
+// x 1000 to 4000 in float32 (91 MB) 30.1 us: vector instructions are issued in
+// half of the cycles (conversion, exponentials, parts), the rest is the first
+// trips to memory, uneven ends and the join (two pages on the way instead of
+// one: 35; nothing fetched behind a wave's last page: 31).
 #include "kv4_common.h"
 
 namespace qmv {
@@ -39,8 +47,9 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kMoveAt = 8.f;
 // How a call is dealt out: few queries to a key/value head, the waves of a
 // workgroup sharing the pages (packed: a tile's columns few enough that each
-// part of a probability has a column of its own) or each with its own columns;
-// or many.
+// part of a probability has a column of its own, so one product takes what two
+// or three took: 32 x 4000 float32 31.4 us, else 34.1) or each with its own
+// columns; or many.
 enum Kind { kShared, kPacked, kSolo, kMany };
 template <uint32_t DT>
 constexpr uint32_t kPackedCols = DT == QMV_F32 ? 4 : 8;
@@ -547,7 +556,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attend4_few_kernel(Atte
 
 // ---- many queries -----------------------------------------------------------
 
-// Many bfloat16 queries to a key/value head: a workgroup of eight waves has 32
+// Many bfloat16 queries to a key/value head: a workgroup of four waves has 32
 // columns a wave, and walks the pages together.  Values are made float16 once
 // for all, in shared memory; keys stay codes there, which each wave turns into
 // bfloat16 on the way to its products: an operand read from shared memory feeds
@@ -577,6 +586,17 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attend4_few_kernel(Atte
 // and w + 4 have the same 32.  Each scores half of a page's tokens, they
 // exchange maxima and probabilities through shared memory, and each adds up
 // half of the output channels.
+//
+// A page's products and exponentials are laid out so that a tile of 32 tokens'
+// products are beside the other's exponentials, and the next page's values are
+// staged beside the last of them: one barrier a page.  Two workgroups share a
+// compute unit (216 of 256 registers), so one's barrier is the other's work.
+//
+// A prompt of 8192 (32 heads on 8 of 128, 550 GFLOP) takes 567 us, 970 TFLOP/s, 71%
+// of what a large bfloat16 product reaches: the exponentials and the conversion
+// of codes are vector instructions, which share the issue with the products.
+// (Waves that read pages from memory themselves, few kernel: 874; eight waves and
+// three barriers: 721.)
 template <int D>
 struct Many {
     static constexpr bool kPair = D == 256;
@@ -1112,9 +1132,31 @@ struct Plan {
     uint32_t tiles, target, least, slots;
     uint64_t room;
 };
-constexpr uint32_t kWorkgroups = 512;          // that a launch of the kernel for few aims at
-constexpr uint64_t kSpreadCols = 512;          // columns of a call up to which a workgroup joins one
-constexpr uint32_t kWhole = 16;                // pages up to which a sequence is not cut
+// Workgroups that a launch of the kernel for few aims at (us with 512, 768 and
+// 1024: 32 x 4000 float32 30.1, 30.4 and 31.1; 2 x 131072 bfloat16 42.4, 44.8 and
+// 44.8).
+constexpr uint32_t kWorkgroups = 512;
+// Columns of a call up to which a workgroup, not a wave, joins one (us, workgroup
+// / wave: 64 columns of 32 pieces 38.5 / 41.1, 256 of 8 30.7 / 31.7, 1024 of 2
+// 31.0 / 30.1).
+constexpr uint64_t kSpreadCols = 512;
+// Pages up to which a sequence is not cut: a join is a launch, of 3 to 5 us; with
+// workgroups enough (kBusy) up to more (us, whole / cut, 8 heads of 128: 1 x 1000
+// 10.3 / 13.8, 32 x 1000 10.4 / 16.2, 1 x 2000 12.3 / 11.8, float32 14.6 / 12.8; 16
+// x 2000 12.6 / 15.5; 1 x 3000 16.0 / 11.6, 16 x 3000 17.3 / 18.6).
+constexpr uint32_t kWhole = 24, kWholeBusy = 34;
+constexpr uint64_t kBusy = 64;
+// In the kernel for many, whose workgroups walk pages faster, and the number that
+// a launch of it aims at, two a compute unit, or one in pairs of waves (us, 512 /
+// 256: 1 x 16000 with 128 rows 63 / 90, 4 x 8000 with 64 53 / 66, head dims of
+// 256, 2 x 16000 with 64 96 / 76); from kManyFull on a launch is not cut (16 x 4000
+// with 64 rows, 256 workgroups, cut 118, else 102).
+constexpr uint32_t kWholeMany = 16;
+constexpr uint64_t kManyAim = 512, kManyPairs = 256, kManyFull = 192;
+// Workgroups from which each wave has its own columns (us, own / shared: 64 x
+// 1000 with 32 and 64 columns 30 / 33 and 35 / 53, 1024 and 2048 workgroups; at
+// 512, 8 x 3000 with 128 51 / 36, 16 x 1000 with 64 22 / 26).
+constexpr uint64_t kSoloFrom = 1024;
 // bfloat16 queries go to the kernel for many where a sequence has columns enough
 // for its tiles (kManyCols / D) and the call work enough (products of 16 columns
 // with a page, times D) that its waves' waiting for each other is paid for.
@@ -1144,14 +1186,15 @@ Plan plan_of(const qmv_kv4_cache& c, const qmv_kv_seqs& s, uint32_t dtype, uint3
     uint64_t tiles = (cols + wide - 1) / wide;
     const uint64_t wgs = uint64_t{s.seqs} * c.kv_heads * tiles;
     if (p.kind != kMany && cols <= (dtype == QMV_F32 ? kPackedCols<QMV_F32> : kPackedCols<QMV_BF16>)) p.kind = kPacked;
-    else if (p.kind != kMany && wgs >= 1024) {
+    else if (p.kind != kMany && wgs >= kSoloFrom) {
         p.kind = kSolo;
         tiles = (tiles + 3) / 4;
     }
     p.tiles = static_cast<uint32_t>(tiles > 65535 ? 65535 : tiles);
     p.slots = s.seqs;
-    if (p.kind == kSolo || s.seqs > kScanSeqs || pages <= kWhole || (p.kind == kMany && wgs >= 192)) return p;
-    const uint64_t aim = p.kind == kMany ? 256 : kWorkgroups;
+    const uint64_t whole = p.kind == kMany ? kWholeMany : (wgs >= kBusy ? kWholeBusy : kWhole);
+    if (p.kind == kSolo || s.seqs > kScanSeqs || pages <= whole || (p.kind == kMany && wgs >= kManyFull)) return p;
+    const uint64_t aim = p.kind == kMany ? (c.head_dim == 256 ? kManyPairs : kManyAim) : kWorkgroups;
     uint64_t target = (aim + c.kv_heads * tiles - 1) / (c.kv_heads * tiles);
     if (target < s.seqs / 2) target = s.seqs / 2;
     if (target < 1) target = 1;
