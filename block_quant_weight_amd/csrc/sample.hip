@@ -7,7 +7,7 @@
 // so that a weight is right to about one rounding also far below the largest.
 //
 // The tokens that stay are a prefix in the order of the logits, and nearly
-// always a short one.  Three kernels:
+// always a short one.  Three kernels (of few rows the first is part of the second):
 //   bound  reads 2048 logits of a row and sets a bound above which some hundreds
 //          or thousands of its tokens lie;
 //   scan   reads every logit once: a wave has 1024, of which it hands on the
@@ -25,8 +25,9 @@
 // top-p sums to it, each by three histograms over 11, 11 and 10 bits of the key,
 // and the draw is a running sum over the indexes.
 //
-// One row of 248320 takes 16.8 us (3.7 + 4.0 + 9.3 by kernel: launches and trips
-// to memory, and in the last the fetching of its instructions), 64 rows (64 MB)
+// One row of 248320 takes 15.4 us (6 in a scan that finds the bound itself, 9 in the
+// last kernel: launches and trips to memory, and the fetching of its instructions),
+// 64 rows (64 MB)
 // 34.6 (scan 14 to 16, 4.5 TB/s; the last 14, a workgroup a row on 64 of 256
 // compute units); a row over the whole of which one workgroup goes about 0.4 ms.
 #include "device_common.h"
@@ -377,6 +378,10 @@ constexpr uint32_t kShort = 2048;
 constexpr uint32_t kGather = 512;          // of a histogram's bin
 constexpr uint32_t kSamples = 2048, kMost = 4;   // read of a row; of kMost the largest counts
 constexpr uint32_t kAhead = 256 * 16 / kThreads;
+// Rows up to which each workgroup of the scan finds the row's bound itself, which
+// saves a launch and costs reads of 32 KB a workgroup (us, itself / a kernel, 248320:
+// 1 row 16.0 / 16.9, 8 18.3 / 18.6, 16 21.9 / 21.3, 64 43 / 36).
+constexpr uint32_t kOwnRows = 8;
 constexpr uint32_t kOver = 0x80000000u;    // more likely tokens than kKept
 
 struct __attribute__((packed, aligned(4))) Four {
@@ -409,68 +414,78 @@ __device__ __forceinline__ bool drawable(const Wish& w) { return w.t >= 0.f && w
 // 2048 of them, 512 times four beside each other: the r-th largest of the fours'
 // largest (its upper 16 bits, rounded down).  Of a row of 248320, r = 6 are about 730 tokens:
 // at least 40 of them but for 2 rows in a million.
-// Four waves read, one finds the bound, another the row's numbers.
-__global__ __launch_bounds__(256) void sample_bound_kernel(SampleArgs a, Work k) {
-    constexpr int kEach = kSamples / kMost / 64;
-    __shared__ uint32_t keys[kSamples / kMost];
+// Four waves read, one finds the bound, another the row's numbers; *to holds
+// them after the next barrier.
+constexpr uint32_t kKeys = kSamples / kMost;
+__device__ __forceinline__ void find_bound(const SampleArgs& a, uint64_t row, uint32_t* keys, Row* to) {
+    constexpr int kEach = kKeys / 64;
     const uint32_t tid = threadIdx.x, lane = tid & 63;
     const int wave = this_wave();
+    const float* x = a.logits + row * a.vocab;
+    Four v[kKeys / 256];
+#pragma unroll
+    for (uint32_t i = 0; i < kKeys / 256; ++i)
+        v[i] = *reinterpret_cast<const Four*>(x + (static_cast<uint64_t>(i * 256 + tid) * (a.vocab - 3)) / kKeys);
+    const Wish w = wish_of(a, row);
+#pragma unroll
+    for (uint32_t i = 0; i < kKeys / 256; ++i) {
+        uint32_t key = 0;
+#pragma unroll
+        for (uint32_t j = 0; j < kMost; ++j) key = max(key, key_of(v[i].v[j]) >> 16);
+        keys[i * 256 + tid] = key;
+    }
+    __syncthreads();
+    if (wave == 0) {
+        uint32_t key[kEach];
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) key[i] = keys[64 * i + lane];
+        const uint64_t some = w.t == 0.f ? 1 : (w.k != 0 ? 6ull * w.k + 500 : 2500);
+        const uint32_t least = w.t == 0.f ? 1 : 5;
+        // (half of the fours at most: about 160 tokens of a wave's 1024, of which it can hand on 256)
+        const uint32_t r = min(max(static_cast<uint32_t>(some * kSamples / a.vocab), least), kKeys / 2);
+        uint32_t bound = 0;
+#pragma unroll
+        for (int b = 15; b >= 0; --b) {
+            const uint32_t at = bound | 1u << b;
+            uint32_t n = 0;
+#pragma unroll
+            for (int i = 0; i < kEach; ++i) n += static_cast<uint32_t>(__popcll(__ballot(key[i] >= at)));
+            if (n >= r) bound = at;
+        }
+        const uint32_t bits = bound << 16;
+        // (rounded down, -infinity is no number: all that is finite is listed then)
+        float low = __builtin_bit_cast(float, bits & 0x80000000u ? bits & 0x7FFFFFFFu : ~bits);
+        if (!(low > -3.4028235e38f)) low = -3.4028235e38f;
+        if (lane == 0) to->bound = wants_list(w) && drawable(w) ? low : __builtin_inff();
+    } else if (wave == 1) {
+        const Weigher g = weigher_of(0.f, w.t == 0.f ? 1.f : w.t);
+        const Floor f = floor_of(w.m);
+        if (lane == 0) {
+            to->c = g.c;
+            to->c_low = g.c_low;
+            to->floor_hi = f.hi;
+            to->floor_lo = f.lo;
+        }
+    }
+}
+__global__ __launch_bounds__(256) void sample_bound_kernel(SampleArgs a, Work k) {
+    __shared__ uint32_t keys[kKeys];
     for (uint64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
-        const float* x = a.logits + row * a.vocab;
-        Four v[kSamples / kMost / 256];
-#pragma unroll
-        for (uint32_t i = 0; i < kSamples / kMost / 256; ++i)
-            v[i] = *reinterpret_cast<const Four*>(x + (static_cast<uint64_t>(i * 256 + tid) * (a.vocab - 3)) / (kSamples / kMost));
-        const Wish w = wish_of(a, row);
-#pragma unroll
-        for (uint32_t i = 0; i < kSamples / kMost / 256; ++i) {
-            uint32_t key = 0;
-#pragma unroll
-            for (uint32_t j = 0; j < kMost; ++j) key = max(key, key_of(v[i].v[j]) >> 16);
-            keys[i * 256 + tid] = key;
-        }
-        __syncthreads();
-        if (wave == 0) {
-            uint32_t key[kEach];
-#pragma unroll
-            for (int i = 0; i < kEach; ++i) key[i] = keys[64 * i + lane];
-            const uint64_t some = w.t == 0.f ? 1 : (w.k != 0 ? 6ull * w.k + 500 : 2500);
-            const uint32_t least = w.t == 0.f ? 1 : 5;
-            const uint32_t r = min(max(static_cast<uint32_t>(some * kSamples / a.vocab), least), kSamples / kMost);
-            uint32_t bound = 0;
-#pragma unroll
-            for (int b = 15; b >= 0; --b) {
-                const uint32_t at = bound | 1u << b;
-                uint32_t n = 0;
-#pragma unroll
-                for (int i = 0; i < kEach; ++i) n += static_cast<uint32_t>(__popcll(__ballot(key[i] >= at)));
-                if (n >= r) bound = at;
-            }
-            const uint32_t bits = bound << 16;
-            // (rounded down, -infinity is no number: all that is finite is listed then)
-            float low = __builtin_bit_cast(float, bits & 0x80000000u ? bits & 0x7FFFFFFFu : ~bits);
-            if (!(low > -3.4028235e38f)) low = -3.4028235e38f;
-            if (lane == 0) k.rows[row].bound = wants_list(w) && drawable(w) ? low : __builtin_inff();
-        } else if (wave == 1) {
-            const Weigher g = weigher_of(0.f, w.t == 0.f ? 1.f : w.t);
-            const Floor f = floor_of(w.m);
-            if (lane == 0) {
-                Row& to = k.rows[row];
-                to.c = g.c;
-                to.c_low = g.c_low;
-                to.floor_hi = f.hi;
-                to.floor_lo = f.lo;
-            }
-        }
+        find_bound(a, row, keys, k.rows + row);
         __syncthreads();
     }
 }
 
-// Reads every logit once: a wave has 1024, 16 a lane.
+// Reads every logit once: a wave has 1024, 16 a lane.  OWN: each workgroup finds
+// the row's bound for itself, while its logits are on their way.
+template <bool OWN>
 __global__ __launch_bounds__(256) void sample_scan_kernel(SampleArgs a, Work k) {
+    __shared__ uint32_t keys[OWN ? kKeys : 1];
+    __shared__ Row own;
     const uint32_t lane = threadIdx.x & 63;
     const uint32_t chunk = blockIdx.x * 4 + static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6)));
-    if (chunk >= k.chunks) return;
+    const bool has = chunk < k.chunks;
+    if (!OWN && !has) return;
     const uint32_t from = chunk * kChunk;
     for (uint64_t row = blockIdx.y; row < a.rows; row += gridDim.y) {
         const float* p = a.logits + row * a.vocab + from;
@@ -492,7 +507,15 @@ __global__ __launch_bounds__(256) void sample_scan_kernel(SampleArgs a, Work k) 
                 }
         }
         const Wish w = wish_of(a, row);
-        const Row of = k.rows[row];
+        Row of;
+        if constexpr (OWN) {
+            find_bound(a, row, keys, &own);
+            __syncthreads();
+            of = own;
+            if (blockIdx.x == 0 && threadIdx.x == 0) k.rows[row] = own;
+        } else {
+            of = k.rows[row];
+        }
         const float bound = of.bound;
         float m = -__builtin_inff();
         bool bad = false;
@@ -545,7 +568,8 @@ __global__ __launch_bounds__(256) void sample_scan_kernel(SampleArgs a, Work k) 
                 n += all;
             }
         }
-        if (lane == 0) k.records[slot] = Record{m, sum, n <= kKept ? n : kOver, 0};
+        if (has && lane == 0) k.records[slot] = Record{m, sum, n <= kKept ? n : kOver, 0};
+        if constexpr (OWN) __syncthreads();      // (keys and own are written again)
     }
 }
 
@@ -959,10 +983,16 @@ hipError_t launch_sample(const SampleArgs& a, void* workspace, hipStream_t strea
     k.records = static_cast<Record*>(workspace);
     k.lists = reinterpret_cast<float2*>(k.records + slots);
     k.rows = reinterpret_cast<Row*>(k.lists + slots * kKept);
-    hipLaunchKernelGGL(sample_bound_kernel, dim3(grid), dim3(256), 0, stream, a, k);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(sample_scan_kernel, dim3((k.chunks + 3) / 4, a.rows < 65535 ? a.rows : 65535), dim3(256), 0, stream, a, k);
+    const dim3 scan((k.chunks + 3) / 4, a.rows < 65535 ? a.rows : 65535);
+    hipError_t e = hipSuccess;
+    if (a.rows <= kOwnRows) {
+        hipLaunchKernelGGL(sample_scan_kernel<true>, scan, dim3(256), 0, stream, a, k);
+    } else {
+        hipLaunchKernelGGL(sample_bound_kernel, dim3(grid), dim3(256), 0, stream, a, k);
+        e = hipGetLastError();
+        if (e != hipSuccess) return e;
+        hipLaunchKernelGGL(sample_scan_kernel<false>, scan, dim3(256), 0, stream, a, k);
+    }
     e = hipGetLastError();
     return e != hipSuccess ? e : pick<kList, false>(a, k, grid, stream);
 }
