@@ -118,11 +118,6 @@ struct Piece {
     uint32_t piece, pieces;
     uint32_t first;
 };
-__device__ __forceinline__ uint32_t wave_sum_u32(uint32_t v) {
-#pragma unroll
-    for (int m = 1; m < 64; m <<= 1) v += static_cast<uint32_t>(__shfl_xor(static_cast<int>(v), m));
-    return v;
-}
 // Piece `slot` in the order of the sequences; with by_seq, piece 0 of sequence
 // `slot`.  All lanes of a wave call it together.
 __device__ __forceinline__ Piece find_piece(const Attend4Args& a, uint32_t slot, bool by_seq) {

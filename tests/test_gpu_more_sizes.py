@@ -1,6 +1,6 @@
-"""Sizes past what a launch's grid holds at once, where workgroups go round:
-each against the same rows in calls of their own, which other tests hold against
-their references."""
+"""Sizes past what a launch's grid holds at once, where workgroups go round, and
+calls beside each other: each against the same rows in calls of their own, which
+other tests hold against their references."""
 import numpy as np
 import pytest
 
@@ -153,3 +153,37 @@ def test_sample_long_rows():
         n = 4
         check(logits(g, n, vocab), g.random(n).astype(np.float32), t=np.array([0.0, 0.7, 1.0, 1.0], dtype=np.float32),
               k=np.array([0, 40, 0, 0]), p=np.array([1.0, 0.9, 0.3, 1.0], dtype=np.float32), m=np.array([0.0, 0.0, 0.01, 0.0], dtype=np.float32))
+
+
+def test_two_draws_and_two_rotations_at_once():
+    """On two streams, a workspace each, over and over: the same bits as alone."""
+    import torch
+    g = generator(8)
+    x = [torch.randn(r, v, generator=g, device="cuda") * 3 for r, v in ((5, 60000), (70, 20001))]
+    u = [torch.rand(len(a), generator=g, device="cuda") for a in x]
+    p = [torch.full((len(a),), 0.8, device="cuda") for a in x]
+    q = [torch.randn(n, 6, 96, generator=g, device="cuda") for n in (3, 900)]
+    pos = [torch.arange(len(a), device="cuda", dtype=torch.int32) for a in q]
+    freq = torch.rand(24, generator=g, device="cuda")
+    ws = [S.workspace(S.qmv_sample_workspace(*a.shape)) for a in x]
+
+    def run(i, ids, lp, out, stream):
+        S.qmv_sample(x[i], u[i], ids, top_p=p[i], lp=lp, workspace=ws[i], stream=stream)
+        S.qmv_qk_rotate(q[i], None, pos[i], freq, out, None, neighbours=i == 1, stream=stream)
+
+    def outs(i):
+        return torch.full((len(x[i]),), -5, dtype=torch.int32, device="cuda"), torch.empty(len(x[i]), device="cuda"), torch.empty_like(q[i])
+    want = [outs(i) for i in range(2)]
+    for i in range(2):
+        run(i, *want[i], None)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[outs(i) for _ in range(20)] for i in range(2)]
+    torch.cuda.synchronize()
+    for turn in range(20):
+        for i in range(2):
+            run(i, *got[i][turn], streams[i])
+    torch.cuda.synchronize()
+    for i in range(2):
+        for o in got[i]:
+            assert all(torch.equal(a, b) for a, b in zip(o, want[i]))
