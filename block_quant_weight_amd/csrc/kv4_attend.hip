@@ -575,7 +575,12 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attend4_few_kernel(Atte
 // bits, and below 2^-27 they count as 0.  A page's values are times 2^-unit,
 // with a unit 4 above its largest exponent that stays while pages' largest are
 // within 10 below and 13 above it, so blocks down to 2^-13 of a page's largest
-// are exact whatever came before.
+// are exact whatever came before.  Blocks of zeros (all that tokens which are no
+// number have, too) carry the least exponent there is: they do not lower the
+// unit.  Nor does it fall further than kFar below the highest so far: outputs
+// are multiplied by what it falls, and a page's are below 2^32 (probabilities
+// of a column sum to less than 2^16, values are below 2^16 units), those of 2^25
+// pages below 2^57: 2^64 times that is a float32.
 //
 // Head dims of 256 hold too many registers for a wave of 32 columns: waves w
 // and w + 4 have the same 32.  Each scores half of a page's tokens, they
@@ -604,7 +609,7 @@ struct Many {
 constexpr float kSumLimit = 0x1p15f;       // of a page's probabilities in a lane
 constexpr float kBias = 2.f;               // log2 of a probability at the reference
 constexpr float kMoveManyAt = 4.f;
-constexpr int32_t kNoUnit = -1000;
+constexpr int32_t kNoUnit = -1000, kFar = 64;
 
 template <int D>
 __global__ __launch_bounds__(Many<D>::kThreads, 2) void attend4_many_kernel(Attend4Args a) {
@@ -715,7 +720,7 @@ __global__ __launch_bounds__(Many<D>::kThreads, 2) void attend4_many_kernel(Atte
         };
         // The unit's exponent (biased) of the page staged, and of the outputs.  What the waves tell each other of a page
         // ahead: 1: its largest exponent is too high for the unit so far, 2: high enough, and the largest byte above.
-        int32_t want = kNoUnit, unit = kNoUnit;
+        int32_t want = kNoUnit, unit = kNoUnit, highest = kNoUnit;
         auto tell = [&](int32_t p) {
             if (!has_v) return;                  // (a whole wave: it says nothing)
             const uint32_t v = visible(p, vs_next), m = max(max(v & 0xFFu, v >> 8 & 0xFFu), max(v >> 16 & 0xFFu, v >> 24));
@@ -730,7 +735,9 @@ __global__ __launch_bounds__(Many<D>::kThreads, 2) void attend4_many_kernel(Atte
             if ((some & 1) == 0) return;
             const int32_t m = __builtin_amdgcn_readfirstlane(static_cast<int>(max(max(max(u.x, u.y), max(u.z, u.w)), max(max(v.x, v.y), max(v.z, v.w))) >> 8));
             // (0: nothing is seen; some waves may have exponents high enough where others have none)
-            if (m != 0 && (want == kNoUnit || m > want + 13 || ((some & 2) == 0 && m < want - 10))) want = m + 4;
+            const bool fall = (some & 2) == 0 && m < want - 10 && m > static_cast<int32_t>(kByteMin);
+            if (m != 0 && (want == kNoUnit || m > want + 13 || fall)) want = max(m + 4, highest - kFar);
+            highest = max(highest, want);
         };
         // Into shared memory.  Rows of 16-byte chunks, permuted so that reads meet in no bank.
         constexpr int kKeyRow = D / 2;

@@ -263,12 +263,14 @@ int qmv_kv4_read(const qmv_kv4_cache *cache, const qmv_kv_seqs *seqs, uint32_t d
  * positions, window and zero rows.  Scores, the softmax's statistics and the
  * output sums are float32.  Queries enter the products exactly; probabilities
  * exactly with float32, with 16 bits or, where bfloat16 queries are many (as
- * there), 11 bits, those below 2^-27 of the largest as 0; then values of blocks
- * whose scale is below 2^-13 of their page's and head's largest scale are off by
- * up to 2^-15 of that scale.  A query, or a token and head that is seen, with a NaN or infinity
- * gives NaN for the rows that see it and touches no other.  Scores past
- * float32's range may give NaN; values below 2^62 in magnitude never leave it.
- * Values below 2^-96 may lose low bits or count as 0.
+ * there), 11 bits (fewer below 2^-16 of the largest, those below 2^-27 as 0);
+ * then values of blocks whose scale is below 2^-13 of their page's and head's
+ * largest scale are off by up to 2^-15 of that scale, and values below 2^-80 of
+ * the largest of their sequence and head may count as 0.  A query, or a token
+ * and head that is seen, with a NaN or infinity gives NaN for the rows that see
+ * it and touches no other.  Scores past float32's range may give NaN; values
+ * below 2^62 in magnitude never leave it.  Values below 2^-96 may lose low bits
+ * or count as 0.
  * A sequence's pages are cut into pieces by its own length beside the others',
  * so one long sequence among short ones uses the whole GPU; max_new and max_len
  * only choose the kernel and how many pieces there are in all.
