@@ -745,7 +745,8 @@ __global__ __launch_bounds__(kThreads) void sample_pick_kernel(SampleArgs a, Wor
             uint64_t mine = 0;
             if (wants_sum(w) && r.max > -__builtin_inff()) {
                 const float2 t = g.log2_of(r.max);
-                if (t.x > -60.f) mine = static_cast<uint64_t>(static_cast<double>(r.sum * __builtin_amdgcn_exp2f(t.x) * (1.f + t.y * 0.6931471805599453f)) * 0x1p39);
+                // (tokens that each weigh nothing do not together either: none of them may be drawn)
+                if (g.weight_of(t) != 0) mine = static_cast<uint64_t>(static_cast<double>(r.sum * __builtin_amdgcn_exp2f(t.x) * (1.f + t.y * 0.6931471805599453f)) * 0x1p39);
             }
             const Sums of = scan2((Lds)s.sums[0], mine, r.count & ~kOver);
             all = of.a_all;
@@ -763,9 +764,9 @@ __global__ __launch_bounds__(kThreads) void sample_pick_kernel(SampleArgs a, Wor
                 const float v = at + 1 < a.vocab ? a.logits[row * a.vocab + at + 1] : -__builtin_inff();
                 const uint64_t q = g(u), q2 = g(v);
                 const Sums in = scan2((Lds)s.sums[1], q + q2, 0);
-                const uint64_t place = in.a_all == 0 ? 0 : min(want, in.a_all - 1);
-                if (in.a_all == 0 ? tid == 0 : (in.a_before <= place && place - in.a_before < q + q2)) {
-                    const bool second = in.a_all != 0 && place - in.a_before >= q;
+                const uint64_t place = min(want, in.a_all - 1);   // (its largest token weighs something)
+                if (in.a_before <= place && place - in.a_before < q + q2) {
+                    const bool second = place - in.a_before >= q;
                     answer(a, row, second ? at + 1 : at, second ? v : u, g, false, all);
                 }
                 continue;

@@ -1,0 +1,54 @@
+"""qmv_sample where the answer lies at an end of the running sum: rows whose
+first or last tokens each weigh nothing, though many of them together would."""
+import numpy as np
+import pytest
+
+import more_ref as M
+from test_gpu_sample import run
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    import torch
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    yield
+
+
+def whole_weights(x, t):
+    """Weights of a row as whole multiples of 2^-39 of the largest."""
+    return np.rint(np.exp((x.astype(np.float64) - x.max()) / t) * 2.0 ** 39)
+
+
+@pytest.mark.parametrize("below", [28.0, 28.5, 29.0])
+@pytest.mark.parametrize("t", [1.0, 0.7])
+@pytest.mark.parametrize("vocab", [3000, 9000, 50001, 248320])
+def test_tokens_that_weigh_nothing_are_not_drawn(vocab, t, below):
+    """u at its ends, and rows that begin and end with thousands of tokens at
+    2^-40.4 to 2^-41.8 of the largest, masked ones among them.  (Weights are
+    right to 2^-22 of themselves: none lies that near to half a unit.)"""
+    g = np.random.default_rng(vocab)
+    rows = 6
+    x = (2.0 * g.standard_normal((rows, vocab))).astype(np.float32)
+    top = x.max(-1) + 3
+    ends = vocab // 3 if vocab < 10000 else 4096
+    for i in range(rows):
+        x[i, vocab // 2] = top[i]
+        x[i, :ends] = x[i, -ends:] = top[i] - np.float32(below * t)
+        x[i, :ends - 1:2 + i] = x[i, -1::-97] = -np.inf
+        x[i, vocab // 2 + 1:vocab - ends:701] = -np.inf
+    u = np.array([0.0, 1.0, 0.0, 1.0, 1e-13, 0.99999994], dtype=np.float32)
+    ids, lp = run(x, u, t=np.full(rows, t))
+    for i in range(rows):
+        w = whole_weights(x[i], float(np.float32(t)))
+        there = np.nonzero(w)[0]
+        if u[i] == 0.0:
+            assert ids[i] == there[0]
+        elif u[i] == 1.0:
+            assert ids[i] == there[-1]
+        assert w[ids[i]] > 0
+        want = float(x[i, ids[i]] - np.float64(top[i])) / float(np.float32(t)) - np.log(w.sum() * 2.0 ** -39)
+        assert M.sample_ok([(ids[i], want)], ids[i], lp[i])
+    assert np.array_equal(run(x, u, t=np.full(rows, t), m=np.full(rows, 1e-20))[0][:4], ids[:4])
