@@ -320,7 +320,8 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attend4_few_kernel(Atte
                 uint32_t part[8][NQ];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const float y = __builtin_bit_cast(float, (__builtin_bit_cast(uint32_t, x[i]) & a.keep) ^ a.flip);
+                    // (+ 0 x: an infinite query, whose products need not all be NaN, is NaN, and with a scale of 0 one that is no number too)
+                    const float y = fmaf(x[i], 0.f, __builtin_bit_cast(float, (__builtin_bit_cast(uint32_t, x[i]) & a.keep) ^ a.flip));
                     if constexpr (PACKED && DT == QMV_F32) {
                         uint32_t of[3];
                         split<3>(y, of);
@@ -616,6 +617,7 @@ __global__ __launch_bounds__(Many<D>::kThreads, 2) void attend4_many_kernel(Atte
     typedef Many<D> M;
     typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
     typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+    typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
     constexpr bool PAIR = M::kPair;
     constexpr int QS = D / 16;                    // k-steps of a score
     constexpr int KB = D / kBlock;                // blocks of a token
@@ -659,12 +661,16 @@ __global__ __launch_bounds__(Many<D>::kThreads, 2) void attend4_many_kernel(Atte
         {
             const uint16_t* qp = static_cast<const uint16_t*>(a.q) + (static_cast<uint64_t>(r.first + max(w.row, 0)) * a.heads + w.head) * D + kBlock * half;
             const uint32_t flip = a.flip | a.flip >> 16;
+            u16x2 high = {0, 0};                 // largest magnitudes, as bits
 #pragma unroll
             for (int s = 0; s < QS; ++s) {
                 uint4 u = make_uint4(0, 0, 0, 0);
                 if (w.row >= 0) u = *reinterpret_cast<const uint4*>(qp + 2 * kBlock * (s / 4) + 8 * (s % 4));
+                for (const uint32_t v : {u.x, u.y, u.z, u.w}) high = __builtin_elementwise_max(high, __builtin_bit_cast(u16x2, v & 0x7FFF7FFFu));
                 qf[s] = __builtin_bit_cast(bf16x8, make_uint4((u.x & a.keep) ^ flip, (u.y & a.keep) ^ flip, (u.z & a.keep) ^ flip, (u.w & a.keep) ^ flip));
             }
+            // (an infinite query's products need not all be NaN, nor those of a scale of 0: one NaN makes them so)
+            if (max(high[0], high[1]) >= 0x7F80u) qf[0][0] = static_cast<__bf16>(__builtin_nanf(""));
         }
 
         // Lane i has the id of page at + i (-1: none).
