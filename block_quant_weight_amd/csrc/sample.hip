@@ -287,13 +287,14 @@ __device__ __forceinline__ uint64_t aim(float u, uint64_t total) {
     return min(static_cast<uint64_t>(floor(static_cast<double>(u) * static_cast<double>(total))), total - 1);
 }
 // ln of the token's weight over the total, a number of 2^-39 of the largest;
-// what the total has above the largest is exact.
+// what the total has above the largest is exact.  (ln 2 in two parts: float32's
+// is above it.)
 __device__ __forceinline__ void answer(const SampleArgs& a, uint64_t row, uint32_t index, float x, const Weigher& g, bool greedy, uint64_t total) {
     a.ids[row] = static_cast<int32_t>(index);
     if (a.lp == nullptr) return;
     const float2 t = g.log2_of(x);
     const float above = static_cast<float>(static_cast<int64_t>(total) - static_cast<int64_t>(kUnit)) * (1.f / kUnit);
-    a.lp[row] = greedy ? 0.f : fmaf(t.x, 0.6931471805599453f, fmaf(t.x, 1.9046542e-9f, t.y * 0.6931471805599453f)) - log1pf(fmaxf(above, 0.f));
+    a.lp[row] = greedy ? 0.f : fmaf(t.x, 0.6931471805599453f, fmaf(t.x, -1.9046542e-9f, t.y * 0.6931471805599453f)) - log1pf(fmaxf(above, 0.f));
 }
 __device__ __forceinline__ void no_answer(const SampleArgs& a, uint64_t row) {
     a.ids[row] = -1;

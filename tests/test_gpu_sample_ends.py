@@ -52,3 +52,27 @@ def test_tokens_that_weigh_nothing_are_not_drawn(vocab, t, below):
         want = float(x[i, ids[i]] - np.float64(top[i])) / float(np.float32(t)) - np.log(w.sum() * 2.0 ** -39)
         assert M.sample_ok([(ids[i], want)], ids[i], lp[i])
     assert np.array_equal(run(x, u, t=np.full(rows, t), m=np.full(rows, 1e-20))[0][:4], ids[:4])
+
+
+@pytest.mark.parametrize("vocab", [2, 20000])
+def test_log_probabilities_are_not_off_to_one_side(vocab):
+    """Log probabilities from -20 to -26, each rounded once to steps of 2^-19
+    (most in one binade), so by half a step at most, and the mean of n by about
+    0.29 / sqrt(n).  float32's ln 2 is 1.9e-9 above ln 2: where its low part is
+    left out the mean is 0.03 steps off, where it is added with the wrong sign
+    0.06 or 0.07."""
+    g = np.random.default_rng(vocab)
+    rows = 1 << 14 if vocab == 2 else 1 << 11
+    t = np.float32(0.7)                       # (with 1 the logits lie on the steps themselves)
+    d = g.uniform(14.0, 18.2, rows).astype(np.float32)
+    x = np.full((rows, vocab), -np.inf, dtype=np.float32)
+    x[:, 0], x[:, 1] = -d, 0.0
+    # (u = 0: the first token that weighs anything)
+    ids, lp = run(x, np.zeros(rows), t=np.full(rows, t))
+    assert np.all(ids == 0)
+    want = -d.astype(np.float64) / float(t)
+    want -= np.log1p(np.exp(want))
+    steps = (lp - want) * 2.0 ** 19
+    # (the total's part above the largest, below 2^-28, and the roundings of the low parts are 0.01 steps)
+    assert np.all(np.abs(steps) <= 0.51)
+    assert abs(steps.mean()) <= 0.01 + 4 * 0.29 / np.sqrt(rows)
