@@ -293,8 +293,10 @@ __device__ __forceinline__ void answer(const SampleArgs& a, uint64_t row, uint32
     a.ids[row] = static_cast<int32_t>(index);
     if (a.lp == nullptr) return;
     const float2 t = g.log2_of(x);
-    const float above = static_cast<float>(static_cast<int64_t>(total) - static_cast<int64_t>(kUnit)) * (1.f / kUnit);
-    a.lp[row] = greedy ? 0.f : fmaf(t.x, 0.6931471805599453f, fmaf(t.x, -1.9046542e-9f, t.y * 0.6931471805599453f)) - log1pf(fmaxf(above, 0.f));
+    // (up to 2^24 times the unit: past what a signed number holds)
+    constexpr uint64_t one = static_cast<uint64_t>(kUnit);
+    const float above = static_cast<float>(total > one ? total - one : 0) * (1.f / kUnit);
+    a.lp[row] = greedy ? 0.f : fmaf(t.x, 0.6931471805599453f, fmaf(t.x, -1.9046542e-9f, t.y * 0.6931471805599453f)) - log1pf(above);
 }
 __device__ __forceinline__ void no_answer(const SampleArgs& a, uint64_t row) {
     a.ids[row] = -1;

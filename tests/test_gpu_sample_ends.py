@@ -76,3 +76,17 @@ def test_log_probabilities_are_not_off_to_one_side(vocab):
     # (the total's part above the largest, below 2^-28, and the roundings of the low parts are 0.01 steps)
     assert np.all(np.abs(steps) <= 0.51)
     assert abs(steps.mean()) <= 0.01 + 4 * 0.29 / np.sqrt(rows)
+
+
+@pytest.mark.parametrize("vocab", [(1 << 24) - 1, 1 << 24])
+def test_the_largest_vocabulary_all_alike(vocab):
+    """Weights of the largest sum there is, 2^63 units; the first half of it with top_p."""
+    x = np.full((3, vocab), -2.5, dtype=np.float32)
+    u = np.array([0.0, 0.75, 1.0], dtype=np.float32)
+    ids, lp = run(x, u)
+    assert list(ids) == [0, int(0.75 * vocab), vocab - 1]
+    assert all(M.sample_ok([(i, -np.log(vocab))], i, l) for i, l in zip(ids, lp))
+    ids, lp = run(x, u, p=np.full(3, 0.5))
+    half = (vocab + 1) // 2
+    assert list(ids) == [0, int(0.75 * half), half - 1]
+    assert all(M.sample_ok([(i, -np.log(half))], i, l) for i, l in zip(ids, lp))
