@@ -141,7 +141,6 @@ struct Shared {
     uint64_t weight[kBins];
     uint32_t count[kBins];
     uint64_t sums[kWaves];
-    uint32_t bins[2];
     float maxes[kWaves];
     uint32_t found;
     uint64_t left;
