@@ -72,25 +72,6 @@ struct Attend4Args {
     uint32_t room;        // rows of pieces that the workspace holds
 };
 
-__device__ __forceinline__ float max_halves(float v) {
-    const uint32_t u = __builtin_bit_cast(uint32_t, v);
-    const auto a = __builtin_amdgcn_permlane32_swap(u, u, false, false);
-    const uint32_t x = a[0], y = a[1];
-    return fmaxf(__builtin_bit_cast(float, x), __builtin_bit_cast(float, y));
-}
-// Largest over the lanes 16, 32 and 48 apart.
-__device__ __forceinline__ float max_quads(float v) {
-    const uint32_t u = __builtin_bit_cast(uint32_t, v);
-    const auto a = __builtin_amdgcn_permlane16_swap(u, u, false, false);
-    const uint32_t x = a[0], y = a[1];
-    return max_halves(fmaxf(__builtin_bit_cast(float, x), __builtin_bit_cast(float, y)));
-}
-
-// First position that a row at position p sees.
-__device__ __forceinline__ int32_t sees_from(uint32_t window, int32_t p) {
-    return window == 0 || window > static_cast<uint32_t>(max(p, 0)) ? 0 : p - static_cast<int32_t>(window) + 1;
-}
-
 // Positions that a table has room for.
 __device__ __forceinline__ int32_t room_of(const qmv_kv_seqs& s) {
     return static_cast<int32_t>(min(s.table_stride, 0x7FFF0000u / kPage) * kPage);
@@ -1126,13 +1107,6 @@ __global__ __launch_bounds__(256) void attend4_join_kernel(Attend4Args a) {
             }
         }
     }
-}
-
-// Pages that a tile of columns may see, as far as the host knows.
-uint64_t span_pages(const qmv_kv_seqs& s, uint32_t window, uint64_t rows) {
-    uint64_t span = s.max_len;
-    if (window != 0 && span > uint64_t{window} + rows) span = uint64_t{window} + rows;
-    return (span + kPage - 1) / kPage + 1;
 }
 
 struct Plan {

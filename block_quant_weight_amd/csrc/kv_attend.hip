@@ -109,28 +109,6 @@ __device__ __forceinline__ float add_slots(float c, float w) {
     return v;
 }
 
-// Largest over the lanes 32 apart, and over those 16, 32 and 48 apart.  With
-// both operands alike, a swap leaves one half of the wave (one row of each
-// pair) in the first and the other in the second.  (The results go through
-// variables of their own: a bit cast of a vector's element takes element 0.)
-__device__ __forceinline__ float max_halves(float v) {
-    const uint32_t u = __builtin_bit_cast(uint32_t, v);
-    const auto a = __builtin_amdgcn_permlane32_swap(u, u, false, false);
-    const uint32_t x = a[0], y = a[1];
-    return fmaxf(__builtin_bit_cast(float, x), __builtin_bit_cast(float, y));
-}
-__device__ __forceinline__ float max_quads(float v) {
-    const uint32_t u = __builtin_bit_cast(uint32_t, v);
-    const auto a = __builtin_amdgcn_permlane16_swap(u, u, false, false);
-    const uint32_t x = a[0], y = a[1];
-    return max_halves(fmaxf(__builtin_bit_cast(float, x), __builtin_bit_cast(float, y)));
-}
-
-// First position that a row at position p sees.
-__device__ __forceinline__ int32_t sees_from(uint32_t window, int32_t p) {
-    return window == 0 || window > static_cast<uint32_t>(max(p, 0)) ? 0 : p - static_cast<int32_t>(window) + 1;
-}
-
 // What a workgroup's columns are.  Columns of a sequence and key/value head
 // (rows * group, below 2^31) are numbered row first.
 struct Columns {
@@ -1105,12 +1083,6 @@ struct Plan {
     uint32_t tiles, pieces, per;
     Few few;
 };
-// Pages that a tile of columns may see, as far as the host knows.
-uint64_t span_pages(const qmv_kv_seqs& s, uint32_t window, uint32_t cols) {
-    uint64_t span = s.max_len;
-    if (window != 0 && span > uint64_t{window} + cols) span = uint64_t{window} + cols;
-    return (span + kPage - 1) / kPage + 1;
-}
 // Each wave has its own columns where there are waves enough that way: tiles of
 // 16 columns for every SIMD (two for head dims of 64), or for few pages a tile
 // fewer, kSoloPage / D a page.  A wave then makes its queries' digits once, not

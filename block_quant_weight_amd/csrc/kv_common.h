@@ -1,5 +1,5 @@
 // What the cache's kernels share: which rows a sequence has, where a token
-// lives, and bfloat16 / float32 loads and stores.
+// lives, bfloat16 / float32 loads and stores, and what a row of queries sees.
 #pragma once
 #include "device_common.h"
 #include "serve_kernels.h"
@@ -70,6 +70,37 @@ __device__ __forceinline__ void store8(typename Elem<DT>::type* p, const float v
         for (int i = 0; i < 8; ++i) b[i] = static_cast<__bf16>(v[i]);
         *reinterpret_cast<bf16x8*>(p) = b;
     }
+}
+
+// ---- attention ------------------------------------------------------------
+
+// Largest over the lanes 32 apart, and over those 16, 32 and 48 apart.  With
+// both operands alike, a swap leaves one half of the wave (one row of each
+// pair) in the first and the other in the second.  (The results go through
+// variables of their own: a bit cast of a vector's element takes element 0.)
+__device__ __forceinline__ float max_halves(float v) {
+    const uint32_t u = __builtin_bit_cast(uint32_t, v);
+    const auto a = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    const uint32_t x = a[0], y = a[1];
+    return fmaxf(__builtin_bit_cast(float, x), __builtin_bit_cast(float, y));
+}
+__device__ __forceinline__ float max_quads(float v) {
+    const uint32_t u = __builtin_bit_cast(uint32_t, v);
+    const auto a = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+    const uint32_t x = a[0], y = a[1];
+    return max_halves(fmaxf(__builtin_bit_cast(float, x), __builtin_bit_cast(float, y)));
+}
+
+// First position that a row at position p sees.
+__device__ __forceinline__ int32_t sees_from(uint32_t window, int32_t p) {
+    return window == 0 || window > static_cast<uint32_t>(max(p, 0)) ? 0 : p - static_cast<int32_t>(window) + 1;
+}
+
+// Pages that a tile of columns may see, as far as the host knows.
+inline uint64_t span_pages(const qmv_kv_seqs& s, uint32_t window, uint64_t rows) {
+    uint64_t span = s.max_len;
+    if (window != 0 && span > uint64_t{window} + rows) span = uint64_t{window} + rows;
+    return (span + kPage - 1) / kPage + 1;
 }
 
 }  // namespace qmv
