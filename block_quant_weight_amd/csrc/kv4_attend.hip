@@ -8,7 +8,9 @@
 // bfloat16 matrix cores with float32 sums; the other operand is split so that
 // nothing that counts is rounded: float32 queries and probabilities into three
 // bfloat16 parts (24 bits, exact), bfloat16 queries are one part, and their
-// probabilities two (16 bits, where the output keeps 8).
+// probabilities two (16 bits, where the output keeps 8; cut off, while their sum
+// is of the whole ones: an output is up to 2^-16 of itself nearer to 0, 1/128 of
+// its rounding).
 //
 // Layout: v_mfma_f32_16x16x32_bf16 takes from lane l eight k-indexes of row (or
 // column) l % 16, those of group l / 16, and gives lane l, register i the
@@ -537,8 +539,11 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attend4_few_kernel(Atte
 // columns a wave, and walks the pages together.  Values are made float16 once
 // for all, in shared memory; keys stay codes there, which each wave turns into
 // bfloat16 on the way to its products: an operand read from shared memory feeds
-// one product of 32 columns, and were both of 2 bytes a value, these reads
-// would take as long as the products.
+// one product of 32 columns, and were both of 2 bytes a value, four waves' reads
+// of a page (head dims of 128: 128 KB, 128 bytes a cycle) would take as long as
+// their products at the matrix cores' full rate, 1024 cycles.  With keys as codes
+// they take 640; at the rate that is reached shared memory is addressed in 26% of
+// the cycles, and would be in 41%.
 //
 // v_mfma_f32_32x32x16 takes from lane l eight k-indexes of row (or column) l %
 // 32, those of half l / 32, and gives lane l, register i the output of row 8 (i
@@ -574,9 +579,11 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attend4_few_kernel(Atte
 // staged beside the last of them: one barrier a page.  Two workgroups share a
 // compute unit (216 of 256 registers), so one's barrier is the other's work.
 //
-// A prompt of 8192 (32 heads on 8 of 128, 550 GFLOP) takes 567 us, 970 TFLOP/s, 71%
-// of what a large bfloat16 product reaches: the exponentials and the conversion
-// of codes are vector instructions, which share the issue with the products.
+// A prompt of 8192 (32 heads on 8 of 128, 550 GFLOP) takes 561 to 576 us, 970
+// TFLOP/s, 70% of what a large bfloat16 product reaches.  Vector instructions (the
+// exponentials, and the codes' conversion, of keys in each wave) are issued in 58%
+// of the cycles and the matrix cores busy in 41%: little of one lies beside the
+// other, though nothing keeps them apart.
 // (Waves that read pages from memory themselves, few kernel: 874; eight waves and
 // three barriers: 721.)
 template <int D>

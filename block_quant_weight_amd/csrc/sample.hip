@@ -28,8 +28,9 @@
 // One row of 248320 takes 15.4 us (6 in a scan that finds the bound itself, 9 in the
 // last kernel: launches and trips to memory, and the fetching of its instructions),
 // 64 rows (64 MB)
-// 34.6 (scan 14 to 16, 4.5 TB/s; the last 14, a workgroup a row on 64 of 256
-// compute units); a row over the whole of which one workgroup goes about 0.4 ms.
+// 34.6 to 35.4 (scan 14 to 16, 4.5 TB/s; the last 14, a workgroup a row on 64 of
+// 256 compute units).  A row over the whole of which one workgroup goes 0.42 ms
+// for top-k, 0.70 for top-p (64 rows 0.8 and 1.2).
 #include "device_common.h"
 #include "serve_kernels.h"
 
@@ -441,6 +442,9 @@ __device__ __forceinline__ void find_bound(const SampleArgs& a, uint64_t row, ui
         uint32_t key[kEach];
 #pragma unroll
         for (int i = 0; i < kEach; ++i) key[i] = keys[64 * i + lane];
+        // (about as many tokens are listed.  Six times k, as a sample finds them, passes kList now and then from k
+        // = 800 or 1000 on, us of one row and of 64: k 500 21 and 41, 800 30 and 47, 1000 33, or as 2000, and 506,
+        // 2000 425 and 806)
         const uint64_t some = w.t == 0.f ? 1 : (w.k != 0 ? 6ull * w.k + 500 : 2500);
         const uint32_t least = w.t == 0.f ? 1 : 5;
         // (half of the fours at most: about 160 tokens of a wave's 1024, of which it can hand on 256)
