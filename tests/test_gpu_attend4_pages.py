@@ -7,7 +7,8 @@ import pytest
 import more_ref as M
 import serve_ref as R
 from block_quant_weight_amd import serve as S
-from test_gpu_attend4 import FAR, attend, near, starts
+from test_gpu_attend4 import FAR, attend, starts
+from test_gpu_attend4 import check as check_random
 from test_gpu_kv4 import put, seqs, to_gpu
 
 pytestmark = pytest.mark.gpu
@@ -157,3 +158,15 @@ def test_pages_far_apart(dim, exps, dtype):
             x[PAGE * p:PAGE * (p + 1)] *= np.float32(2.0 ** exps[p % len(exps)])
     check(g, k, v, [130, 60], 2, dtype)
     check(g, k, v, [130, 60], 2, dtype, window=40)
+
+
+@pytest.mark.parametrize("window", [1, 2, 50, 64, 200])
+@pytest.mark.parametrize("dim", DIMS)
+def test_kernel_for_many_under_a_window(dim, window):
+    """Edges of causality and window inside a page, groups that do not divide a
+    tile, more rows than tokens, in a call that looks large enough for that
+    kernel though a window leaves few pages."""
+    empty = [0] * SPARE_SEQS
+    for lens, news, heads, kv_heads in (([300, 40], [200, 40], 4, 2), ([400], [90], 5, 1), ([3, 70, 0], [80, 100, 9], 3, 1)):
+        check_random(lens + empty, news + empty, heads, kv_heads, dim, "bf16", seed=dim + window, window=window,
+                     spare=SPARE_ROWS, hints=(SPARE_ROWS, 1 << 20))
